@@ -371,6 +371,200 @@ ditango_status ditango_plan_noalloc(const ditango_geom *g, const float *cache_ls
                                     int32_t anchor, int8_t *plan, int32_t *fresh_list,
                                     int32_t *counts, float *score_out, ditango_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * A key/value history in 4 bits.  Where states cannot stand in for a history
+ * (the queries are new: the next chunk of a streamed video, text tokens), its
+ * keys and values are kept instead, in pages of DITANGO_PAGE tokens and 4 bits
+ * a value, for a batch of requests of any lengths.  Attention over it gives
+ * states (O, lse) like the rest of the library: written into a state buffer's
+ * slot (the strides allow it) they merge with the partitions' own.
+ *
+ * A page of one key head is DITANGO_PAGE * (d + 8) bytes: K codes, V codes
+ * (token-major, d/2 bytes a token, channel 2b in the low half of byte b), then
+ * for each token K's (scale, least) and for each token V's, all bf16.  A code
+ * c in 0..15 stands for c * scale + least.  least is the row's least value
+ * (exact: the rows are bf16) and scale the smallest bf16 value whose 15 steps
+ * reach its largest, so that every value is at most half a step off.
+ *
+ * Slots: token place page * DITANGO_PAGE + offset.  Tables: block_table int32
+ * [R][max_blocks] holds the pages of each request in order; entries behind a
+ * request's last page may hold anything.  Page numbers out of range are never
+ * followed: they count as pages without tokens, and DITANGO_ERR_BOUNDS is
+ * recorded in dev_status (in every build). */
+enum { DITANGO_PAGE = 64, DITANGO_QBLOCK = 128 };
+
+typedef struct {
+  int32_t n_pages, Hkv, d; /* pages, key heads, head dim in {64, 96, 128} */
+  uint8_t *data;           /* dev [n_pages][Hkv][DITANGO_PAGE * (d + 8)], 16-byte aligned */
+} ditango_kv4;
+
+/* Block tables, slot map and offsets of a batch, from request lengths (the
+ * device's counterpart of ditango_slot_table; nothing is read on the host).
+ * Request r holds ctx_len[r] tokens and receives new_len[r] more; its first
+ * ceil(ctx_len / 64) table entries are its pages.  The pages that it lacks are
+ * taken from free_pages in request order, and every new token's slot is
+ * written in request order.
+ *   R            requests, 1 <= R <= 4096 (else UNSUPPORTED).
+ *   ctx_len, new_len  dev int32 [R];  free_pages  dev int32 [n_free].
+ *   block_table  dev int32 [R][max_blocks], in and out: only new entries are
+ *                written.
+ *   kv_len       dev int32 [R] out: ctx_len + new_len.  Must not overlap the
+ *                inputs (INVALID), like every other output.
+ *   q_off        dev int32 [R + 1] out: running sum of new_len.
+ *   slot_map     dev int64 [max_tokens] out: slots of the new tokens; -1 from
+ *                q_off[R] on.
+ *   pages_used   dev int32 [1] out: entries of free_pages taken.
+ * A request that does not fit (a negative length, more than max_blocks pages,
+ * the free list or max_tokens exhausted) takes nothing: its kv_len stays
+ * ctx_len, its tokens' slots are -1, and DITANGO_ERR_BOUNDS is recorded. */
+ditango_status ditango_block_tables(int32_t R, int32_t max_blocks, int32_t max_tokens,
+                                    int32_t n_pages, const int32_t *ctx_len,
+                                    const int32_t *new_len, const int32_t *free_pages,
+                                    int32_t n_free, int32_t *block_table, int32_t *kv_len,
+                                    int32_t *q_off, int64_t *slot_map, int32_t *pages_used,
+                                    int32_t *dev_status, ditango_stream stream);
+
+/* Write T tokens into the slots slot_map dev int64 [T] (-1: the token is left
+ * out; slots out of range: left out and recorded; the slots of one call must
+ * differ, else what is stored there is undefined).  K, V dev bf16
+ * [T][Hkv][d] with (token, head) element strides, multiples of 8, and 16-byte
+ * aligned.  Codes are exactly round-to-nearest-even of (x - least) / scale.  A
+ * row that holds an infinity or a NaN is stored as NaN. */
+ditango_status ditango_kv4_write(const ditango_kv4 *c, int64_t T, const uint16_t *K,
+                                 const uint16_t *V, const int64_t k_strides[2],
+                                 const int64_t v_strides[2], const int64_t *slot_map,
+                                 int32_t *dev_status, ditango_stream stream);
+
+/* Read slots back as bf16 rows (each value c * scale + least rounded once);
+ * rows of slots -1 or out of range are left as they were.  The result can be
+ * the K and V of ditango_attn_partial or ditango_block_attn. */
+ditango_status ditango_kv4_read(const ditango_kv4 *c, int64_t T, uint16_t *K, uint16_t *V,
+                                const int64_t k_strides[2], const int64_t v_strides[2],
+                                const int64_t *slot_map, int32_t *dev_status,
+                                ditango_stream stream);
+
+/* Summaries of the pages that hold tokens [ctx_len[r], kv_len[r]) of the
+ * requests, for ditango_block_select: sum_codes dev int8 [n_pages][Hkv][d],
+ * sum_scale dev float32 [n_pages][Hkv], of the mean of all of the page's keys
+ * up to kv_len (see ditango_block_summary).  Call it after ditango_kv4_write. */
+ditango_status ditango_kv4_summary(const ditango_kv4 *c, int32_t R, int32_t max_blocks,
+                                   const int32_t *ctx_len, const int32_t *kv_len,
+                                   const int32_t *block_table, int8_t *sum_codes,
+                                   float *sum_scale, int32_t *dev_status,
+                                   ditango_stream stream);
+
+/* Bytes of device scratch of ditango_kv4_attn (0 for an unsupported d).  Zero
+ * it once when it is allocated: every launch leaves its counters at zero
+ * again.  Launches that may run at the same time (other streams, concurrent
+ * graph branches) must not share one. */
+size_t ditango_kv4_attn_workspace_size(int32_t d);
+
+/* Attention of the requests' new tokens over their histories.  Token t of
+ * request r (row q_off[r] + t of Q) attends the first kv_len[r] tokens of the
+ * request, with causal != 0 those before and at its own place, the new tokens
+ * being the last ones: kv_len - (n - 1 - t) tokens, n = q_off[r+1] - q_off[r].
+ * Query head h reads key head h / (H / Hkv).
+ *   T, max_q     rows of Q, and a bound on the new tokens of one request (it
+ *                chooses the kernel; a bound that is too small costs time only).
+ *   Q            dev bf16 [T][H][d], (token, head) element strides, multiples
+ *                of 8, 16-byte aligned.
+ *   q_off, kv_len, block_table   as ditango_block_tables leaves them.
+ *   sel, sel_count  dev int32 [R][Hkv][max_sel] and [R][Hkv], or NULL: only the
+ *                listed blocks (indices into the request's table row, distinct)
+ *                are attended, for all new tokens of the request alike.
+ *   scale        logit scale; 0 means 1/sqrt(d).
+ *   out          dev [T][H][d] bf16 or float32 (out_is_fp32), (token, head)
+ *                element strides out_strides, multiples of 4 (NULL: packed);
+ *                16-byte (bf16: 8-byte) aligned.  Must not be Q.
+ *   out_lse      dev float32 (token, head) strides lse_strides (NULL: [T][H]),
+ *                or NULL.
+ *   workspace    dev, ditango_kv4_attn_workspace_size bytes, 16-byte aligned.
+ * A row that sees no key gets O = 0, lse = -inf.  Rows behind q_off[R] are left
+ * as they were.  Keys that a row does not see never touch it, whatever they
+ * hold.  The result does not depend on the order in which blocks run. */
+ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int32_t T,
+                                int32_t max_q, int32_t max_blocks, const uint16_t *Q,
+                                const int64_t q_strides[2], const int32_t *q_off,
+                                const int32_t *kv_len, const int32_t *block_table,
+                                const int32_t *sel, const int32_t *sel_count, int32_t max_sel,
+                                float scale, int32_t causal, void *out, int32_t out_is_fp32,
+                                const int64_t *out_strides, float *out_lse,
+                                const int64_t *lse_strides, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_status,
+                                ditango_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over selected key blocks: the plan's idea (near units always, of
+ * the others the most important ones under a budget) at the grain of query
+ * blocks of DITANGO_QBLOCK rows and key blocks of DITANGO_PAGE rows, per head,
+ * with a score that needs no earlier step.
+ *
+ * Summaries of the blocks of x dev bf16 [B][H][N][d] ((b, h, n) element
+ * strides, multiples of 8; 16-byte aligned): of each block of `block` rows
+ * (DITANGO_PAGE or DITANGO_QBLOCK; the last one may be shorter) the sum S over
+ * its rows and, with top = max |S|,
+ *   codes int8 [B][H][nb][d] = rint(127 S / top), scale float32 [B][H][nb] =
+ *   top / (127 n), mean float32 [B][H][nb][d] (or NULL) = S / n.
+ *   len          dev int32 [B] valid rows, or NULL; blocks without a valid row,
+ *                and blocks whose sum is not finite, get codes 0 and scale 0. */
+ditango_status ditango_block_summary(int32_t B, int32_t H, int32_t N, int32_t d, int32_t block,
+                                     const uint16_t *x, const int64_t strides[3],
+                                     const int32_t *len, int8_t *codes, float *scale,
+                                     float *mean, ditango_stream stream);
+
+/* Selection.  Per (b, key head g, query block i) the score of key block j is
+ *   k_scale_j * sum over query heads h of g, ascending, of q_scale_h (q_h . k_j)
+ * in fp32, each operation rounded by itself (the dot product of codes is a
+ * whole number), -0 counting as 0 and NaN as the least.  Always taken: j <
+ * sink, and with band >= 0 the blocks within band of the query block's own
+ * (own_blocks * i ... own_blocks * i + own_blocks - 1; own_blocks = 0: the
+ * request's last block).  Then the best others until max(those, k) are taken
+ * or none is left, ties to the lower j.
+ *   q_codes int8 [B][H][n_q][d], q_scale float32 [B][H][n_q].
+ *   k_codes, k_scale  [B][Hkv][n_k][d] and [B][Hkv][n_k], or with block_table
+ *                (dev int32 [B][n_k]) the pages' [n_pages][Hkv][d] and
+ *                [n_pages][Hkv].
+ *   k_len        dev int32 [B] or NULL: only blocks that hold one of the first
+ *                k_len[b] tokens can be taken.
+ *   sel          dev int32 [B][Hkv][n_q][max_sel] out: ascending, then -1;
+ *   sel_count    dev int32 [B][Hkv][n_q] out.  max_sel must hold k and what is
+ *                always taken: max(k, sink + max(own_blocks, 1) + 2 band), else
+ *                INVALID.
+ * n_k <= 51200 (else UNSUPPORTED). */
+ditango_status ditango_block_select(int32_t B, int32_t H, int32_t Hkv, int32_t n_q, int32_t n_k,
+                                    int32_t d, int32_t k, int32_t band, int32_t sink,
+                                    int32_t own_blocks, int32_t max_sel, const int8_t *q_codes,
+                                    const float *q_scale, const int8_t *k_codes,
+                                    const float *k_scale, const int32_t *block_table,
+                                    int32_t n_pages, const int32_t *k_len, int32_t *sel,
+                                    int32_t *sel_count, int32_t *dev_status,
+                                    ditango_stream stream);
+
+/* Attention of every query block over its listed key blocks (tcgen05, TMA).
+ *   Q            dev bf16 [B][H][Nq][d]; K, V [B][Hkv][Nk][d]; (b, h, n) element
+ *                strides as in ditango_geom.  Query head h reads key head
+ *                h / (H / Hkv).
+ *   sel, sel_count  dev int32 [B][Hkv][ceil(Nq / DITANGO_QBLOCK)][max_sel] and
+ *                [B][Hkv][ceil(Nq / DITANGO_QBLOCK)]: distinct key blocks, in
+ *                any order.  Entries out of range count as empty and are
+ *                recorded as DITANGO_ERR_BOUNDS.
+ *   k_len        dev int32 [B] valid keys, or NULL; what lies behind them never
+ *                touches the result.
+ *   out          dev [B][H][Nq][d] bf16 or float32 (out_is_fp32), (b, h, n)
+ *                element strides, multiples of 16 bytes (NULL: packed).
+ *   out_lse      dev float32 [B][H][Nq] or NULL.
+ * bf16 products with fp32 accumulation and softmax; the probabilities are
+ * rounded to bf16 for the second product.  A query block without keys gets
+ * O = 0, lse = -inf. */
+ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk,
+                                  int32_t d, const uint16_t *Q, const uint16_t *K,
+                                  const uint16_t *V, const int64_t q_strides[3],
+                                  const int64_t k_strides[3], const int64_t v_strides[3],
+                                  const int32_t *sel, const int32_t *sel_count, int32_t max_sel,
+                                  const int32_t *k_len, float scale, void *out,
+                                  int32_t out_is_fp32, const int64_t *out_strides,
+                                  float *out_lse, int32_t *dev_status, ditango_stream stream);
+
 /* Time limit, in nanoseconds, of every wait inside the kernels (default
  * 1e9).  Process-wide; read at each launch. */
 void ditango_set_wait_limit_ns(int64_t ns);

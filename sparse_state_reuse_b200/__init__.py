@@ -11,6 +11,11 @@ into coarser groups without recomputation to shrink it.  An optional
 frame-tile mask keeps only some frame tiles (Efficient-vDiT: "Efficient Video
 Diffusion Transformers With Attention Tile").
 
+Beside the states, a history of keys and values can be kept in 4 bits
+(KV4Cache), and attention can be restricted, per head and block of queries, to
+the key blocks that a cheap score selects (BlockSparseAttention); both give
+states of the same kind.
+
 All compute runs in libditango.so (CUDA, sm_100a) through its C ABI
 (include/ditango.h); this package only marshals arguments.  PyTorch is used
 for device memory and streams.
@@ -24,7 +29,9 @@ from ._abi import (  # noqa: F401
     ditango_merge, ditango_cache_update, ditango_set_wait_limit_ns,
     ditango_selftest_bounded_wait, ditango_plan_noalloc, ditango_cache_compose, status_string,
     ditango_plan_error, error_state, ditango_plan_from_mass, ditango_checked_build,
-    ditango_check_status,
+    ditango_check_status, PAGE, QBLOCK, kv4, ditango_block_tables, ditango_kv4_write,
+    ditango_kv4_read, ditango_kv4_summary, ditango_kv4_attn, ditango_kv4_attn_workspace_size,
+    ditango_block_summary, ditango_block_select, ditango_block_attn,
 )
 
 
@@ -231,3 +238,314 @@ class ErrorPlanner:
         self.pa.partial(Q, K, V, scale, stream, drift_rows=self.drift_rows)
         self.pa.merge(out, out_lse, stream)
         self.step_index += 1
+
+
+def _launch_on(device):
+    """The device current for a launch: nothing to do when it already is."""
+    import contextlib
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
+
+
+class KV4Cache:
+    """A paged history of keys and values in 4 bits, and attention over it.
+
+    Holds the pages (data, uint8 [n_pages, Hkv, 64 * (d + 8)]), the tables of
+    up to max_requests requests of up to max_blocks pages each (block_table,
+    kv_len, q_off), the slots of up to max_tokens new tokens (slot_map) and the
+    page summaries (sum_codes, sum_scale).  A step of a batch is
+
+        cache.tables(ctx_len, new_len, free_pages)   # place the new tokens
+        cache.write(K, V)                            # K, V [T, Hkv, d] bf16
+        cache.summarize(ctx_len)                     # only if select() is used
+        sel, count = cache.select(Q, k)              # only for single tokens
+        cache.attend(Q, out, out_lse, ...)           # Q [T, H, d] bf16
+
+    Every length stays on the device; nothing synchronises, and the calls can
+    be captured into a CUDA graph.  status holds DITANGO_ERR_BOUNDS after a
+    request that did not fit or a page number out of range.  The buffers are
+    one batch's: calls that may overlap on the GPU need objects of their own.
+    data and block_table may be given (a cache that already exists).
+    """
+
+    def __init__(self, n_pages, Hkv, d, max_requests, max_blocks, max_tokens, H=None, device="cuda",
+                 data=None, block_table=None):
+        import torch
+        for name, v in (("n_pages", n_pages), ("Hkv", Hkv), ("max_requests", max_requests),
+                        ("max_blocks", max_blocks), ("max_tokens", max_tokens)):
+            if int(v) < 1:
+                raise ValueError(f"{name} must be >= 1")
+        if d not in (64, 96, 128):
+            raise ValueError(f"head dimension {d}: 64, 96 or 128 is required")
+        H = Hkv if H is None else H
+        if H < 1 or H % Hkv:
+            raise ValueError(f"{H} query heads are not a multiple of {Hkv} key heads")
+        dev = torch.device(device if data is None else data.device)
+        if dev.type != "cuda":
+            raise ValueError(f"the history lives on a CUDA device, not {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.n_pages, self.Hkv, self.H, self.d = n_pages, Hkv, H, d
+        self.max_requests, self.max_blocks, self.max_tokens = max_requests, max_blocks, max_tokens
+        self.n_requests = max_requests     # requests of the last tables() call
+        shape = (n_pages, Hkv, PAGE * (d + 8))
+        if data is None:
+            data = torch.zeros(shape, dtype=torch.uint8, device=dev)
+        else:
+            check_tensor(data, "data", shape, (torch.uint8,), contiguous=True)
+        self.data = data
+        shape = (max_requests, max_blocks)
+        if block_table is None:
+            block_table = torch.zeros(shape, dtype=torch.int32, device=dev)
+        else:
+            check_tensor(block_table, "block_table", shape, (torch.int32,), contiguous=True)
+            _same_device(dev, block_table=block_table)
+        self.block_table = block_table
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.kv_len = torch.zeros(max_requests, **i32)
+        self.q_off = torch.zeros(max_requests + 1, **i32)
+        self.slot_map = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
+        self.pages_used = torch.zeros(1, **i32)
+        self.status = torch.zeros(1, **i32)
+        self.sum_codes = torch.zeros((n_pages, Hkv, d), dtype=torch.int8, device=dev)
+        self.sum_scale = torch.zeros((n_pages, Hkv), dtype=torch.float32, device=dev)
+        # the attention's partial states and counters (each launch leaves the counters at zero)
+        self.workspace = torch.zeros(ditango_kv4_attn_workspace_size(d), dtype=torch.uint8, device=dev)
+        # the single tokens' 8-bit codes, for select()
+        self._q_codes = torch.empty((max_requests, H, d), dtype=torch.int8, device=dev)
+        self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
+        self._lists = {}
+        self.kv = kv4(n_pages, Hkv, d, self.data)
+
+    def _lengths(self, name, t, n=None):
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            raise TypeError(f"{name}: a one-dimensional tensor is required")
+        check_tensor(t, name, (t.shape[0] if n is None else n,), (torch.int32,), contiguous=True)
+        _same_device(self.device, **{name: t})
+
+    def tables(self, ctx_len, new_len, free_pages, stream=None):
+        """Tables of a batch: request r holds ctx_len[r] tokens and gets
+        new_len[r] more; missing pages come from free_pages, in order
+        (pages_used says how many were taken).  kv_len holds the new lengths:
+        pass a copy of it as the next step's ctx_len."""
+        self._lengths("ctx_len", ctx_len)
+        R = ctx_len.shape[0]
+        if not 1 <= R <= self.max_requests:
+            raise ValueError(f"{R} requests, the tables hold 1 to {self.max_requests}")
+        self._lengths("new_len", new_len, R)
+        self._lengths("free_pages", free_pages)
+        with _launch_on(self.device):
+            ditango_block_tables(R, self.max_blocks, self.max_tokens, self.n_pages, ctx_len, new_len,
+                                 free_pages if free_pages.shape[0] else None, free_pages.shape[0],
+                                 self.block_table, self.kv_len, self.q_off, self.slot_map,
+                                 self.pages_used, self.status, stream)
+        self.n_requests = R
+
+    def _rows(self, K, V, slots):
+        import torch
+        T = K.shape[0] if isinstance(K, torch.Tensor) and K.dim() == 3 else -1
+        for name, t in (("K", K), ("V", V)):
+            check_tensor(t, name, (T, self.Hkv, self.d), (torch.bfloat16,))
+        if slots is None:
+            if T > self.max_tokens:
+                raise ValueError(f"{T} tokens, the slot map holds {self.max_tokens}")
+            slots = self.slot_map
+        else:
+            check_tensor(slots, "slots", (T,), (torch.int64,), contiguous=True)
+        _same_device(self.device, K=K, V=V, slots=slots)
+        return T, slots, K.stride()[:2], V.stride()[:2]
+
+    def write(self, K, V, slots=None, stream=None):
+        """Quantise K, V [T, Hkv, d] into the slots (default: the slot map of
+        the last tables() call; -1 leaves a token out)."""
+        T, slots, ks, vs = self._rows(K, V, slots)
+        with _launch_on(self.device):
+            ditango_kv4_write(self.kv, T, K, V, ks, vs, slots, self.status, stream)
+
+    def read(self, slots, K, V, stream=None):
+        """Slots back as bf16 rows of K, V [T, Hkv, d] (rows of -1 are left alone)."""
+        T, slots, ks, vs = self._rows(K, V, slots)
+        with _launch_on(self.device):
+            ditango_kv4_read(self.kv, T, K, V, ks, vs, slots, self.status, stream)
+
+    def summarize(self, ctx_len, stream=None):
+        """Refresh the summaries of the pages that got tokens behind ctx_len[r]."""
+        self._lengths("ctx_len", ctx_len, self.n_requests)
+        with _launch_on(self.device):
+            ditango_kv4_summary(self.kv, self.n_requests, self.max_blocks, ctx_len, self.kv_len,
+                                self.block_table, self.sum_codes, self.sum_scale, self.status, stream)
+
+    def select(self, Q, k, band=0, sink=0, stream=None):
+        """(sel, count): the k best pages for one query token a request, Q
+        [n_requests, H, d]; the last band + 1 pages and the first sink pages
+        are always among them.  The lists are this object's: the next call of
+        the same sizes overwrites them."""
+        import torch
+        R, H, d = self.n_requests, self.H, self.d
+        check_tensor(Q, "Q", (R, H, d), (torch.bfloat16,))
+        _same_device(self.device, Q=Q)
+        if k < 0 or sink < 0 or band < -1:
+            raise ValueError("k and sink must be >= 0, band >= -1")
+        room = max(1, k, sink + (1 + 2 * band if band >= 0 else 0))
+        if (R, room) not in self._lists:
+            self._lists[R, room] = (
+                torch.empty((R, self.Hkv, room), dtype=torch.int32, device=self.device),
+                torch.empty((R, self.Hkv), dtype=torch.int32, device=self.device))
+        sel, count = self._lists[R, room]
+        s = Q.stride()
+        with _launch_on(self.device):
+            ditango_block_summary(R, H, 1, d, PAGE, Q, (s[0], s[1], d), self._q_codes, self._q_scale,
+                                  stream=stream)
+            ditango_block_select(R, H, self.Hkv, 1, self.max_blocks, d, k, band, sink, 0, room,
+                                 self._q_codes, self._q_scale, self.sum_codes, self.sum_scale, sel, count,
+                                 self.block_table, self.n_pages, self.kv_len, self.status, stream)
+        return sel, count
+
+    def attend(self, Q, out, out_lse=None, max_q=None, causal=False, scale=0.0, sel=None, sel_count=None,
+               stream=None):
+        """O and lse of the new tokens Q [T, H, d] over their requests' pages
+        (with sel, sel_count: over the listed pages).  out is bf16 or float32
+        [T, H, d], out_lse float32 [T, H]; both may be strided views, such as a
+        slot of a PartitionedAttention's state buffer.  max_q bounds the new
+        tokens of one request (default T)."""
+        import torch
+        T = Q.shape[0] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else -1
+        shape = (T, self.H, self.d)
+        check_tensor(Q, "Q", shape, (torch.bfloat16,))
+        check_tensor(out, "out", shape, (torch.bfloat16, torch.float32))
+        lse_strides = None
+        if out_lse is not None:
+            if not isinstance(out_lse, torch.Tensor) or out_lse.dtype != torch.float32:
+                raise TypeError("out_lse: a float32 tensor is required")
+            if tuple(out_lse.shape) != (T, self.H) or not out_lse.is_cuda:
+                raise ValueError(f"out_lse: a CUDA tensor of shape {(T, self.H)} is required")
+            lse_strides = out_lse.stride()
+        if (sel is None) != (sel_count is None):
+            raise ValueError("sel and sel_count go together")
+        room = 0
+        if sel is not None:
+            room = sel.shape[-1]
+            check_tensor(sel, "sel", (self.n_requests, self.Hkv, room), (torch.int32,), contiguous=True)
+            check_tensor(sel_count, "sel_count", (self.n_requests, self.Hkv), (torch.int32,),
+                         contiguous=True)
+        _same_device(self.device, Q=Q, out=out, out_lse=out_lse, sel=sel, sel_count=sel_count)
+        with _launch_on(self.device):
+            ditango_kv4_attn(self.kv, self.n_requests, self.H, T, T if max_q is None else max_q,
+                             self.max_blocks, Q, Q.stride()[:2], self.q_off, self.kv_len,
+                             self.block_table, out, out.dtype == torch.float32, self.workspace,
+                             self.workspace.numel(), out.stride()[:2], out_lse, lse_strides, sel,
+                             sel_count, room, scale, causal, self.status, stream)
+
+
+class BlockSparseAttention:
+    """Attention of 128-query blocks over the 64-key blocks each selects.
+
+    Q [B, H, Nq, d], K and V [B, Hkv, Nk, d], bf16 with any (b, h, n) strides.
+    The lists hold, per key head and query block, the blocks within band of the
+    query block's own ones (band = -1: none), the first sink blocks and the best
+    others by the scores of block means, k in all.  select() fills sel and
+    sel_count (and q_/k_ summaries, and k_mean, the means of the key blocks);
+    attend() takes those or any other lists; step() does both.  The buffers are
+    one call's: calls that may overlap on the GPU need objects of their own.
+    """
+
+    def __init__(self, B, H, Nq, Nk, d, k, band=0, sink=0, Hkv=None, device="cuda"):
+        import torch
+        Hkv = H if Hkv is None else Hkv
+        for name, v in (("B", B), ("H", H), ("Hkv", Hkv), ("Nq", Nq), ("Nk", Nk)):
+            if int(v) < 1:
+                raise ValueError(f"{name} must be >= 1")
+        if d not in (64, 96, 128):
+            raise ValueError(f"head dimension {d}: 64, 96 or 128 is required")
+        if H % Hkv:
+            raise ValueError(f"{H} query heads are not a multiple of {Hkv} key heads")
+        if k < 0 or sink < 0 or band < -1:
+            raise ValueError("k and sink must be >= 0, band >= -1")
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"the lists live on a CUDA device, not {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.B, self.H, self.Hkv, self.Nq, self.Nk, self.d = B, H, Hkv, Nq, Nk, d
+        self.k, self.band, self.sink = k, band, sink
+        self.n_q, self.n_k = -(-Nq // QBLOCK), -(-Nk // PAGE)
+        per = QBLOCK // PAGE
+        self.room = max(1, k, sink + (per + 2 * band if band >= 0 else 0))
+        f32, i32, i8 = (dict(dtype=t, device=dev) for t in (torch.float32, torch.int32, torch.int8))
+        self.q_codes = torch.empty((B, H, self.n_q, d), **i8)
+        self.q_scale = torch.empty((B, H, self.n_q), **f32)
+        self.k_codes = torch.empty((B, Hkv, self.n_k, d), **i8)
+        self.k_scale = torch.empty((B, Hkv, self.n_k), **f32)
+        self.k_mean = torch.empty((B, Hkv, self.n_k, d), **f32)
+        self.sel = torch.full((B, Hkv, self.n_q, self.room), -1, **i32)
+        self.sel_count = torch.zeros((B, Hkv, self.n_q), **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def _check_len(self, k_len):
+        import torch
+        if k_len is not None:
+            check_tensor(k_len, "k_len", (self.B,), (torch.int32,), contiguous=True)
+            _same_device(self.device, k_len=k_len)
+
+    def select(self, Q, K, k_len=None, stream=None):
+        """(sel, sel_count) for Q and K; k_len [B] int32 (device) bounds the
+        valid keys of each batch entry."""
+        import torch
+        B, H, Hkv, d = self.B, self.H, self.Hkv, self.d
+        check_tensor(Q, "Q", (B, H, self.Nq, d), (torch.bfloat16,))
+        check_tensor(K, "K", (B, Hkv, self.Nk, d), (torch.bfloat16,))
+        self._check_len(k_len)
+        _same_device(self.device, Q=Q, K=K)
+        with _launch_on(self.device):
+            ditango_block_summary(B, H, self.Nq, d, QBLOCK, Q, Q.stride()[:3], self.q_codes, self.q_scale,
+                                  stream=stream)
+            ditango_block_summary(B, Hkv, self.Nk, d, PAGE, K, K.stride()[:3], self.k_codes, self.k_scale,
+                                  self.k_mean, k_len, stream)
+            ditango_block_select(B, H, Hkv, self.n_q, self.n_k, d, self.k, self.band, self.sink,
+                                 QBLOCK // PAGE, self.room, self.q_codes, self.q_scale, self.k_codes,
+                                 self.k_scale, self.sel, self.sel_count, None, 0, k_len, self.status,
+                                 stream)
+        return self.sel, self.sel_count
+
+    def attend(self, Q, K, V, out, out_lse=None, sel=None, sel_count=None, k_len=None, scale=0.0,
+               stream=None):
+        """O (and lse [B, H, Nq]) of every query block over its listed key
+        blocks: the object's lists, or sel [B, Hkv, n_q, any] and sel_count."""
+        import torch
+        B, H, Hkv, Nq, d = self.B, self.H, self.Hkv, self.Nq, self.d
+        check_tensor(Q, "Q", (B, H, Nq, d), (torch.bfloat16,))
+        for name, t in (("K", K), ("V", V)):
+            check_tensor(t, name, (B, Hkv, self.Nk, d), (torch.bfloat16,))
+        check_tensor(out, "out", (B, H, Nq, d), (torch.bfloat16, torch.float32))
+        if out_lse is not None:
+            check_tensor(out_lse, "out_lse", (B, H, Nq), (torch.float32,), contiguous=True)
+        if (sel is None) != (sel_count is None):
+            raise ValueError("sel and sel_count go together")
+        if sel is None:
+            sel, sel_count = self.sel, self.sel_count
+        else:
+            check_tensor(sel, "sel", (B, Hkv, self.n_q, sel.shape[-1]), (torch.int32,), contiguous=True)
+            check_tensor(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), contiguous=True)
+        self._check_len(k_len)
+        _same_device(self.device, Q=Q, K=K, V=V, out=out, out_lse=out_lse, sel=sel, sel_count=sel_count)
+        with _launch_on(self.device):
+            ditango_block_attn(B, H, Hkv, Nq, self.Nk, d, Q, K, V, Q.stride()[:3], K.stride()[:3],
+                               V.stride()[:3], sel, sel_count, sel.shape[-1], out,
+                               out.dtype == torch.float32, out.stride()[:3], out_lse, k_len, scale,
+                               self.status, stream)
+
+    def step(self, Q, K, V, out, out_lse=None, k_len=None, scale=0.0, stream=None):
+        """select, then attend."""
+        self.select(Q, K, k_len, stream)
+        self.attend(Q, K, V, out, out_lse, k_len=k_len, scale=scale, stream=stream)

@@ -48,6 +48,13 @@ class ditango_error_state(C.Structure):
     ]
 
 
+class ditango_kv4(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("Hkv", C.c_int32), ("d", C.c_int32), ("data", C.c_void_p)]
+
+
+PAGE, QBLOCK = 64, 128   # DITANGO_PAGE, DITANGO_QBLOCK
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -59,6 +66,7 @@ def _load():
 _lib = _load()
 _P = C.c_void_p
 _G = C.POINTER(ditango_geom)
+_KV = C.POINTER(ditango_kv4)
 _SIGS = {
     "ditango_version": (C.c_int32, []),
     "ditango_status_string": (C.c_char_p, [C.c_int32]),
@@ -83,6 +91,19 @@ _SIGS = {
     "ditango_plan_noalloc": (C.c_int, [_G, _P, _P, C.c_int32, C.c_double, C.c_int32, _P, _P, _P,
                                        _P, _P]),
     "ditango_cache_compose": (C.c_int, [_G, _G, _P, _P, _P, _P, _P, _P, C.c_int32, _P]),
+    "ditango_block_tables": (C.c_int, [C.c_int32, C.c_int32, C.c_int32, C.c_int32, _P, _P, _P,
+                                       C.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+    "ditango_kv4_write": (C.c_int, [_KV, C.c_int64, _P, _P, _P, _P, _P, _P, _P]),
+    "ditango_kv4_read": (C.c_int, [_KV, C.c_int64, _P, _P, _P, _P, _P, _P, _P]),
+    "ditango_kv4_summary": (C.c_int, [_KV, C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+    "ditango_kv4_attn_workspace_size": (C.c_size_t, [C.c_int32]),
+    "ditango_kv4_attn": (C.c_int, [_KV, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _P, _P,
+                                   _P, _P, _P, _P, _P, C.c_int32, C.c_float, C.c_int32, _P, C.c_int32,
+                                   _P, _P, _P, _P, C.c_size_t, _P, _P]),
+    "ditango_block_summary": (C.c_int, [C.c_int32] * 5 + [_P] * 7),
+    "ditango_block_select": (C.c_int, [C.c_int32] * 11 + [_P] * 5 + [C.c_int32] + [_P] * 5),
+    "ditango_block_attn": (C.c_int, [C.c_int32] * 6 + [_P] * 8 + [C.c_int32, _P, C.c_float, _P,
+                                     C.c_int32, _P, _P, _P, _P]),
     "ditango_set_wait_limit_ns": (None, [C.c_int64]),
     "ditango_checked_build": (C.c_int32, []),
     "ditango_check_status": (C.c_int, [_P, C.c_int32]),
@@ -297,3 +318,88 @@ def ditango_plan_noalloc(geom, cache_lse, cache_valid, band_k, budget, anchor, p
     _check("ditango_plan_noalloc", _lib.ditango_plan_noalloc(
         geom.ref, _ptr(cache_lse), _ptr(cache_valid), int(band_k), float(budget), int(bool(anchor)),
         _ptr(plan), _ptr(fresh_list), _ptr(counts), _ptr(score_out), _stream(stream)))
+
+
+def _i64s(v):
+    """A host int64 array of strides (None stays None)."""
+    return None if v is None else (C.c_int64 * len(v))(*v)
+
+
+def kv4(n_pages, Hkv, d, data):
+    """A ditango_kv4 over the page buffer (tensor or address)."""
+    return ditango_kv4(int(n_pages), int(Hkv), int(d), _ptr(data))
+
+
+def ditango_block_tables(R, max_blocks, max_tokens, n_pages, ctx_len, new_len, free_pages, n_free,
+                         block_table, kv_len, q_off, slot_map, pages_used, dev_status=None, stream=None):
+    """Block table, slot map and offsets of a batch from its request lengths."""
+    _check("ditango_block_tables", _lib.ditango_block_tables(
+        R, max_blocks, max_tokens, n_pages, _ptr(ctx_len), _ptr(new_len), _ptr(free_pages), n_free,
+        _ptr(block_table), _ptr(kv_len), _ptr(q_off), _ptr(slot_map), _ptr(pages_used), _ptr(dev_status),
+        _stream(stream)))
+
+
+def ditango_kv4_write(kv, T, K, V, k_strides, v_strides, slot_map, dev_status=None, stream=None):
+    """Quantise T tokens' keys and values into their slots."""
+    _check("ditango_kv4_write", _lib.ditango_kv4_write(
+        C.byref(kv), T, _ptr(K), _ptr(V), _i64s(k_strides), _i64s(v_strides), _ptr(slot_map),
+        _ptr(dev_status), _stream(stream)))
+
+
+def ditango_kv4_read(kv, T, K, V, k_strides, v_strides, slot_map, dev_status=None, stream=None):
+    """Slots back as bf16 rows."""
+    _check("ditango_kv4_read", _lib.ditango_kv4_read(
+        C.byref(kv), T, _ptr(K), _ptr(V), _i64s(k_strides), _i64s(v_strides), _ptr(slot_map),
+        _ptr(dev_status), _stream(stream)))
+
+
+def ditango_kv4_summary(kv, R, max_blocks, ctx_len, kv_len, block_table, sum_codes, sum_scale,
+                        dev_status=None, stream=None):
+    """Summaries of the pages that hold the tokens [ctx_len, kv_len) of the requests."""
+    _check("ditango_kv4_summary", _lib.ditango_kv4_summary(
+        C.byref(kv), R, max_blocks, _ptr(ctx_len), _ptr(kv_len), _ptr(block_table), _ptr(sum_codes),
+        _ptr(sum_scale), _ptr(dev_status), _stream(stream)))
+
+
+def ditango_kv4_attn_workspace_size(d) -> int:
+    return _lib.ditango_kv4_attn_workspace_size(int(d))
+
+
+def ditango_kv4_attn(kv, R, H, T, max_q, max_blocks, Q, q_strides, q_off, kv_len, block_table, out,
+                     out_is_fp32, workspace, workspace_bytes, out_strides=None, out_lse=None,
+                     lse_strides=None, sel=None, sel_count=None, max_sel=0, scale=0.0, causal=0,
+                     dev_status=None, stream=None):
+    """Attention of the requests' new tokens over their paged histories."""
+    _check("ditango_kv4_attn", _lib.ditango_kv4_attn(
+        C.byref(kv), R, H, T, max_q, max_blocks, _ptr(Q), _i64s(q_strides), _ptr(q_off), _ptr(kv_len),
+        _ptr(block_table), _ptr(sel), _ptr(sel_count), max_sel, scale, int(bool(causal)), _ptr(out),
+        int(bool(out_is_fp32)), _i64s(out_strides), _ptr(out_lse), _i64s(lse_strides), _ptr(workspace),
+        workspace_bytes, _ptr(dev_status), _stream(stream)))
+
+
+def ditango_block_summary(B, H, N, d, block, x, strides, codes, scale, mean=None, length=None,
+                          stream=None):
+    """8-bit summaries of the blocks of `block` rows of x."""
+    _check("ditango_block_summary", _lib.ditango_block_summary(
+        B, H, N, d, block, _ptr(x), _i64s(strides), _ptr(length), _ptr(codes), _ptr(scale), _ptr(mean),
+        _stream(stream)))
+
+
+def ditango_block_select(B, H, Hkv, n_q, n_k, d, k, band, sink, own_blocks, max_sel, q_codes, q_scale,
+                         k_codes, k_scale, sel, sel_count, block_table=None, n_pages=0, k_len=None,
+                         dev_status=None, stream=None):
+    """The key blocks that each query block attends."""
+    _check("ditango_block_select", _lib.ditango_block_select(
+        B, H, Hkv, n_q, n_k, d, k, band, sink, own_blocks, max_sel, _ptr(q_codes), _ptr(q_scale),
+        _ptr(k_codes), _ptr(k_scale), _ptr(block_table), n_pages, _ptr(k_len), _ptr(sel),
+        _ptr(sel_count), _ptr(dev_status), _stream(stream)))
+
+
+def ditango_block_attn(B, H, Hkv, Nq, Nk, d, Q, K, V, q_strides, k_strides, v_strides, sel, sel_count,
+                       max_sel, out, out_is_fp32, out_strides=None, out_lse=None, k_len=None, scale=0.0,
+                       dev_status=None, stream=None):
+    """Attention of every query block over its listed key blocks."""
+    _check("ditango_block_attn", _lib.ditango_block_attn(
+        B, H, Hkv, Nq, Nk, d, _ptr(Q), _ptr(K), _ptr(V), _i64s(q_strides), _i64s(k_strides),
+        _i64s(v_strides), _ptr(sel), _ptr(sel_count), max_sel, _ptr(k_len), scale, _ptr(out),
+        int(bool(out_is_fp32)), _i64s(out_strides), _ptr(out_lse), _ptr(dev_status), _stream(stream)))

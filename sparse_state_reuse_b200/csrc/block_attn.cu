@@ -1,0 +1,497 @@
+// Attention of 128-query blocks over the 64-key blocks that each selected.
+//
+// For query block i of (b, h) and the list sel[b][h / G][i]: S = Q K^T scale
+// over the keys of the listed blocks, O = softmax(S) V, lse = log sum exp(S),
+// by an online softmax over tiles of two listed blocks (128 keys).  Q, K and V
+// are staged by TMA, a listed block as one 64-row box, so that a list costs the
+// tile nothing; both products run on tcgen05 with S, P and O in TMEM.
+//
+// One block of threads takes one query block, and two of them share an SM
+// (256 TMEM columns and at most 113 KB each): while one exponentiates its
+// scores the other's products have the tensor pipe, which is what a second
+// query tile in one block would do, but neither waits for the other, and one's
+// start and end run under the other's loop.  Query blocks have lists of their
+// own, so there are no key tiles to share between them.
+//   warps 0-3  softmax, a thread a row, and the epilogue
+//   warp  4    TMEM owner, MMA issuer (one thread)
+//   warp  5    TMA producer
+// TMEM: S [0, 128), O [128, 128 + d); the bf16 P overwrites the first 64
+// columns of S and feeds the second product from there.
+// Bound: 4 * 128 * 128 * d flops a tile against the exponentials of 128 * 128
+// scores, and 2 * 128 * d * 2 bytes of L2 reads a tile.
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "blocks.cuh"
+
+namespace ditango {
+namespace battn {
+
+constexpr int BM = kQBlock;          // query rows
+constexpr int BN = 2 * kPage;        // keys of a tile
+constexpr int kThreads = 256;
+constexpr int kLaunchRegs = 128;     // 65536 / (2 * 256)
+// A softmax thread holds a row of 128 scores.  The two shares are what the
+// block is launched with: 128 * 200 + 128 * 56 = 256 * 128.
+constexpr int kSoftmaxRegs = 200, kControlRegs = 56;
+static_assert(128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kTmemCols = 256;
+
+template <int D>
+struct Cfg {
+  static constexpr int NCH = (D + 63) / 64;          // 64-column chunks
+  static constexpr int CHUNK = 128 * 128;            // 128 rows of 128 bytes
+  static constexpr int HALF = CHUNK / 2;             // one key block of a chunk
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int OFF_Q = 0, OFF_K = TILE, OFF_V = 2 * TILE, OFF_BAR = 3 * TILE;
+  static constexpr int USED = OFF_BAR + 128;
+  // above 76 KB, so that no third block comes to the SM (its TMEM columns are taken)
+  static constexpr int SMEM = (USED + 1024 > 100 * 1024) ? USED + 1024 : 100 * 1024;
+  static_assert(SMEM <= 113 * 1024, "two blocks an SM");
+  static_assert(TILE >= 4 * 4096, "the epilogue stages rows in the Q tile");
+};
+
+struct Params {
+  int H, G, Hkv, Nq, Nk, n_q, n_k, room;
+  const int *sel, *count, *k_len;
+  float scale_log2;
+  void *out;
+  int out_fp32;
+  long long osb, osh, osn;
+  float *out_lse;                    // [B, H, Nq] or null
+  int *dev_status;
+  long long wait_limit_ns;
+};
+
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The list of one query block.
+struct List {
+  const int *sel;
+  int n, n_k, keys;
+  // valid keys of entry e: 0 for entries past the end or out of range
+  __device__ __forceinline__ int at(int e, int &block) const {
+    block = e < n ? __ldg(sel + e) : -1;
+    if (block < 0 || block >= n_k) return 0;
+    return max(0, min(kPage, keys - block * kPage));
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + C::OFF_Q, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
+  const uint32_t bar = sbase + C::OFF_BAR;
+  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 16, v_full = bar + 24, v_empty = bar + 32,
+                 s_full = bar + 40, p_full = bar + 48, o_full = bar + 56;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 64);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 68);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
+  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, hk = h / p.G;
+
+  List list;
+  {
+    const size_t at = ((size_t)b * p.Hkv + hk) * p.n_q + i;
+    const int n = __ldg(p.count + at);
+    list.n = max(0, min(n, p.room));
+    list.sel = p.sel + at * p.room;
+    list.n_k = p.n_k;
+    list.keys = p.Nk;
+    if (p.k_len) list.keys = max(0, min(p.Nk, __ldg(p.k_len + b)));
+    if (threadIdx.x == 0 && n != list.n) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+  }
+  const int T = (list.n + 1) / 2;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);      // one arrival per softmax warp
+    mbar_init(o_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 5 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 5 && T > 0) {
+      // ---------------------------------------------------------- producer
+      const bool leader = elect_one();
+      bool ok = true;
+      int armed = 0;           // tiles of K armed; V the same or one fewer
+      int v_armed = 0;
+      if (leader) {
+        mbar_arrive_expect_tx(q_full, C::TILE);
+        for (int c = 0; c < C::NCH; ++c)
+          tma_load_4d(sQ + c * C::CHUNK, &tmQ, q_full, c * 64, i * BM, h, b);
+      }
+      int b0, b1;
+      int n0 = list.at(0, b0), n1 = list.at(1, b1);
+      for (int t = 0; t < T && ok; ++t) {
+        // the next entries are read under this tile's waits
+        int c0, c1;
+        const int m0 = list.at(2 * t + 2, c0), m1 = list.at(2 * t + 3, c1);
+        if (lane == 0 && ((b0 < 0 || b0 >= p.n_k) || (2 * t + 1 < list.n && (b1 < 0 || b1 >= p.n_k))))
+          set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+        const uint32_t bytes = ((n0 > 0) + (n1 > 0)) * C::NCH * C::HALF;
+        if (!(ok = wait_warp(k_empty, (t & 1) ^ 1, ctl))) break;
+        if (leader) {
+          mbar_arrive_expect_tx(k_full, bytes);
+          for (int c = 0; c < C::NCH; ++c) {
+            if (n0 > 0) tma_load_4d(sK + c * C::CHUNK, &tmK, k_full, c * 64, b0 * kPage, hk, b);
+            if (n1 > 0) tma_load_4d(sK + c * C::CHUNK + C::HALF, &tmK, k_full, c * 64, b1 * kPage, hk, b);
+          }
+        }
+        ++armed;
+        if (!(ok = wait_warp(v_empty, (t & 1) ^ 1, ctl))) break;
+        if (leader) {
+          mbar_arrive_expect_tx(v_full, bytes);
+          for (int c = 0; c < C::NCH; ++c) {
+            if (n0 > 0) tma_load_4d(sV + c * C::CHUNK, &tmV, v_full, c * 64, b0 * kPage, hk, b);
+            if (n1 > 0) tma_load_4d(sV + c * C::CHUNK + C::HALF, &tmV, v_full, c * 64, b1 * kPage, hk, b);
+          }
+        }
+        ++v_armed;
+        b0 = c0;
+        b1 = c1;
+        n0 = m0;
+        n1 = m1;
+      }
+      // every load issued lands before the warp exits, on both paths
+      volatile int never = 0;
+      WaitCtl drain{&never, nullptr, 100000000LL};
+      wait_bounded(q_full, 0, drain);
+      if (armed > 0) wait_bounded(k_full, (armed - 1) & 1, drain);
+      if (v_armed > 0) wait_bounded(v_full, (v_armed - 1) & 1, drain);
+    } else if (warp == 4 && T > 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(BM, BN, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t dK = smem_desc_sw128(sK, 16, 1024);
+      const uint64_t dV = smem_desc_sw128(sV, C::CHUNK, 1024);   // MN-major: chunks of d are CHUNK apart
+      bool ok = wait_warp(q_full, 0, ctl);
+      for (int t = 0; t < T && ok; ++t) {
+        if (!(ok = wait_warp(k_full, t & 1, ctl))) break;
+        tc_fence_after();
+        if (leader) {
+          // S = Q K^T.  P of the tile before lives in S: its product was
+          // issued before, and one thread's products run in order.
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
+            mma_ss(tmem, dQ + off, dK + off, idesc_qk, kk > 0);
+          }
+          tc_commit(s_full);
+          tc_commit(k_empty);
+        }
+        if (!(ok = wait_warp(v_full, t & 1, ctl))) break;
+        if (!(ok = wait_warp(p_full, t & 1, ctl))) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + 128, tmem + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, t > 0 || kk > 0);
+          tc_commit(v_empty);
+          if (t + 1 == T) tc_commit(o_full);
+        }
+      }
+      // what was issued ends before TMEM is released, on both paths
+      volatile int never = 0;
+      WaitCtl drain{&never, nullptr, 100000000LL};
+      if (!ok && leader) tc_commit(o_full);
+      wait_bounded(o_full, 0, drain);
+      __syncwarp();
+    }
+    if (warp == 4) {
+      named_bar_sync(1, kThreads);
+      tc_fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+    } else {
+      tc_fence_before();
+      named_bar_arrive(1, kThreads);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- softmax
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  const int r = threadIdx.x;                    // row of the block = TMEM lane
+  const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16);
+  const uint32_t tO = tS + 128;
+  const float sl2 = p.scale_log2;
+  float m_used = -INFINITY, l = 0.f;
+  bool ok = true;
+  for (int t = 0; t < T; ++t) {
+    int b0, b1;
+    const int n0 = list.at(2 * t, b0), n1 = list.at(2 * t + 1, b1);
+    if (!(ok = wait_bounded(s_full, t & 1, ctl))) break;
+    tc_fence_after();
+    uint32_t sv[BN];
+#pragma unroll
+    for (int c = 0; c < BN / 16; ++c) tmem_ld16p(tS + c * 16, &sv[c * 16]);
+    tc_wait_ld();
+    const bool partial = n0 + n1 < BN;
+    if (partial) {
+#pragma unroll
+      for (int c = 0; c < BN; ++c)
+        if (c < kPage ? c >= n0 : c - kPage >= n1) sv[c] = __float_as_uint(-INFINITY);
+    }
+    float m8[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      m8[q] = max3(__uint_as_float(sv[q]), __uint_as_float(sv[q + 8]), __uint_as_float(sv[q + 16]));
+#pragma unroll
+    for (int c = 24; c + 16 <= BN; c += 16)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        m8[q] = max3(m8[q], __uint_as_float(sv[c + q]), __uint_as_float(sv[c + q + 8]));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) m8[q] = fmaxf(m8[q], __uint_as_float(sv[BN - 8 + q]));
+    const float mx2 =
+        max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * sl2;
+    if (t == 0) {
+      m_used = mx2;
+    } else {
+      // S of this tile is complete, and with it every product issued before:
+      // O may be rescaled (only when a maximum grew by more than 2^8)
+      const bool need = mx2 > m_used + kRescaleLog2;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = need ? mx2 : m_used;
+        const float alpha = need ? fast_ex2(m_used - m_new) : 1.f;
+        l *= alpha;
+        m_used = m_new;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tO + c * 32, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+          tmem_st32(tO + c * 32, v);
+        }
+      }
+    }
+    const float neg = m_used > -INFINITY ? -m_used : 0.f;   // no key so far: exponentiate against 0
+    const uint64_t sl2x2 = f2(sl2, sl2), negx2 = f2(neg, neg);
+    uint64_t lsum0 = 0, lsum1 = 0;
+#pragma unroll
+    for (int g8 = 0; g8 < BN / 16; ++g8) {
+      uint32_t pk[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = g8 * 16 + 2 * e;
+        float xa, xb;
+        unf2(fma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, negx2), xa, xb);
+        const float a = fast_ex2(xa), bb = fast_ex2(xb);
+        if (e & 1) lsum1 = add2(lsum1, f2(a, bb)); else lsum0 = add2(lsum0, f2(a, bb));
+        pk[e] = pack_bf16x2(a, bb);
+      }
+      tmem_st8(tS + g8 * 8, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+    }
+    {
+      float s0, s1, s2, s3;
+      unf2(lsum0, s0, s1);
+      unf2(lsum1, s2, s3);
+      l += (s0 + s1) + (s2 + s3);
+    }
+    if (partial) {
+      // V rows of masked keys: their probabilities are 0, but the row (past
+      // the valid length, or left from another tile) may hold anything
+      if (!(ok = wait_bounded(v_full, t & 1, ctl))) break;
+      if (r < kPage ? r >= n0 : r - kPage >= n1) {
+#pragma unroll
+        for (int c = 0; c < C::NCH; ++c)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4 *>(smem + C::OFF_V + c * C::CHUNK + r * 128 + q * 16) =
+                make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+    }
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(p_full);
+  }
+  if (ok && T > 0) ok = wait_bounded(o_full, 0, ctl);
+  if (ok) {
+    tc_fence_after();
+    // every product is done: the Q tile is free to stage rows, 4 KB a warp
+    const float inv_l = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    float4 *epi = reinterpret_cast<float4 *>(smem + C::OFF_Q + warp * 4096);
+    const int rows = min(BM, p.Nq - i * BM) - (r & ~31);   // rows of this warp
+    const long long base = b * p.osb + h * p.osh + (long long)(i * BM + (r & ~31)) * p.osn;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t ov[32];
+      if (T > 0) {
+        tmem_ld32(tO + c * 32, ov);
+        tc_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = 0u;
+      }
+      if (!(l > 0.f) && l == l) {      // no key: 0, whatever the masked product left
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = 0u;
+      }
+      if (p.out_fp32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float4 o;
+          o.x = __uint_as_float(ov[4 * q + 0]) * inv_l;
+          o.y = __uint_as_float(ov[4 * q + 1]) * inv_l;
+          o.z = __uint_as_float(ov[4 * q + 2]) * inv_l;
+          o.w = __uint_as_float(ov[4 * q + 3]) * inv_l;
+          epi[lane * 8 + (q ^ (lane & 7))] = o;
+        }
+        __syncwarp();
+        float *dst = static_cast<float *>(p.out) + base + c * 32;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int row = (lane >> 3) + 4 * q, seg = lane & 7;
+          if (row < rows)
+            reinterpret_cast<float4 *>(dst + row * p.osn)[seg] = epi[row * 8 + (seg ^ (row & 7))];
+        }
+      } else {
+        uint4 *ep = reinterpret_cast<uint4 *>(epi);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 u;
+          u.x = pack_bf16x2(__uint_as_float(ov[8 * q + 0]) * inv_l, __uint_as_float(ov[8 * q + 1]) * inv_l);
+          u.y = pack_bf16x2(__uint_as_float(ov[8 * q + 2]) * inv_l, __uint_as_float(ov[8 * q + 3]) * inv_l);
+          u.z = pack_bf16x2(__uint_as_float(ov[8 * q + 4]) * inv_l, __uint_as_float(ov[8 * q + 5]) * inv_l);
+          u.w = pack_bf16x2(__uint_as_float(ov[8 * q + 6]) * inv_l, __uint_as_float(ov[8 * q + 7]) * inv_l);
+          ep[lane * 4 + (q ^ ((lane >> 1) & 3))] = u;
+        }
+        __syncwarp();
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + base + c * 32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = (lane >> 2) + 8 * q, seg = lane & 3;
+          if (row < rows)
+            reinterpret_cast<uint4 *>(dst + row * p.osn)[seg] = ep[row * 4 + (seg ^ ((row >> 1) & 3))];
+        }
+      }
+      __syncwarp();
+    }
+    if (p.out_lse && (r & 31) < rows)
+      p.out_lse[((size_t)b * p.H + h) * p.Nq + i * BM + r] =
+          l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
+  }
+  tc_fence_before();
+  named_bar_arrive(1, kThreads);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int B,
+                   cudaStream_t stream) {
+  auto kfn = block_attn_kernel<D>;
+  static std::mutex mu;
+  static std::set<int> ready;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready.count(dev)) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kfn);
+      if (e != cudaSuccess) return e;
+      // another count would leave setmaxnreg waiting for registers that do not come
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+      if (e != cudaSuccess) return e;
+      ready.insert(dev);
+    }
+  }
+  const dim3 grid((unsigned)p.n_q, (unsigned)p.H, (unsigned)B);
+  kfn<<<grid, kThreads, Cfg<D>::SMEM, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace battn
+
+cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B, int H,
+                              int Hkv, int Nq, int Nk, int d, const int *sel, const int *count, int room,
+                              const int *k_len, float scale, void *out, int out_fp32, const long long *os,
+                              float *out_lse, int *dev_status, long long wait_limit_ns, cudaStream_t stream) {
+  battn::Params p;
+  p.H = H;
+  p.G = H / Hkv;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.n_q = (Nq + kQBlock - 1) / kQBlock;
+  p.n_k = (Nk + kPage - 1) / kPage;
+  p.room = room;
+  p.sel = sel;
+  p.count = count;
+  p.k_len = k_len;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out;
+  p.out_fp32 = out_fp32;
+  p.osb = os[0];
+  p.osh = os[1];
+  p.osn = os[2];
+  p.out_lse = out_lse;
+  p.dev_status = dev_status;
+  p.wait_limit_ns = wait_limit_ns;
+  switch (d) {
+    case 64: return battn::launch<64>(tq, tk, tv, p, B, stream);
+    case 96: return battn::launch<96>(tq, tk, tv, p, B, stream);
+    case 128: return battn::launch<128>(tq, tk, tv, p, B, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace ditango

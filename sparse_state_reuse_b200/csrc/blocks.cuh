@@ -1,0 +1,60 @@
+// Shared pieces of the paged 4-bit history and of the selected-block
+// operators: the page format, and small device helpers.
+//
+// A page holds kPage tokens of one key head, K and V, as 64 * (d + 8) bytes:
+//   [0, 32 d)            K codes, token-major, d/2 bytes a token; channel 2b in
+//                        the low half of byte b, channel 2b + 1 in the high one
+//   [32 d, 64 d)         V codes
+//   [64 d, 64 d + 256)   K (scale, least), two bf16 a token
+//   [64 d + 256, ...)    V (scale, least)
+// A code c stands for c * scale + least.  One page of one head is one
+// contiguous run, so that a kernel fetches it with one bulk copy.
+#pragma once
+
+#include "common.cuh"
+
+namespace ditango {
+
+constexpr int kPage = DITANGO_PAGE;       // tokens of a page = keys of a key block
+constexpr int kQBlock = DITANGO_QBLOCK;   // queries of a query block
+
+__host__ __device__ constexpr int page_bytes(int d) { return kPage * (d + 8); }
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ void set_status(int *dev_status, int code) {
+  if (dev_status) atomicExch(dev_status, code);
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+__device__ __forceinline__ float fast_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Order this thread's earlier shared-memory accesses before later accesses
+// by the asynchronous proxy (bulk copies, tensor core operands).
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ditango

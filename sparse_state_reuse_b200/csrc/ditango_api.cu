@@ -40,6 +40,39 @@ cudaError_t launch_cache_compose(const DevGeom &fine, const DevGeom &coarse, con
                                  int state_bf16, cudaStream_t stream);
 cudaError_t launch_bounded_wait_selftest(long long limit_ns, int *dev_status,
                                          cudaStream_t stream);
+cudaError_t launch_block_tables(int R, int max_blocks, int max_tokens, int n_pages, const int *ctx_len,
+                                const int *new_len, const int *free_pages, int n_free, int *block_table,
+                                int *kv_len, int *q_off, long long *slot_map, int *pages_used,
+                                int *dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_rows(bool write, long long T, int Hkv, int d, int n_pages, const uint16_t *K,
+                            const uint16_t *V, uint16_t *Ko, uint16_t *Vo, const int64_t *k_strides,
+                            const int64_t *v_strides, const long long *slots, uint8_t *data,
+                            int *dev_status, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_summary(int R, int Hkv, int d, int max_blocks, int n_pages, const int *ctx_len,
+                               const int *kv_len, const int *block_table, const uint8_t *data,
+                               signed char *codes, float *scale, int *dev_status, cudaStream_t stream);
+size_t kv4_attn_workspace_bytes(int d);
+cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int max_blocks, int n_pages,
+                            const uint16_t *Q, const int64_t *q_strides, const int *q_off,
+                            const int *kv_len, const int *block_table, const uint8_t *data,
+                            const int *sel, const int *sel_count, int max_sel, float scale, int causal,
+                            void *out, int out_fp32, const int64_t *out_strides, float *out_lse,
+                            const int64_t *lse_strides, void *workspace, int *dev_status,
+                            long long wait_limit_ns, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_summary(int B, int H, int N, int d, int block, const uint16_t *x,
+                                 const int64_t *s, const int *len, signed char *codes, float *scale,
+                                 float *mean, cudaStream_t stream);
+int select_max_blocks();
+cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, int k, int band, int sink,
+                                int room, int own, const signed char *qc, const float *qs,
+                                const signed char *kc, const float *ks, const int *block_table,
+                                int n_pages, const int *k_len, int *sel_out, int *count,
+                                int *dev_status, cudaStream_t stream);
+cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B,
+                              int H, int Hkv, int Nq, int Nk, int d, const int *sel, const int *count,
+                              int room, const int *k_len, float scale, void *out, int out_fp32,
+                              const long long *os, float *out_lse, int *dev_status,
+                              long long wait_limit_ns, cudaStream_t stream);
 cudaError_t attn_check_status(int *out, bool reset);
 cudaError_t merge_check_status(int *out, bool reset);
 }  // namespace ditango
@@ -249,7 +282,7 @@ ditango_status cuda_status(cudaError_t e) {
 
 extern "C" {
 
-int32_t ditango_version(void) { return 10200; }
+int32_t ditango_version(void) { return 10300; }
 
 const char *ditango_status_string(int32_t s) {
   switch (s) {
@@ -631,3 +664,260 @@ extern "C" ditango_status ditango_plan_noalloc(const ditango_geom *g, const floa
                                  score_out, scratch, static_cast<cudaStream_t>(stream), nullptr,
                                  nullptr, nullptr, nullptr, nullptr, 0, 0));
 }
+
+// ---------------------------------------------------------------------------
+// The 4-bit history and the selected-block operators
+namespace {
+
+constexpr int kMaxRequests = 4096;                        // shared memory of the tables kernel
+constexpr int kMaxTableBlocks = 0x7fffffff / DITANGO_PAGE;  // token places of a request fit 31 bits
+
+bool dim_ok(int d) { return d == 64 || d == 96 || d == 128; }
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
+ditango_status check_kv4(const ditango_kv4 *c) {
+  if (!c || !c->data || c->n_pages < 1 || c->Hkv < 1 || c->d < 1 || !aligned16(c->data))
+    return DITANGO_ERR_INVALID;
+  if (!dim_ok(c->d) || c->Hkv > 65535) return DITANGO_ERR_UNSUPPORTED;
+  return DITANGO_OK;
+}
+
+// (token, head) strides in elements; the stride of a dimension of size 1 is
+// not used and gets the packed value.
+bool row_strides(const int64_t *s, long long T, int H, int d, int multiple, int64_t out[2]) {
+  out[0] = s ? s[0] : (int64_t)H * d;
+  out[1] = s ? s[1] : d;
+  if (H == 1) out[1] = d;
+  if (T == 1) out[0] = (int64_t)H * (out[1] > 0 ? out[1] : d);
+  for (int k = 0; k < 2; ++k)
+    if (out[k] <= 0 || out[k] % multiple || out[k] >= (1LL << 40)) return false;
+  return true;
+}
+
+ditango_status kv4_rows(bool write, const ditango_kv4 *c, int64_t T, const uint16_t *K, const uint16_t *V,
+                        uint16_t *Ko, uint16_t *Vo, const int64_t *ks, const int64_t *vs,
+                        const int64_t *slots, int32_t *dev_status, ditango_stream stream) {
+  const ditango_status st = check_kv4(c);
+  if (st != DITANGO_OK) return st;
+  const void *k = write ? (const void *)K : (const void *)Ko, *v = write ? (const void *)V : (const void *)Vo;
+  if (T < 0 || !ks || !vs) return DITANGO_ERR_INVALID;
+  if (T == 0) return DITANGO_OK;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return DITANGO_ERR_INVALID;
+  if (T >= (1LL << 40) / c->Hkv) return DITANGO_ERR_UNSUPPORTED;
+  int64_t kst[2], vst[2];
+  if (!row_strides(ks, T, c->Hkv, c->d, 8, kst) || !row_strides(vs, T, c->Hkv, c->d, 8, vst))
+    return DITANGO_ERR_INVALID;
+  return cuda_status(launch_kv4_rows(write, T, c->Hkv, c->d, c->n_pages, K, V, Ko, Vo, kst, vst,
+                                     reinterpret_cast<const long long *>(slots), c->data, dev_status,
+                                     num_sms_current(), static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+ditango_status ditango_block_tables(int32_t R, int32_t max_blocks, int32_t max_tokens, int32_t n_pages,
+                                    const int32_t *ctx_len, const int32_t *new_len,
+                                    const int32_t *free_pages, int32_t n_free, int32_t *block_table,
+                                    int32_t *kv_len, int32_t *q_off, int64_t *slot_map,
+                                    int32_t *pages_used, int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_block_tables");
+  if (R < 1 || max_blocks < 1 || max_tokens < 1 || n_pages < 1 || n_free < 0) return DITANGO_ERR_INVALID;
+  if (!ctx_len || !new_len || (n_free > 0 && !free_pages) || !block_table || !kv_len || !q_off ||
+      !slot_map || !pages_used)
+    return DITANGO_ERR_INVALID;
+  if (R > kMaxRequests || max_blocks > kMaxTableBlocks) return DITANGO_ERR_UNSUPPORTED;
+  // the blocks read every input while others already write: no output may
+  // lie on an input or on another output
+  struct Span { const void *p; size_t n; };
+  const size_t r4 = (size_t)R * 4;
+  const Span in[3] = {{ctx_len, r4}, {new_len, r4}, {free_pages, (size_t)n_free * 4}};
+  const Span out[5] = {{block_table, r4 * max_blocks}, {kv_len, r4}, {q_off, r4 + 4},
+                       {slot_map, (size_t)max_tokens * 8}, {pages_used, 4}};
+  for (int a = 0; a < 5; ++a) {
+    for (const Span &s : in)
+      if (overlap(out[a].p, out[a].n, s.p, s.n)) return DITANGO_ERR_INVALID;
+    for (int b = 0; b < a; ++b)
+      if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return DITANGO_ERR_INVALID;
+  }
+  return cuda_status(launch_block_tables(R, max_blocks, max_tokens, n_pages, ctx_len, new_len, free_pages,
+                                         n_free, block_table, kv_len, q_off,
+                                         reinterpret_cast<long long *>(slot_map), pages_used, dev_status,
+                                         num_sms_current(), static_cast<cudaStream_t>(stream)));
+}
+
+ditango_status ditango_kv4_write(const ditango_kv4 *c, int64_t T, const uint16_t *K, const uint16_t *V,
+                                 const int64_t k_strides[2], const int64_t v_strides[2],
+                                 const int64_t *slot_map, int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_kv4_write");
+  return kv4_rows(true, c, T, K, V, nullptr, nullptr, k_strides, v_strides, slot_map, dev_status, stream);
+}
+
+ditango_status ditango_kv4_read(const ditango_kv4 *c, int64_t T, uint16_t *K, uint16_t *V,
+                                const int64_t k_strides[2], const int64_t v_strides[2],
+                                const int64_t *slot_map, int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_kv4_read");
+  return kv4_rows(false, c, T, nullptr, nullptr, K, V, k_strides, v_strides, slot_map, dev_status, stream);
+}
+
+ditango_status ditango_kv4_summary(const ditango_kv4 *c, int32_t R, int32_t max_blocks,
+                                   const int32_t *ctx_len, const int32_t *kv_len,
+                                   const int32_t *block_table, int8_t *sum_codes, float *sum_scale,
+                                   int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_kv4_summary");
+  const ditango_status st = check_kv4(c);
+  if (st != DITANGO_OK) return st;
+  if (R < 1 || max_blocks < 1 || !ctx_len || !kv_len || !block_table || !sum_codes || !sum_scale)
+    return DITANGO_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(sum_codes) & 7u) return DITANGO_ERR_INVALID;
+  if (R > kMaxRequests || max_blocks > kMaxTableBlocks) return DITANGO_ERR_UNSUPPORTED;
+  return cuda_status(launch_kv4_summary(R, c->Hkv, c->d, max_blocks, c->n_pages, ctx_len, kv_len,
+                                        block_table, c->data, reinterpret_cast<signed char *>(sum_codes),
+                                        sum_scale, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ditango_kv4_attn_workspace_size(int32_t d) { return dim_ok(d) ? kv4_attn_workspace_bytes(d) : 0; }
+
+ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int32_t T, int32_t max_q,
+                                int32_t max_blocks, const uint16_t *Q, const int64_t q_strides[2],
+                                const int32_t *q_off, const int32_t *kv_len, const int32_t *block_table,
+                                const int32_t *sel, const int32_t *sel_count, int32_t max_sel, float scale,
+                                int32_t causal, void *out, int32_t out_is_fp32, const int64_t *out_strides,
+                                float *out_lse, const int64_t *lse_strides, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_kv4_attn");
+  const ditango_status st = check_kv4(c);
+  if (st != DITANGO_OK) return st;
+  if (R < 1 || H < 1 || H % c->Hkv || T < 0 || max_q < 1 || max_blocks < 1) return DITANGO_ERR_INVALID;
+  if (!q_strides || !q_off || !kv_len || !block_table) return DITANGO_ERR_INVALID;
+  if ((sel == nullptr) != (sel_count == nullptr) || (sel && max_sel < 1)) return DITANGO_ERR_INVALID;
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return DITANGO_ERR_INVALID;
+  if (R > kMaxRequests || max_blocks > kMaxTableBlocks || H > 65535) return DITANGO_ERR_UNSUPPORTED;
+  if (T == 0) return DITANGO_OK;
+  if (!Q || !out || Q == out || !workspace || !aligned16(Q) || !aligned16(workspace))
+    return DITANGO_ERR_INVALID;
+  if (workspace_bytes < kv4_attn_workspace_bytes(c->d)) return DITANGO_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(out) % (out_is_fp32 ? 16 : 8)) return DITANGO_ERR_INVALID;
+  int64_t qs[2], os[2], ls[2] = {H, 1};
+  if (!row_strides(q_strides, T, H, c->d, 8, qs) || !row_strides(out_strides, T, H, c->d, 4, os))
+    return DITANGO_ERR_INVALID;
+  if (lse_strides) {
+    ls[0] = lse_strides[0];
+    ls[1] = lse_strides[1];
+    if ((T > 1 && ls[0] <= 0) || (H > 1 && ls[1] <= 0)) return DITANGO_ERR_INVALID;
+  }
+  if (scale == 0.f) scale = 1.f / std::sqrt((float)c->d);
+  return cuda_status(launch_kv4_attn(R, H, c->Hkv, c->d, T, max_q, max_blocks, c->n_pages, Q, qs, q_off,
+                                     kv_len, block_table, c->data, sel, sel_count, max_sel, scale,
+                                     causal ? 1 : 0, out, out_is_fp32 ? 1 : 0, os, out_lse, ls, workspace,
+                                     dev_status, g_wait_limit_ns.load(), num_sms_current(),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+ditango_status ditango_block_summary(int32_t B, int32_t H, int32_t N, int32_t d, int32_t block,
+                                     const uint16_t *x, const int64_t strides[3], const int32_t *len,
+                                     int8_t *codes, float *scale, float *mean, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_block_summary");
+  if (B < 1 || H < 1 || N < 1 || d < 1 || !x || !strides || !codes || !scale || !aligned16(x))
+    return DITANGO_ERR_INVALID;
+  if (block != DITANGO_PAGE && block != DITANGO_QBLOCK) return DITANGO_ERR_INVALID;
+  if (!dim_ok(d) || B > 65535 || H > 65535) return DITANGO_ERR_UNSUPPORTED;
+  int64_t s[3] = {strides[0], strides[1], strides[2]};
+  if (N == 1) s[2] = d;
+  if (H == 1) s[1] = s[2] * N;
+  if (B == 1) s[0] = s[1] * H;
+  if (!strides_ok(s)) return DITANGO_ERR_INVALID;
+  return cuda_status(launch_block_summary(B, H, N, d, block, x, s, len, reinterpret_cast<signed char *>(codes),
+                                          scale, mean, static_cast<cudaStream_t>(stream)));
+}
+
+ditango_status ditango_block_select(int32_t B, int32_t H, int32_t Hkv, int32_t n_q, int32_t n_k, int32_t d,
+                                    int32_t k, int32_t band, int32_t sink, int32_t own_blocks,
+                                    int32_t max_sel, const int8_t *q_codes, const float *q_scale,
+                                    const int8_t *k_codes, const float *k_scale, const int32_t *block_table,
+                                    int32_t n_pages, const int32_t *k_len, int32_t *sel,
+                                    int32_t *sel_count, int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_block_select");
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || n_q < 1 || n_k < 1 || d < 1) return DITANGO_ERR_INVALID;
+  if (k < 0 || sink < 0 || band < -1 || own_blocks < 0 || max_sel < 1) return DITANGO_ERR_INVALID;
+  if (!q_codes || !q_scale || !k_codes || !k_scale || !sel || !sel_count) return DITANGO_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(q_codes) & 7u) || (reinterpret_cast<uintptr_t>(k_codes) & 7u))
+    return DITANGO_ERR_INVALID;
+  if (block_table && n_pages < 1) return DITANGO_ERR_INVALID;
+  const long long near = band < 0 ? 0 : (own_blocks > 0 ? own_blocks : 1) + 2LL * band;
+  long long must = sink + near;
+  if (must < k) must = k;
+  if (must > n_k) must = n_k;
+  if (max_sel < must) return DITANGO_ERR_INVALID;
+  if (!dim_ok(d) || B > 65535 || Hkv > 65535 || n_k > select_max_blocks()) return DITANGO_ERR_UNSUPPORTED;
+  // indices of the forced band fit 31 bits
+  if (band > (1 << 24) || own_blocks > 1024 || (long long)n_q * own_blocks > (1 << 30))
+    return DITANGO_ERR_UNSUPPORTED;
+  return cuda_status(launch_block_select(B, H, Hkv, n_q, n_k, d, k, band, sink, max_sel, own_blocks,
+                                         reinterpret_cast<const signed char *>(q_codes), q_scale,
+                                         reinterpret_cast<const signed char *>(k_codes), k_scale, block_table,
+                                         n_pages, k_len, sel, sel_count, dev_status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk, int32_t d,
+                                  const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                  const int64_t q_strides[3], const int64_t k_strides[3],
+                                  const int64_t v_strides[3], const int32_t *sel, const int32_t *sel_count,
+                                  int32_t max_sel, const int32_t *k_len, float scale, void *out,
+                                  int32_t out_is_fp32, const int64_t *out_strides, float *out_lse,
+                                  int32_t *dev_status, ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_block_attn");
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || Nq < 1 || Nk < 1 || d < 1 || max_sel < 1)
+    return DITANGO_ERR_INVALID;
+  if (!Q || !K || !V || !q_strides || !k_strides || !v_strides || !sel || !sel_count || !out)
+    return DITANGO_ERR_INVALID;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(out)) return DITANGO_ERR_INVALID;
+  if (out == Q || out == K || out == V) return DITANGO_ERR_INVALID;
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return DITANGO_ERR_INVALID;
+  if (!dim_ok(d) || B > 65535 || H > 65535) return DITANGO_ERR_UNSUPPORTED;
+  DevGeom gq, gk;
+  std::memset(&gq, 0, sizeof(gq));
+  gq.B = B;
+  gq.H = H;
+  gq.N = Nq;
+  gq.d = d;
+  gk = gq;
+  gk.H = Hkv;
+  gk.N = Nk;
+  int64_t qs[3], ks[3], vs[3];
+  long long os[3] = {(long long)H * Nq * d, (long long)Nq * d, d};
+  for (int a = 0; a < 3; ++a) {
+    qs[a] = q_strides[a];
+    ks[a] = k_strides[a];
+    vs[a] = v_strides[a];
+    if (out_strides) os[a] = out_strides[a];
+  }
+  auto pack = [&](auto *s, int heads, int n) {
+    if (n == 1) s[2] = d;
+    if (heads == 1) s[1] = s[2] * n;
+    if (B == 1) s[0] = s[1] * heads;
+  };
+  pack(qs, H, Nq);
+  pack(ks, Hkv, Nk);
+  pack(vs, Hkv, Nk);
+  pack(os, H, Nq);
+  if (!strides_ok(qs) || !strides_ok(ks) || !strides_ok(vs)) return DITANGO_ERR_INVALID;
+  const int esz = out_is_fp32 ? 4 : 2;
+  for (int a = 0; a < 3; ++a)
+    if (os[a] <= 0 || (os[a] * esz) % 16) return DITANGO_ERR_INVALID;
+  if (scale == 0.f) scale = 1.f / std::sqrt((float)d);
+  CUtensorMap tq, tk, tv;
+  if (!make_qkv_map(&tq, Q, gq, qs, DITANGO_QBLOCK) || !make_qkv_map(&tk, K, gk, ks, DITANGO_PAGE) ||
+      !make_qkv_map(&tv, V, gk, vs, DITANGO_PAGE))
+    return DITANGO_ERR_CUDA;
+  return cuda_status(launch_block_attn(tq, tk, tv, B, H, Hkv, Nq, Nk, d, sel, sel_count, max_sel, k_len,
+                                       scale, out, out_is_fp32 ? 1 : 0, os, out_lse, dev_status,
+                                       g_wait_limit_ns.load(), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
