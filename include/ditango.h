@@ -429,7 +429,8 @@ ditango_status ditango_block_tables(int32_t R, int32_t max_blocks, int32_t max_t
  * differ, else what is stored there is undefined).  K, V dev bf16
  * [T][Hkv][d] with (token, head) element strides, multiples of 8, and 16-byte
  * aligned.  Codes are exactly round-to-nearest-even of (x - least) / scale.  A
- * row that holds an infinity or a NaN is stored as NaN. */
+ * row that holds an infinity or a NaN is stored as NaN.  T * Hkv < 2^27 (else
+ * UNSUPPORTED), here and in ditango_kv4_read. */
 ditango_status ditango_kv4_write(const ditango_kv4 *c, int64_t T, const uint16_t *K,
                                  const uint16_t *V, const int64_t k_strides[2],
                                  const int64_t v_strides[2], const int64_t *slot_map,

@@ -242,17 +242,35 @@ class ErrorPlanner:
 
 def _launch_on(device):
     """The device current for a launch: nothing to do when it already is."""
-    import contextlib
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if device.index == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(device)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _need(t, name, shape, dtypes, device, contiguous=False):
+    """check_tensor, and the device the buffers are on.  One pass over the
+    properties in the common case (these calls take a few microseconds on the
+    device); what is wrong is found and said by check_tensor."""
+    try:
+        if (t.dtype in dtypes and t.shape == shape and t.device == device
+                and (t.is_contiguous() or not contiguous and (shape[-1] == 1 or t.stride(-1) == 1))):
+            return
+    except AttributeError:
+        pass
+    check_tensor(t, name, shape, dtypes, contiguous)
+    raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
 
 
 class KV4Cache:
@@ -307,8 +325,7 @@ class KV4Cache:
         if block_table is None:
             block_table = torch.zeros(shape, dtype=torch.int32, device=dev)
         else:
-            check_tensor(block_table, "block_table", shape, (torch.int32,), contiguous=True)
-            _same_device(dev, block_table=block_table)
+            _need(block_table, "block_table", shape, (torch.int32,), dev, contiguous=True)
         self.block_table = block_table
         i32 = dict(dtype=torch.int32, device=dev)
         self.kv_len = torch.zeros(max_requests, **i32)
@@ -319,7 +336,8 @@ class KV4Cache:
         self.sum_codes = torch.zeros((n_pages, Hkv, d), dtype=torch.int8, device=dev)
         self.sum_scale = torch.zeros((n_pages, Hkv), dtype=torch.float32, device=dev)
         # the attention's partial states and counters (each launch leaves the counters at zero)
-        self.workspace = torch.zeros(ditango_kv4_attn_workspace_size(d), dtype=torch.uint8, device=dev)
+        self.ws_bytes = ditango_kv4_attn_workspace_size(d)
+        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         # the single tokens' 8-bit codes, for select()
         self._q_codes = torch.empty((max_requests, H, d), dtype=torch.int8, device=dev)
         self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
@@ -330,8 +348,7 @@ class KV4Cache:
         import torch
         if not isinstance(t, torch.Tensor) or t.dim() != 1:
             raise TypeError(f"{name}: a one-dimensional tensor is required")
-        check_tensor(t, name, (t.shape[0] if n is None else n,), (torch.int32,), contiguous=True)
-        _same_device(self.device, **{name: t})
+        _need(t, name, t.shape if n is None else (n,), (torch.int32,), self.device, contiguous=True)
 
     def tables(self, ctx_len, new_len, free_pages, stream=None):
         """Tables of a batch: request r holds ctx_len[r] tokens and gets
@@ -354,15 +371,15 @@ class KV4Cache:
     def _rows(self, K, V, slots):
         import torch
         T = K.shape[0] if isinstance(K, torch.Tensor) and K.dim() == 3 else -1
-        for name, t in (("K", K), ("V", V)):
-            check_tensor(t, name, (T, self.Hkv, self.d), (torch.bfloat16,))
+        shape, dev = (T, self.Hkv, self.d), self.device
+        _need(K, "K", shape, (torch.bfloat16,), dev)
+        _need(V, "V", shape, (torch.bfloat16,), dev)
         if slots is None:
             if T > self.max_tokens:
                 raise ValueError(f"{T} tokens, the slot map holds {self.max_tokens}")
             slots = self.slot_map
         else:
-            check_tensor(slots, "slots", (T,), (torch.int64,), contiguous=True)
-        _same_device(self.device, K=K, V=V, slots=slots)
+            _need(slots, "slots", (T,), (torch.int64,), dev, contiguous=True)
         return T, slots, K.stride()[:2], V.stride()[:2]
 
     def write(self, K, V, slots=None, stream=None):
@@ -392,8 +409,7 @@ class KV4Cache:
         the same sizes overwrites them."""
         import torch
         R, H, d = self.n_requests, self.H, self.d
-        check_tensor(Q, "Q", (R, H, d), (torch.bfloat16,))
-        _same_device(self.device, Q=Q)
+        _need(Q, "Q", (R, H, d), (torch.bfloat16,), self.device)
         if k < 0 or sink < 0 or band < -1:
             raise ValueError("k and sink must be >= 0, band >= -1")
         room = max(1, k, sink + (1 + 2 * band if band >= 0 else 0))
@@ -421,29 +437,28 @@ class KV4Cache:
         import torch
         T = Q.shape[0] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else -1
         shape = (T, self.H, self.d)
-        check_tensor(Q, "Q", shape, (torch.bfloat16,))
-        check_tensor(out, "out", shape, (torch.bfloat16, torch.float32))
+        dev = self.device
+        _need(Q, "Q", shape, (torch.bfloat16,), dev)
+        _need(out, "out", shape, (torch.bfloat16, torch.float32), dev)
         lse_strides = None
         if out_lse is not None:
             if not isinstance(out_lse, torch.Tensor) or out_lse.dtype != torch.float32:
                 raise TypeError("out_lse: a float32 tensor is required")
-            if tuple(out_lse.shape) != (T, self.H) or not out_lse.is_cuda:
-                raise ValueError(f"out_lse: a CUDA tensor of shape {(T, self.H)} is required")
+            if out_lse.shape != (T, self.H) or out_lse.device != dev:
+                raise ValueError(f"out_lse: a tensor of shape {(T, self.H)} on {dev} is required")
             lse_strides = out_lse.stride()
         if (sel is None) != (sel_count is None):
             raise ValueError("sel and sel_count go together")
         room = 0
         if sel is not None:
             room = sel.shape[-1]
-            check_tensor(sel, "sel", (self.n_requests, self.Hkv, room), (torch.int32,), contiguous=True)
-            check_tensor(sel_count, "sel_count", (self.n_requests, self.Hkv), (torch.int32,),
-                         contiguous=True)
-        _same_device(self.device, Q=Q, out=out, out_lse=out_lse, sel=sel, sel_count=sel_count)
+            _need(sel, "sel", (self.n_requests, self.Hkv, room), (torch.int32,), dev, contiguous=True)
+            _need(sel_count, "sel_count", (self.n_requests, self.Hkv), (torch.int32,), dev, contiguous=True)
         with _launch_on(self.device):
             ditango_kv4_attn(self.kv, self.n_requests, self.H, T, T if max_q is None else max_q,
                              self.max_blocks, Q, Q.stride()[:2], self.q_off, self.kv_len,
                              self.block_table, out, out.dtype == torch.float32, self.workspace,
-                             self.workspace.numel(), out.stride()[:2], out_lse, lse_strides, sel,
+                             self.ws_bytes, out.stride()[:2], out_lse, lse_strides, sel,
                              sel_count, room, scale, causal, self.status, stream)
 
 
@@ -495,18 +510,16 @@ class BlockSparseAttention:
     def _check_len(self, k_len):
         import torch
         if k_len is not None:
-            check_tensor(k_len, "k_len", (self.B,), (torch.int32,), contiguous=True)
-            _same_device(self.device, k_len=k_len)
+            _need(k_len, "k_len", (self.B,), (torch.int32,), self.device, contiguous=True)
 
     def select(self, Q, K, k_len=None, stream=None):
         """(sel, sel_count) for Q and K; k_len [B] int32 (device) bounds the
         valid keys of each batch entry."""
         import torch
         B, H, Hkv, d = self.B, self.H, self.Hkv, self.d
-        check_tensor(Q, "Q", (B, H, self.Nq, d), (torch.bfloat16,))
-        check_tensor(K, "K", (B, Hkv, self.Nk, d), (torch.bfloat16,))
+        _need(Q, "Q", (B, H, self.Nq, d), (torch.bfloat16,), self.device)
+        _need(K, "K", (B, Hkv, self.Nk, d), (torch.bfloat16,), self.device)
         self._check_len(k_len)
-        _same_device(self.device, Q=Q, K=K)
         with _launch_on(self.device):
             ditango_block_summary(B, H, self.Nq, d, QBLOCK, Q, Q.stride()[:3], self.q_codes, self.q_scale,
                                   stream=stream)
@@ -524,21 +537,21 @@ class BlockSparseAttention:
         blocks: the object's lists, or sel [B, Hkv, n_q, any] and sel_count."""
         import torch
         B, H, Hkv, Nq, d = self.B, self.H, self.Hkv, self.Nq, self.d
-        check_tensor(Q, "Q", (B, H, Nq, d), (torch.bfloat16,))
-        for name, t in (("K", K), ("V", V)):
-            check_tensor(t, name, (B, Hkv, self.Nk, d), (torch.bfloat16,))
-        check_tensor(out, "out", (B, H, Nq, d), (torch.bfloat16, torch.float32))
+        dev, bf16 = self.device, (torch.bfloat16,)
+        _need(Q, "Q", (B, H, Nq, d), bf16, dev)
+        _need(K, "K", (B, Hkv, self.Nk, d), bf16, dev)
+        _need(V, "V", (B, Hkv, self.Nk, d), bf16, dev)
+        _need(out, "out", (B, H, Nq, d), (torch.float32, torch.bfloat16), dev)
         if out_lse is not None:
-            check_tensor(out_lse, "out_lse", (B, H, Nq), (torch.float32,), contiguous=True)
+            _need(out_lse, "out_lse", (B, H, Nq), (torch.float32,), dev, contiguous=True)
         if (sel is None) != (sel_count is None):
             raise ValueError("sel and sel_count go together")
         if sel is None:
             sel, sel_count = self.sel, self.sel_count
         else:
-            check_tensor(sel, "sel", (B, Hkv, self.n_q, sel.shape[-1]), (torch.int32,), contiguous=True)
-            check_tensor(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), contiguous=True)
+            _need(sel, "sel", (B, Hkv, self.n_q, sel.shape[-1]), (torch.int32,), dev, contiguous=True)
+            _need(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), dev, contiguous=True)
         self._check_len(k_len)
-        _same_device(self.device, Q=Q, K=K, V=V, out=out, out_lse=out_lse, sel=sel, sel_count=sel_count)
         with _launch_on(self.device):
             ditango_block_attn(B, H, Hkv, Nq, self.Nk, d, Q, K, V, Q.stride()[:3], K.stride()[:3],
                                V.stride()[:3], sel, sel_count, sel.shape[-1], out,

@@ -123,9 +123,7 @@ def status_string(s: int) -> str:
 
 def _ptr(x):
     """Device address of a tensor (or an address given as an int)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     if getattr(x, "is_cuda", True) is False:
         # a host tensor's address would be dereferenced by a kernel
@@ -136,7 +134,10 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        dev = torch.cuda.current_device()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # the same handle as current_stream().cuda_stream, without a Stream object (3 us)
+        return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -320,9 +321,12 @@ def ditango_plan_noalloc(geom, cache_lse, cache_valid, band_k, budget, anchor, p
         _ptr(plan), _ptr(fresh_list), _ptr(counts), _ptr(score_out), _stream(stream)))
 
 
+_I64 = {2: C.c_int64 * 2, 3: C.c_int64 * 3}
+
+
 def _i64s(v):
     """A host int64 array of strides (None stays None)."""
-    return None if v is None else (C.c_int64 * len(v))(*v)
+    return None if v is None else _I64[len(v)](*v)
 
 
 def kv4(n_pages, Hkv, d, data):

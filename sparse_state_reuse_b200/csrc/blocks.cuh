@@ -20,6 +20,25 @@ constexpr int kQBlock = DITANGO_QBLOCK;   // queries of a query block
 
 __host__ __device__ constexpr int page_bytes(int d) { return kPage * (d + 8); }
 
+// Division of numbers below 2^31 by a fixed divisor: with l = ceil(log2 d),
+// m = floor(2^(31+l) / d) + 1 is over 2^(31+l) / d by at most one, so n m /
+// 2^(31+l) is over n / d by less than 1 / d and its floor is exact.
+struct FastDiv {
+  uint32_t d, m, shift;
+  FastDiv() : d(1), m(0), shift(0) {}
+  explicit FastDiv(uint32_t div) : d(div), m(0), shift(0) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    if (l > 0) {
+      m = (uint32_t)(((1ull << (31 + l)) / d) + 1);
+      shift = l - 1;
+    }
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
+#endif
+};
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ void set_status(int *dev_status, int code) {

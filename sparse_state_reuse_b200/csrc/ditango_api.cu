@@ -707,7 +707,7 @@ ditango_status kv4_rows(bool write, const ditango_kv4 *c, int64_t T, const uint1
   if (T < 0 || !ks || !vs) return DITANGO_ERR_INVALID;
   if (T == 0) return DITANGO_OK;
   if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return DITANGO_ERR_INVALID;
-  if (T >= (1LL << 40) / c->Hkv) return DITANGO_ERR_UNSUPPORTED;
+  if (T > ((1LL << 27) - 1) / c->Hkv) return DITANGO_ERR_UNSUPPORTED;   // the kernels' 32-bit row numbers
   int64_t kst[2], vst[2];
   if (!row_strides(ks, T, c->Hkv, c->d, 8, kst) || !row_strides(vs, T, c->Hkv, c->d, 8, vst))
     return DITANGO_ERR_INVALID;

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
 
 // ---------------------------------------------------------------- write, read
 struct RowsParams {
-  long long T;
+  uint32_t rows;                // T * Hkv, below 2^27
+  FastDiv heads;
   int Hkv, n_pages;
   const uint16_t *K, *V;
   uint16_t *Ko, *Vo;
@@ -146,34 +147,72 @@ struct RowsParams {
   int *dev_status;
 };
 
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Codes of 8 values of a row: c = round to nearest even of (x - lo) / s, as
-// exact arithmetic gives it.  The quotient is formed with one reciprocal; a
-// quotient too near to a half (closer than its error, or with sizes that
-// leave fp32's comfortable range) is formed again in fp64, where the
-// difference of two bf16 values is exact and the division correctly rounded.
-// The second path is rare (about one group of 8 in 10^4 on normal data).
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float hi, float s) {
-  if (!(s > 0.f)) return 0u;
-  const float inv = __frcp_rn(s);
-  const float off = -lo * inv;
-  const float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer
-  const float err = (fmaxf(fabsf(lo), fabsf(hi)) * inv + 16.f) * 4e-7f;
-  float far = 0.f;
+// exact arithmetic gives it.  Values that lie exactly between two codes are
+// common (x, lo and s are bf16: one in 200), so the quotient itself is formed
+// with correct rounding, by one step of Newton's iteration for the quotient on
+// t = x - lo with the correctly rounded reciprocal of s:
+//   q = t r,  q' = q + (t - q s) r.
+// A quotient that is k + 1/2 then comes out as that (it is a fp32 number), and
+// one that is not stays on its side: t and s being multiples of powers of two
+// with 24 and 8 bits, it is at least 2^-24 of itself away.  All of this needs t
+// to be exact; `bad` collects t + lo - x, which is 0 exactly then.  The few
+// groups with an inexact t, and scales outside fp32's comfortable range, are
+// formed again in fp64, where the difference of two bf16 values is exact for
+// what can matter to the rounding.
+__device__ __noinline__ uint32_t codes8_wide(uint4 v, float lo, float s) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   uint32_t w = 0;
-#pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float q = fmaf(x[k], inv, off);
-    const float t = q + kRound;
-    far = fmaxf(far, fabsf(q - (t - kRound)));
-    w |= (__float_as_uint(t) & 15u) << (4 * k);
+    const float x = (k & 1) ? bf_hi(u[k >> 1]) : bf_lo(u[k >> 1]);
+    const double q = rint(((double)x - (double)lo) / (double)s);
+    w |= (uint32_t)(int)fmin(fmax(q, 0.0), 15.0) << (4 * k);
   }
-  const bool plain = far < 0.5f - err && s > 1e-30f && s < 1e30f;
-  if (!plain) {
-    w = 0;
-    for (int k = 0; k < 8; ++k) {
-      const double q = rint(((double)x[k] - (double)lo) / (double)s);
-      w |= (uint32_t)(int)fmin(fmax(q, 0.0), 15.0) << (4 * k);
-    }
+  return w;
+}
+
+__device__ __forceinline__ uint32_t codes8(uint4 v, float lo, float s, float inv, float &bad) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  const float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, in the low bits
+  const uint64_t nlo2 = f2(-lo, -lo), lo2 = f2(lo, lo), inv2 = f2(inv, inv), ns2 = f2(-s, -s),
+                 round2 = f2(kRound, kRound), minus1 = f2(-1.f, -1.f);
+  uint32_t w = 0u - 0x4b400000u * 0x11111111u;   // the exponents of the eight sums, taken off
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t x = f2(bf_lo(u[k]), bf_hi(u[k]));
+    const uint64_t t = add2(x, nlo2);
+    const uint64_t back = fma2(x, minus1, add2(t, lo2));
+    const uint64_t q = mul2(t, inv2);
+    const uint64_t q1 = fma2(fma2(q, ns2, t), inv2, q);
+    float a, b, e, f;
+    unf2(add2(q1, round2), a, b);
+    unf2(back, e, f);
+    bad = fmaxf(bad, fmaxf(fabsf(e), fabsf(f)));
+    w += (__float_as_uint(a) << (8 * k)) + (__float_as_uint(b) << (8 * k + 4));
   }
   return w;
 }
@@ -192,117 +231,128 @@ __device__ __forceinline__ uint32_t scale_bits(float lo, float hi) {
   return (b + 0xffffu) >> 16;
 }
 
-// Quantise rows of D values into their pages.  A group of lanes takes a row,
-// 8 values a lane (16-byte loads), finds its least and largest value by
-// shuffles and writes one 4-byte word of codes a lane.
-template <int D>
-struct RowLanes {
-  static constexpr int kGroup = (D == 64) ? 8 : 16;     // lanes of a row (12 of 16 busy at 96)
-  static constexpr int kBusy = D / 8;
-  static constexpr int kRows = 32 / kGroup;             // rows of a warp
-};
-
+// Quantise rows of D values into their pages.  Four lanes take a row, D / 4
+// values each (16-byte loads), so that all lanes are busy for every d and the
+// address arithmetic is spread over 16 to 32 values; least and largest value
+// are found with packed bf16 minima of (x, -x) and two shuffles.
 constexpr int kRowThreads = 256;
-constexpr int kRowsAhead = 4;      // rows a lane has in flight
+
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {   // NaN if either is
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) write_kernel(const RowsParams p) {
-  using L = RowLanes<D>;
-  const int lane = threadIdx.x & 31;
-  const int sub = lane % L::kGroup, grp = lane / L::kGroup;
-  const bool busy = sub < L::kBusy;
+  constexpr int kLoads = D / 32;                        // 16-byte loads of a lane and row
+  const int sub = threadIdx.x & 3;
   const int which = blockIdx.y;      // 0: K, 1: V
   const uint16_t *src = which ? p.V : p.K;
   const long long ts = which ? p.vt : p.kt, hs = which ? p.vh : p.kh;
-  const long long rows = p.T * p.Hkv;
-  const long long step = (long long)gridDim.x * (kRowThreads / 32) * L::kRows;
-  long long row = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * L::kRows + grp;
-  const uint32_t mask = 0xffffffffu;
-  for (; row - grp < rows; row += step * kRowsAhead) {
-    uint4 v[kRowsAhead];
-    long long slot[kRowsAhead];
-    int head[kRowsAhead];
+  const uint32_t step = gridDim.x * (kRowThreads / 4);
+  const uint32_t padded = (p.rows + 7u) & ~7u;          // whole warps stay together
+  uint32_t row = blockIdx.x * (kRowThreads / 4) + threadIdx.x / 4;
+  uint4 v[kLoads];
+  long long slot = -1;
+  int head = 0;
+  auto fetch = [&](uint32_t r) {
+    slot = -1;
+    if (r < p.rows) {
+      const uint32_t t = p.heads.div(r);
+      head = (int)(r - t * p.heads.d);
+      slot = __ldg(p.slots + t);
+      const uint4 *at = reinterpret_cast<const uint4 *>(src + t * ts + head * hs + sub * (D / 4));
 #pragma unroll
-    for (int a = 0; a < kRowsAhead; ++a) {
-      const long long r = row + a * step;
-      slot[a] = -1;
-      v[a] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const long long t = r / p.Hkv;
-        head[a] = (int)(r - t * p.Hkv);
-        slot[a] = __ldg(p.slots + t);
-        if (busy) v[a] = __ldcs(reinterpret_cast<const uint4 *>(src + t * ts + head[a] * hs) + sub);
-      }
+      for (int k = 0; k < kLoads; ++k) v[k] = __ldg(at + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) v[k] = make_uint4(0, 0, 0, 0);
     }
+  };
+  for (; row < padded; row += step) {
+    fetch(row);
+    uint32_t mn = min_bf16x2(min_bf16x2(v[0].x, v[0].y), min_bf16x2(v[0].z, v[0].w));
+    uint32_t mx = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
 #pragma unroll
-    for (int a = 0; a < kRowsAhead; ++a) {
-      const uint32_t u[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-      float x[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = bf_lo(u[k]);
-        x[2 * k + 1] = bf_hi(u[k]);
-      }
-      float lo = x[0], hi = x[0], bad = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        lo = fminf(lo, x[k]);
-        hi = fmaxf(hi, x[k]);
-        bad = fmaf(x[k], 0.f, bad);     // NaN once a value is not finite
-      }
-      if (!busy) {
-        lo = INFINITY;
-        hi = -INFINITY;
-      }
-#pragma unroll
-      for (int o = 1; o < L::kGroup; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-        bad += __shfl_xor_sync(mask, bad, o);
-      }
-      if (slot[a] < 0) continue;
-      if (slot[a] >= (long long)p.n_pages * kPage) {
-        if (sub == 0) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
-        continue;
-      }
-      const long long page = slot[a] / kPage;
-      const int at = (int)(slot[a] % kPage);
-      uint8_t *base = p.data + ((size_t)page * p.Hkv + head[a]) * page_bytes(D);
-      uint32_t sb = scale_bits(lo, hi);
-      uint32_t w = codes8(x, lo, hi, __uint_as_float(sb << 16));
-      uint32_t lb = __float_as_uint(lo) >> 16;
-      if (!(bad == 0.f)) {              // an infinity or a NaN: the row stands for NaN
-        w = 0;
-        sb = lb = 0x7fff;
-      }
-      if (busy) *reinterpret_cast<uint32_t *>(base + which * (kPage * D / 2) + at * (D / 2) + sub * 4) = w;
-      if (sub == 0) *reinterpret_cast<uint32_t *>(base + kPage * D + which * (kPage * 4) + at * 4) = sb | (lb << 16);
+    for (int k = 1; k < kLoads; ++k) {
+      mn = min_bf16x2(mn, min_bf16x2(min_bf16x2(v[k].x, v[k].y), min_bf16x2(v[k].z, v[k].w)));
+      mx = max_bf16x2(mx, max_bf16x2(max_bf16x2(v[k].x, v[k].y), max_bf16x2(v[k].z, v[k].w)));
     }
+    // (least, -largest) in one register
+    const uint32_t neg = mx ^ 0x80008000u;
+    uint32_t both = min_bf16x2(__byte_perm(mn, neg, 0x5410), __byte_perm(mn, neg, 0x7632));
+    both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+    both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+    if (slot < 0) continue;
+    if (slot >= (long long)p.n_pages * kPage) {
+      if (sub == 0) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+      continue;
+    }
+    const float lo = bf_lo(both), hi = -bf_hi(both);
+    const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;   // false for NaN
+    uint32_t sb = scale_bits(lo, hi);
+    const float s = __uint_as_float(sb << 16);
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    const bool fine = (s > 1e-30f && s < 1e30f) || s == 0.f;
+    uint32_t w[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      float bad = fine ? 0.f : 1.f;
+      w[k] = codes8(v[k], lo, s, inv, bad);
+      if (bad != 0.f && finite && s > 0.f) w[k] = codes8_wide(v[k], lo, s);
+    }
+    uint32_t lb = both & 0xffffu;
+    if (!finite) {                    // an infinity or a NaN: the row stands for NaN
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) w[k] = 0u;
+      sb = lb = 0x7fffu;
+    }
+    const long long page = slot / kPage;
+    const int at = (int)(slot % kPage);
+    uint8_t *base = p.data + ((size_t)page * p.Hkv + head) * page_bytes(D);
+    uint32_t *codes = reinterpret_cast<uint32_t *>(base + which * (kPage * D / 2) + at * (D / 2) + sub * (D / 8));
+    if constexpr (kLoads == 4) {
+      *reinterpret_cast<uint4 *>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (kLoads == 2) {
+      *reinterpret_cast<uint2 *>(codes) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) codes[k] = w[k];
+    }
+    if (sub == 0) *reinterpret_cast<uint32_t *>(base + kPage * D + which * (kPage * 4) + at * 4) = sb | (lb << 16);
   }
 }
+
+constexpr int kRowsAhead = 4;      // units that a lane of read_kernel has in flight
 
 // Rows back to bf16: each value c * scale + least, formed in fp32 (the
 // product of a 4-bit code and an 8-bit significand is exact) and rounded once.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const RowsParams p) {
-  constexpr int kLanes = D / 8;
+  constexpr uint32_t kLanes = D / 8;
   const int which = blockIdx.y;
   uint16_t *dst = which ? p.Vo : p.Ko;
   const long long ts = which ? p.vt : p.kt, hs = which ? p.vh : p.kh;
-  const long long n = p.T * p.Hkv * kLanes, step = (long long)gridDim.x * kRowThreads;
-  long long i0 = (long long)blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t n = p.rows * kLanes, step = gridDim.x * kRowThreads;
+  uint32_t i0 = blockIdx.x * kRowThreads + threadIdx.x;
   for (; i0 < n; i0 += step * kRowsAhead) {
     uint32_t w[kRowsAhead], meta[kRowsAhead];
     uint16_t *out[kRowsAhead];
 #pragma unroll
     for (int a = 0; a < kRowsAhead; ++a) {
-      const long long i = i0 + a * step;
+      const uint32_t i = i0 + a * step;
       out[a] = nullptr;
       if (i >= n) continue;
-      const long long r = i / kLanes;
+      const uint32_t r = i / kLanes;
       const int sub = (int)(i - r * kLanes);
-      const long long t = r / p.Hkv;
-      const int h = (int)(r - t * p.Hkv);
+      const uint32_t t = p.heads.div(r);
+      const int h = (int)(r - t * p.heads.d);
       const long long slot = __ldg(p.slots + t);
       if (slot < 0) continue;
       if (slot >= (long long)p.n_pages * kPage) {
@@ -430,11 +480,11 @@ cudaError_t launch_kv4_rows(bool write, long long T, int Hkv, int d, int n_pages
                             const int64_t *v_strides, const long long *slots, uint8_t *data,
                             int *dev_status, int num_sms, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  hist::RowsParams p{T, Hkv, n_pages, K, V, Ko, Vo, k_strides[0], k_strides[1], v_strides[0],
+  hist::RowsParams p{(uint32_t)(T * Hkv), FastDiv((uint32_t)Hkv), Hkv, n_pages, K, V, Ko, Vo, k_strides[0], k_strides[1], v_strides[0],
                      v_strides[1], slots, data, dev_status};
-  const long long lanes = T * Hkv * (write ? (d == 64 ? 8 : 16) : d / 8);
+  const long long lanes = T * Hkv * (write ? 4 : d / 8);
   long long grid = (lanes + hist::kRowThreads - 1) / hist::kRowThreads;
-  if (grid > 4LL * num_sms) grid = 4LL * num_sms;
+  if (grid > 8LL * num_sms) grid = 8LL * num_sms;
   const dim3 g((unsigned)grid, 2);
 #define DITANGO_ROWS(D)                                                          \
   if (write)                                                                     \

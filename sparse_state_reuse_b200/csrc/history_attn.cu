@@ -1,23 +1,30 @@
 // Attention of few query rows over the paged 4-bit history.
 //
-// For request r, key head h and row (token, query head of the group):
-//   k_j = s_j c_j + m_j  =>  q.k_j = s_j (q.c_j) + m_j sum(q)
-//   O = sum_j p_j v_j    =   sum_j (p_j s'_j) c'_j + sum_j p_j m'_j
-// so that the 4-bit codes enter the tensor core as they are: a code c is put
-// into the significand of a bf16 number, 1 + c/16, by a shift and one LOP3 for
-// two codes (exact), and scale and least value are applied to whole rows of
-// scores and to the probabilities in fp32.  Of the values that are rounded
-// only the probabilities times the V scale are (to bf16, as everywhere in the
-// library); the part that the added 1 contributes is taken out again with the
-// same rounded values, so that it cancels.
+// For request r, key head h and row (token, query head of the group), with the
+// codes taken around the middle, k_j = s_j (c_j - 8) + h_j, h_j = m_j + 8 s_j:
+//   q.k_j = s_j (q.(c_j - 8)) + h_j sum(q)
+//   O     = sum_j (p_j s'_j) (c'_j - 8) + sum_j p_j h'_j
+// so that the 4-bit codes enter the tensor core as they are.  Two codes become
+// a pair of fp16 numbers by one LOP3 (1024 + c, or 1024 + 16 c for every other
+// code; one shift serves four) and one packed FMA that leaves c - 8, exactly;
+// scales and h are applied to scores and probabilities in fp32.  fp16 and not
+// bf16: its longer significand takes two codes in place, and it rounds p s' to
+// 2^-11.  Q is scaled by a power of two a row to lie below 2 (an exact step for
+// all but values 2^-24 of the row's largest), p s' by one that follows the
+// largest V scale met so far.
 //
-// It is bound by the history's bytes: d + 8 a key and key head.  Each warp is
-// by itself: it takes every fourth page of its block's range, fetches a page
-// of one head (one contiguous run) with one bulk copy into a ring of its own
-// and runs m16n8k16 products over it, 16 rows a tile; no block-wide barrier
-// until the end of a range.  The tile has 16 rows because a few rows are all
-// there is; with so few the legacy tensor instructions already outrun the
-// memory, and a tcgen05 tile of 128 rows would be mostly padding.
+// Keys and channels are the rows of the products (m16n8k16, S^T = K Q^T and
+// O^T = V^T P^T) and query rows their 8 columns: 8 rows at a time, of which a
+// decode step has few.  P^T goes from the first product's layout to the
+// second's by a transpose of 8x8 tiles in registers.
+//
+// It is bound by the history's bytes, d + 8 a key and key head, as long as the
+// instructions that unpack them keep up.  Each warp is by itself: it takes
+// every fourth page of its block's range, fetches a page of one head (one
+// contiguous run) with one bulk copy into a ring of its own and works through
+// it; no block-wide barrier until the end of a range.  With so few rows the
+// legacy tensor instructions are not what bounds it (30% of their rate), and a
+// tcgen05 tile of 128 rows would be mostly padding.
 //
 // Work split: the pages of all (request, key head, row tile) items are one
 // line of work that is cut into equal ranges, one a block, so that a single
@@ -37,8 +44,11 @@ namespace hattn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // rows of a tile, at most
-constexpr int kMaxBlocks = 512;      // most blocks of a launch (the workspace has room for them)
+constexpr int kMaxBlocks = 768;      // most blocks of a launch (the workspace has room for them)
 constexpr float kRescaleLog2 = 8.0f;
+// p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
+// 2^6 more uses the range that is left.
+constexpr float kWeightScale = 64.f;
 
 struct Params {
   int R, H, Hkv, G, T, max_blocks, n_pages, max_sel, causal;
@@ -59,24 +69,48 @@ struct Params {
   long long wait_limit_ns;
 };
 
-// Key of column n of an 8-key tile.  The order within a tile is free (scores
-// and values use the same); this one spreads the rows that a warp reads at
-// once over the shared-memory banks.
+// Key of row n of an 8-key tile.  The order within a tile is free (scores and
+// values use the same); this one spreads the rows that a warp reads at once
+// over the shared-memory banks.
 __device__ __forceinline__ int key_of(int n) { return n ^ ((n >> 1) & 1); }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word (i = 0..3) as the bf16 pair 1 + c/16.
-template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  const uint32_t x = (I == 0) ? (w << 3) : (w >> (4 * I - 3));
-  return (x & 0x00780078u) | 0x3f803f80u;
+// Transpose of an 8x8 tile of 16-bit values held by the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Codes i and i + 4 of a word, i = 0..3, less 8, as fp16 pairs.
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&pair)[4]) {
+  const uint32_t kOne = 0x3c003c00u, k16th = 0x2c002c00u;            // 1, 1/16
+  const uint32_t kEven = 0xe408e408u, kOdd = 0xd480d480u;            // -1032, -72
+  const uint32_t v = w >> 8;
+  pair[0] = hfma2((w & 0x000f000fu) | 0x64006400u, kOne, kEven);     // 1024 + c
+  pair[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, k16th, kOdd);     // 1024 + 16 c
+  pair[2] = hfma2((v & 0x000f000fu) | 0x64006400u, kOne, kEven);
+  pair[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, k16th, kOdd);
 }
 
 struct Request {
@@ -139,13 +173,213 @@ struct Smem {
   static_assert(kStage % 16 == 0, "bulk copies");
 };
 
-// LOW: tiles of 8 rows (the upper half of each product is padding).
-template <int D, bool LOW, int NS>
-__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constant__ Params p) {
+// What a warp holds of a row tile of 8 NR rows: Q as the second operand of
+// K Q^T, O^T, and of its rows 2t, 2t + 1 (+ 8) the softmax state.
+template <int D, int NR>
+struct WarpTile {
+  static constexpr int W = D / 32;   // words of K codes of a lane and key
+  static constexpr int MT = D / 16;  // 16-channel tiles of O^T
+  uint32_t q[NR][2 * W][2];
+  float o[NR][MT][4];
+  float qsum[2 * NR], mul[2 * NR];   // sum of the scaled q; log2(e) scale 2^exponent
+  float m[2 * NR], l[2 * NR], z[2 * NR];   // running maximum (log2), lane's sums of p and of p h'
+  int vis[2 * NR];                   // keys that the row sees
+  float vref;                        // power of two that no V scale so far exceeds
+};
+
+// One page: 64 keys of one head, codes and scales at st.
+template <int D, int NR, bool MASKED>
+__device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const uint8_t *st, int k_base, int kv) {
+  using T = WarpTile<D, NR>;
+  const int lane = threadIdx.x & 31, t = lane & 3, n8 = lane >> 2;
+  const int kn = key_of(n8);
+  // scores of keys 16 u + {kn, 8 + kn} for rows 2t, 2t + 1, before the row's factor
+  float sc[4][NR][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[u][x][e] = 0.f;
+    const uint8_t *ra = st + (16 * u + kn) * (D / 2) + t * (D / 8), *rb = ra + 8 * (D / 2);
+    uint32_t ka[T::W], kb[T::W];
+    if constexpr (T::W == 4) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(ra), b = *reinterpret_cast<const uint4 *>(rb);
+      ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
+      kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
+    } else if constexpr (T::W == 2) {
+      const uint2 a = *reinterpret_cast<const uint2 *>(ra), b = *reinterpret_cast<const uint2 *>(rb);
+      ka[0] = a.x; ka[1] = a.y;
+      kb[0] = b.x; kb[1] = b.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < T::W; ++i) {
+        ka[i] = *reinterpret_cast<const uint32_t *>(ra + 4 * i);
+        kb[i] = *reinterpret_cast<const uint32_t *>(rb + 4 * i);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < T::W; ++i) {
+      uint32_t pa[4], pb[4];
+      unpack8(ka[i], pa);
+      unpack8(kb[i], pb);
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        mma16816(sc[u][x], pa[0], pb[0], pa[1], pb[1], w.q[x][2 * i][0], w.q[x][2 * i][1]);
+        mma16816(sc[u][x], pa[2], pb[2], pa[3], pb[3], w.q[x][2 * i + 1][0], w.q[x][2 * i + 1][1]);
+      }
+    }
+    const uint8_t *meta = st + kPage * D + (16 * u + kn) * 4;
+    const uint32_t ma = *reinterpret_cast<const uint32_t *>(meta), mb = *reinterpret_cast<const uint32_t *>(meta + 32);
+    const float sa = bf_lo(ma), sb = bf_lo(mb);
+    const float ha = fmaf(8.f, sa, bf_hi(ma)), hb = fmaf(8.f, sb, bf_hi(mb));
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      sc[u][x][0] = fmaf(sc[u][x][0], sa, ha * w.qsum[2 * x]);
+      sc[u][x][1] = fmaf(sc[u][x][1], sa, ha * w.qsum[2 * x + 1]);
+      sc[u][x][2] = fmaf(sc[u][x][2], sb, hb * w.qsum[2 * x]);
+      sc[u][x][3] = fmaf(sc[u][x][3], sb, hb * w.qsum[2 * x + 1]);
+    }
+    if constexpr (MASKED) {
+      const int key = k_base + 16 * u + kn;
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key + 8 * (e >> 1) >= w.vis[2 * x + (e & 1)]) sc[u][x][e] = -INFINITY;
+    }
+  }
+  // running maximum; O is rescaled only when it grew by more than 2^8
+  bool need = false;
+  float mx[2 * NR];
+#pragma unroll
+  for (int y = 0; y < 2 * NR; ++y) {
+    float v = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v = fmaxf(v, fmaxf(sc[u][y >> 1][y & 1], sc[u][y >> 1][2 + (y & 1)]));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+    mx[y] = v * w.mul[y];
+    need = need || mx[y] > w.m[y] + kRescaleLog2;
+  }
+  // the largest V scale of the page (rows that stand for NaN have none)
+  uint32_t top;
+  {
+    const uint32_t *vm = reinterpret_cast<const uint32_t *>(st + kPage * D + kPage * 4);
+    uint32_t a = vm[lane] & 0xffffu, b = vm[lane + 32] & 0xffffu;
+    if constexpr (MASKED) {
+      if (k_base + lane >= kv) a = 0u;
+      if (k_base + lane + 32 >= kv) b = 0u;
+    }
+    if (a >= 0x7f80u) a = 0u;
+    if (b >= 0x7f80u) b = 0u;
+    top = __reduce_max_sync(0xffffffffu, max(a, b));
+  }
+  float vmul = 1.f;
+  if (__uint_as_float(top << 16) > w.vref) {
+    const float v = __uint_as_float(min(max(((top >> 7) + 1u), 64u), 254u) << 23);
+    vmul = w.vref / v;
+    w.vref = v;
+    need = true;
+  }
+  if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+    for (int y = 0; y < 2 * NR; ++y) {
+      const float mn = fmaxf(w.m[y], mx[y]);
+      const float al = w.m[y] == mn ? 1.f : fast_ex2(w.m[y] - mn);
+      w.m[y] = mn;
+      w.l[y] *= al;
+      w.z[y] *= al;
+      const float ao = al * vmul;
+#pragma unroll
+      for (int j = 0; j < T::MT; ++j) {
+        w.o[y >> 1][j][y & 1] *= ao;
+        w.o[y >> 1][j][2 + (y & 1)] *= ao;
+      }
+    }
+  }
+  float neg[2 * NR];
+#pragma unroll
+  for (int y = 0; y < 2 * NR; ++y) neg[y] = w.m[y] > -INFINITY ? -w.m[y] : 0.f;   // no key so far: against 0
+  const float vs = kWeightScale / w.vref;
+  // 16 keys at a time: p, the weights p s', and the second product
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint8_t *meta = st + kPage * D + kPage * 4 + (16 * u + kn) * 4;
+    const uint32_t ma = *reinterpret_cast<const uint32_t *>(meta), mb = *reinterpret_cast<const uint32_t *>(meta + 32);
+    const float sa = bf_lo(ma), sb = bf_lo(mb);
+    const float ha = fmaf(8.f, sa, bf_hi(ma)), hb = fmaf(8.f, sb, bf_hi(mb));
+    const float wa = sa * vs, wb = sb * vs;
+    uint32_t pb[NR][2];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      float e[4], g[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int y = 2 * x + (q & 1);
+        e[q] = fast_ex2(fmaf(sc[u][x][q], w.mul[y], neg[y]));
+        g[q] = e[q] * (q < 2 ? wa : wb);
+        float c = e[q] * (q < 2 ? ha : hb);
+        if constexpr (MASKED) {       // a masked token's scale may be anything
+          if (k_base + 16 * u + kn + 8 * (q >> 1) >= w.vis[y]) g[q] = c = 0.f;
+        }
+        w.l[y] += e[q];
+        w.z[y] += c;
+      }
+      pb[x][0] = transpose8x8(pack_f16x2(g[0], g[1]));
+      pb[x][1] = transpose8x8(pack_f16x2(g[2], g[3]));
+    }
+    // keys 2t, 2t + 1 (+ 8) of the 16, channels by lane: 8 n8 + i of each 64
+    const uint8_t *r0 = st + kPage * (D / 2) + (16 * u + key_of(2 * t)) * (D / 2);
+    const uint8_t *r1 = st + kPage * (D / 2) + (16 * u + key_of(2 * t + 1)) * (D / 2);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int at = 32 * i + 4 * n8;
+      const uint32_t a = *reinterpret_cast<const uint32_t *>(r0 + at);
+      const uint32_t b = *reinterpret_cast<const uint32_t *>(r1 + at);
+      const uint32_t c = *reinterpret_cast<const uint32_t *>(r0 + 8 * (D / 2) + at);
+      const uint32_t d = *reinterpret_cast<const uint32_t *>(r1 + 8 * (D / 2) + at);
+      uint32_t xl[4], xh[4], yl[4], yh[4];
+      unpack8(__byte_perm(a, b, 0x5410), xl);
+      unpack8(__byte_perm(a, b, 0x7632), xh);
+      unpack8(__byte_perm(c, d, 0x5410), yl);
+      unpack8(__byte_perm(c, d, 0x7632), yh);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+          mma16816(w.o[x][4 * i + j], xl[j], xh[j], yl[j], yh[j], pb[x][0], pb[x][1]);
+    }
+    if constexpr (D % 64 != 0) {     // d = 96: the last 32 channels, 4 n8 + i
+      const int at = 32 * (D / 64) + 2 * n8;
+      const uint32_t a = *reinterpret_cast<const uint16_t *>(r0 + at);
+      const uint32_t b = *reinterpret_cast<const uint16_t *>(r1 + at);
+      const uint32_t c = *reinterpret_cast<const uint16_t *>(r0 + 8 * (D / 2) + at);
+      const uint32_t d = *reinterpret_cast<const uint16_t *>(r1 + 8 * (D / 2) + at);
+      uint32_t xl[4], yl[4];
+      unpack8(__byte_perm(a, b, 0x5410), xl);
+      unpack8(__byte_perm(c, d, 0x5410), yl);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+          mma16816(w.o[x][T::MT - 2 + j], xl[2 * j], xl[2 * j + 1], yl[2 * j], yl[2 * j + 1], pb[x][0], pb[x][1]);
+    }
+  }
+}
+
+// Blocks of an SM: at d = 96 and 64 a fourth fits beside the rings of three
+// if a thread keeps to 128 registers.
+template <int D, int NR>
+__host__ __device__ constexpr int min_blocks() { return NR == 2 ? 2 : (D == 128 ? 3 : 4); }
+
+// NR: 8-row groups of a tile.
+template <int D, int NR, int NS>
+__global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel(const __grid_constant__ Params p) {
   using S = Smem<D, NS>;
-  constexpr int W = D / 32;          // words of K codes of a lane and key
-  constexpr int NT = D / 8;          // channel tiles of O
-  constexpr int NR = LOW ? 1 : 2;    // rows of a lane
+  using WT = WarpTile<D, NR>;
+  constexpr int W = WT::W, MT = WT::MT;
   constexpr int TR = 8 * NR;         // rows of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) unsigned long long bars[kWarps][NS];
@@ -221,49 +455,67 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
                            : (rq.kv + kPage - 1) / kPage;
     const int end = min(p1, n_list);
 
-    // Q of the lane's rows, in the order in which code_pair gives the codes
-    uint32_t qa[2 * W][4];
-    float qsum[NR];
-    int vis[NR];
+    WT w;
+    // Q: the lane holds row n8 (+ 8) as the second operand, channels in the
+    // order in which unpack8 gives the codes, scaled to lie below 2
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NR; ++x) {
       const int row = n8 + 8 * x;
-      float sum = 0.f;
-      const bool live = (x < NR) && row < rows;
+      const bool live = row < rows;
       const int tok = live ? (row0 + row) / p.G : 0, head = live ? (row0 + row) % p.G : 0;
       const uint16_t *src = p.Q + (rq.q0 + tok) * p.qt + (h * p.G + head) * p.qh + t * (D / 4);
+      uint4 u[W];
+      float big = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (live) u = __ldg(reinterpret_cast<const uint4 *>(src) + w);
-        qa[2 * w][x] = __byte_perm(u.x, u.z, 0x5410);
-        qa[2 * w][2 + x] = __byte_perm(u.x, u.z, 0x7632);
-        qa[2 * w + 1][x] = __byte_perm(u.y, u.w, 0x5410);
-        qa[2 * w + 1][2 + x] = __byte_perm(u.y, u.w, 0x7632);
-        sum += ((bf_lo(u.x) + bf_hi(u.x)) + (bf_lo(u.y) + bf_hi(u.y))) +
-               ((bf_lo(u.z) + bf_hi(u.z)) + (bf_lo(u.w) + bf_hi(u.w)));
+      for (int i = 0; i < W; ++i) {
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (live) u[i] = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf_lo(v[e])), fabsf(bf_hi(v[e]))));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+      const float down = __uint_as_float((254u - ex) << 23);      // 2^-(ex - 127)
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[2 * e] = bf_lo(v[e]) * down;
+          f[2 * e + 1] = bf_hi(v[e]) * down;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += f[e];
+        w.q[x][2 * i][0] = pack_f16x2(f[0], f[4]);
+        w.q[x][2 * i][1] = pack_f16x2(f[1], f[5]);
+        w.q[x][2 * i + 1][0] = pack_f16x2(f[2], f[6]);
+        w.q[x][2 * i + 1][1] = pack_f16x2(f[3], f[7]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (x < NR) {
-        qsum[x] = sum;
-        vis[x] = p.causal && live ? rq.kv - (rq.n_q - 1 - tok) : rq.kv;
+      // rows 2t and 2t + 1 belong to lanes 8t and 8t + 4
+      const float mul = p.scale_log2 * __uint_as_float(ex << 23);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int y = 2 * x + e, r8 = 2 * t + e;
+        w.qsum[y] = __shfl_sync(0xffffffffu, sum, 4 * r8);
+        w.mul[y] = __shfl_sync(0xffffffffu, mul, 4 * r8);
+        w.vis[y] = p.causal ? rq.kv - (rq.n_q - 1 - min(rq.n_q - 1, (row0 + 8 * x + r8) / p.G)) : rq.kv;
+        w.m[y] = -INFINITY;
+        w.l[y] = w.z[y] = 0.f;
       }
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.o[x][j][e] = 0.f;
     }
+    w.vref = __uint_as_float(64u << 23);
     // keys that every row of the tile sees
     const int vis_all = p.causal ? rq.kv - (rq.n_q - 1 - row0 / p.G) : rq.kv;
-
-    float o[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[NR], l[NR], z[NR];      // running maximum; lane's sums of p, and of p least - p'
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      m[x] = -INFINITY;
-      l[x] = z[x] = 0.f;
-    }
 
     auto issue = [&](uint32_t at, int page) {
       if (lane == 0 && page >= 0) {
@@ -309,138 +561,10 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
       if (!(ok = wait_warp(bar0 + 8 * (it % NS), (it / NS) & 1, ctl))) break;
       const uint8_t *st = ring + (it % NS) * S::kStage;
       const int k_base = blk[0] * kPage;
-      const bool masked = k_base + kPage > vis_all;
-
-      // scores of 64 keys: x = log2(e) scale (s 16 acc + (m - 16 s) sum q)
-      float sc[8][2 * NR];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint8_t *kr = st + (8 * u + key_of(n8)) * (D / 2) + t * (D / 8);
-        uint32_t kw[W];
-        if constexpr (W == 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(kr);
-          kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-        } else if constexpr (W == 2) {
-          const uint2 v = *reinterpret_cast<const uint2 *>(kr);
-          kw[0] = v.x; kw[1] = v.y;
-        } else {
-#pragma unroll
-          for (int w = 0; w < W; ++w) kw[w] = *reinterpret_cast<const uint32_t *>(kr + 4 * w);
-        }
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          mma16816(acc, qa[2 * w], code_pair<0>(kw[w]), code_pair<1>(kw[w]));
-          mma16816(acc, qa[2 * w + 1], code_pair<2>(kw[w]), code_pair<3>(kw[w]));
-        }
-        // columns 2t and 2t + 1 are keys 2t and 2t + 1, exchanged where t is odd
-        const uint2 mt = *reinterpret_cast<const uint2 *>(st + kPage * D + (8 * u + 2 * t) * 4);
-        const uint32_t m0 = (t & 1) ? mt.y : mt.x, m1 = (t & 1) ? mt.x : mt.y;
-        const float a0 = bf_lo(m0) * (16.f * p.scale_log2), a1 = bf_lo(m1) * (16.f * p.scale_log2);
-        const float b0 = fmaf(bf_hi(m0), p.scale_log2, -a0), b1 = fmaf(bf_hi(m1), p.scale_log2, -a1);
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          sc[u][2 * x] = fmaf(acc[2 * x], a0, b0 * qsum[x]);
-          sc[u][2 * x + 1] = fmaf(acc[2 * x + 1], a1, b1 * qsum[x]);
-        }
-      }
-      if (masked) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-          for (int e = 0; e < 2 * NR; ++e) {
-            const int key = k_base + 8 * u + key_of(2 * t + (e & 1));
-            if (key >= vis[e >> 1]) sc[u][e] = -INFINITY;
-          }
-      }
-      // running maximum; O is rescaled only when it grew by more than 2^8
-      bool need = false;
-      float mx[NR];
-#pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        float v = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v = fmaxf(v, fmaxf(sc[u][2 * x], sc[u][2 * x + 1]));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        mx[x] = v;
-        need = need || v > m[x] + kRescaleLog2;
-      }
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          const float mn = fmaxf(m[x], mx[x]);
-          const float al = m[x] == mn ? 1.f : fast_ex2(m[x] - mn);
-          m[x] = mn;
-          l[x] *= al;
-          z[x] *= al;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[j][2 * x] *= al;
-            o[j][2 * x + 1] *= al;
-          }
-        }
-      }
-      // 16 keys at a time: p, then p times the V scale, rounded, and the products
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t pa[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int u = 2 * v + g;
-          const uint2 mt = *reinterpret_cast<const uint2 *>(st + kPage * D + kPage * 4 + (8 * u + 2 * t) * 4);
-          const uint32_t m0 = (t & 1) ? mt.y : mt.x, m1 = (t & 1) ? mt.x : mt.y;
-          const float s0 = 16.f * bf_lo(m0), s1 = 16.f * bf_lo(m1), h0 = bf_hi(m0), h1 = bf_hi(m1);
-#pragma unroll
-          for (int x = 0; x < NR; ++x) {
-            const float neg = m[x] > -INFINITY ? -m[x] : 0.f;
-            const float e0 = fast_ex2(sc[u][2 * x] + neg), e1 = fast_ex2(sc[u][2 * x + 1] + neg);
-            l[x] += e0 + e1;
-            float w0_ = e0 * s0, w1_ = e1 * s1, c0 = e0 * h0, c1 = e1 * h1;
-            if (masked) {           // a masked token's scale may be anything
-              const int kb = k_base + 8 * u;
-              if (kb + key_of(2 * t) >= vis[x]) w0_ = c0 = 0.f;
-              if (kb + key_of(2 * t + 1) >= vis[x]) w1_ = c1 = 0.f;
-            }
-            const uint32_t pk = pack_bf16x2(w0_, w1_);
-            pa[2 * g + x] = pk;
-            z[x] += (c0 - bf_lo(pk)) + (c1 - bf_hi(pk));
-          }
-        }
-        const uint8_t *vr = st + kPage * (D / 2);
-        const uint8_t *r0p = vr + (16 * v + key_of(2 * t)) * (D / 2);
-        const uint8_t *r1p = vr + (16 * v + key_of(2 * t + 1)) * (D / 2);
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          const int at = 32 * w + 4 * n8;
-          const uint32_t ka = *reinterpret_cast<const uint32_t *>(r0p + at);
-          const uint32_t kb = *reinterpret_cast<const uint32_t *>(r1p + at);
-          const uint32_t kc = *reinterpret_cast<const uint32_t *>(r0p + 8 * (D / 2) + at);
-          const uint32_t kd = *reinterpret_cast<const uint32_t *>(r1p + 8 * (D / 2) + at);
-          const uint32_t xl = __byte_perm(ka, kb, 0x5410), xh = __byte_perm(ka, kb, 0x7632);
-          const uint32_t yl = __byte_perm(kc, kd, 0x5410), yh = __byte_perm(kc, kd, 0x7632);
-          mma16816(o[8 * w + 0], pa, code_pair<0>(xl), code_pair<0>(yl));
-          mma16816(o[8 * w + 1], pa, code_pair<1>(xl), code_pair<1>(yl));
-          mma16816(o[8 * w + 2], pa, code_pair<2>(xl), code_pair<2>(yl));
-          mma16816(o[8 * w + 3], pa, code_pair<3>(xl), code_pair<3>(yl));
-          mma16816(o[8 * w + 4], pa, code_pair<0>(xh), code_pair<0>(yh));
-          mma16816(o[8 * w + 5], pa, code_pair<1>(xh), code_pair<1>(yh));
-          mma16816(o[8 * w + 6], pa, code_pair<2>(xh), code_pair<2>(yh));
-          mma16816(o[8 * w + 7], pa, code_pair<3>(xh), code_pair<3>(yh));
-        }
-        if constexpr (D % 64 != 0) {   // d = 96: the last 32 channels, four a lane
-          const int at = 32 * (D / 64) + 2 * n8;
-          const uint32_t ka = *reinterpret_cast<const uint16_t *>(r0p + at);
-          const uint32_t kb = *reinterpret_cast<const uint16_t *>(r1p + at);
-          const uint32_t kc = *reinterpret_cast<const uint16_t *>(r0p + 8 * (D / 2) + at);
-          const uint32_t kd = *reinterpret_cast<const uint16_t *>(r1p + 8 * (D / 2) + at);
-          const uint32_t xl = __byte_perm(ka, kb, 0x5410), yl = __byte_perm(kc, kd, 0x5410);
-          mma16816(o[NT - 4], pa, code_pair<0>(xl), code_pair<0>(yl));
-          mma16816(o[NT - 3], pa, code_pair<1>(xl), code_pair<1>(yl));
-          mma16816(o[NT - 2], pa, code_pair<2>(xl), code_pair<2>(yl));
-          mma16816(o[NT - 1], pa, code_pair<3>(xl), code_pair<3>(yl));
-        }
-      }
+      if (k_base + kPage > vis_all)
+        page_step<D, NR, true>(w, st, k_base, rq.kv);
+      else
+        page_step<D, NR, false>(w, st, k_base, rq.kv);
       ++it;
       __syncwarp();                 // every lane has read the page
 #pragma unroll
@@ -468,31 +592,30 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
     __syncthreads();
     if (s_abort) return;            // uniform after the barrier: a wait gave up
     float *mg = reinterpret_cast<float *>(ring);
+    const float vout = w.vref / kWeightScale;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      z[x] += __shfl_xor_sync(0xffffffffu, z[x], 1);
-      z[x] += __shfl_xor_sync(0xffffffffu, z[x], 2);
-      float *row = mg + (n8 + 8 * x) * S::kMergeStride;
+    for (int y = 0; y < 2 * NR; ++y) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int n = 2 * t + e;
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w)
-#pragma unroll
-          for (int j = 0; j < 8; j += 4)
-            *reinterpret_cast<float4 *>(row + 64 * w + 8 * n + j) =
-                make_float4(o[8 * w + j][2 * x + e] + z[x], o[8 * w + j + 1][2 * x + e] + z[x],
-                            o[8 * w + j + 2][2 * x + e] + z[x], o[8 * w + j + 3][2 * x + e] + z[x]);
-        if constexpr (D % 64 != 0)
-          *reinterpret_cast<float4 *>(row + 64 * (D / 64) + 4 * n) =
-              make_float4(o[NT - 4][2 * x + e] + z[x], o[NT - 3][2 * x + e] + z[x],
-                          o[NT - 2][2 * x + e] + z[x], o[NT - 1][2 * x + e] + z[x]);
+      for (int o = 4; o < 32; o <<= 1) {
+        w.l[y] += __shfl_xor_sync(0xffffffffu, w.l[y], o);
+        w.z[y] += __shfl_xor_sync(0xffffffffu, w.z[y], o);
       }
-      if (t == 0) {
-        row[D] = m[x];
-        row[D + 1] = l[x];
+      const int x = y >> 1, e = y & 1;
+      float *row = mg + (8 * x + 2 * t + e) * S::kMergeStride;
+      const float z = w.z[y];
+      auto val = [&](int j, int up) { return fmaf(w.o[x][j][2 * up + e], vout, z); };
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int up = 0; up < 2; ++up)
+          *reinterpret_cast<float4 *>(row + 64 * i + 8 * n8 + 4 * up) =
+              make_float4(val(4 * i, up), val(4 * i + 1, up), val(4 * i + 2, up), val(4 * i + 3, up));
+      if constexpr (D % 64 != 0)
+        *reinterpret_cast<float4 *>(row + 64 * (D / 64) + 4 * n8) =
+            make_float4(val(MT - 2, 0), val(MT - 2, 1), val(MT - 1, 0), val(MT - 1, 1));
+      if (n8 == 0) {
+        row[D] = w.m[y];
+        row[D + 1] = w.l[y];
       }
     }
     __syncthreads();
@@ -603,10 +726,10 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
   }
 }
 
-template <int D, bool LOW>
+template <int D, int NR>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
   constexpr int NS = 2;
-  auto kfn = kv4_attn_kernel<D, LOW, NS>;
+  auto kfn = kv4_attn_kernel<D, NR, NS>;
   constexpr int bytes = Smem<D, NS>::kBytes;
   static std::mutex mu;
   static std::set<int> ready;
@@ -682,7 +805,7 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   switch (d) {
 #define DITANGO_KV4(D)                                                                     \
   case D:                                                                                  \
-    return low ? hattn::launch<D, true>(p, num_sms, stream) : hattn::launch<D, false>(p, num_sms, stream)
+    return low ? hattn::launch<D, 1>(p, num_sms, stream) : hattn::launch<D, 2>(p, num_sms, stream)
     DITANGO_KV4(64);
     DITANGO_KV4(96);
     DITANGO_KV4(128);

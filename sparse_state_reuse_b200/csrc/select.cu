@@ -16,14 +16,14 @@ namespace ditango {
 namespace sel {
 
 // ---------------------------------------------------------------- summaries
-// One block of threads a block of rows, which is all in flight at once (16
-// bytes a load): bound by reading x.  Sums are exact: a lane adds up to four
-// bf16 values in fp32 (24 bits hold them but for values 2^13 times smaller
-// than their neighbours), and goes on in fp64.
+// A block of threads takes 128 rows (one query block or two key blocks), all in
+// flight at once (16 bytes a load): bound by reading x.  Sums are exact: a lane
+// adds up to four bf16 values in fp32 (24 bits hold them but for values 2^13
+// times smaller than their neighbours), and goes on in fp64.
 constexpr int kSumThreads = 256;
 
 struct SummaryParams {
-  int H, N, block, nb;
+  int H, N, nb;
   const uint16_t *x;
   long long sb, sh, sn;
   const int *len;               // [B] valid rows, or null
@@ -36,73 +36,82 @@ template <int D, int BLOCK>
 __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const SummaryParams p) {
   constexpr int kGroup = (D == 64) ? 8 : 16;             // lanes of a row (12 of 16 busy at 96)
   constexpr int kPass = kSumThreads / kGroup;            // rows of one pass
-  constexpr int kLoads = (BLOCK + kPass - 1) / kPass;
+  constexpr int NB = 128 / BLOCK;                        // blocks of this block of threads
+  constexpr int kLoads = BLOCK / kPass;                  // of each of them
   constexpr int kWarps = kSumThreads / 32;
-  __shared__ double part[kWarps][D];
-  __shared__ double s_top[kWarps];
+  __shared__ double part[NB][kWarps][D];
+  __shared__ double s_top[NB][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = tid % kGroup, row = tid / kGroup;
-  const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int blk0 = blockIdx.x * NB, h = blockIdx.y, b = blockIdx.z;
   int len = p.N;
   if (p.len) len = max(0, min(p.N, __ldg(p.len + b)));
-  const int n = max(0, min(BLOCK, len - blk * BLOCK));
+  const int left = len - blk0 * BLOCK;                   // valid rows from here on
   const bool busy = sub < D / 8;
-  const uint16_t *src = p.x + b * p.sb + h * p.sh + (long long)blk * BLOCK * p.sn + sub * 8;
-  uint4 v[kLoads];
+  const uint16_t *src = p.x + b * p.sb + h * p.sh + (long long)blk0 * BLOCK * p.sn + sub * 8;
+  uint4 v[NB * kLoads];
 #pragma unroll
-  for (int a = 0; a < kLoads; ++a) {
+  for (int a = 0; a < NB * kLoads; ++a) {
     const int r = row + a * kPass;
     v[a] = make_uint4(0, 0, 0, 0);
-    if (busy && r < n) v[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * p.sn));
+    if (busy && r < left) v[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * p.sn));
   }
-  double acc[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.0;
+  for (int q = 0; q < NB; ++q) {
+    double acc[8];
 #pragma unroll
-  for (int a = 0; a < kLoads; a += 4) {
-    float f[8];
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = 0.f;
+    for (int a = 0; a < kLoads; a += 4) {
+      float f[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (a + e < kLoads) {
-        const uint4 u = v[a + e];
-        f[0] += bf_lo(u.x); f[1] += bf_hi(u.x); f[2] += bf_lo(u.y); f[3] += bf_hi(u.y);
-        f[4] += bf_lo(u.z); f[5] += bf_hi(u.z); f[6] += bf_lo(u.w); f[7] += bf_hi(u.w);
+      for (int k = 0; k < 8; ++k) f[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (a + e < kLoads) {
+          const uint4 u = v[q * kLoads + a + e];
+          f[0] += bf_lo(u.x); f[1] += bf_hi(u.x); f[2] += bf_lo(u.y); f[3] += bf_hi(u.y);
+          f[4] += bf_lo(u.z); f[5] += bf_hi(u.z); f[6] += bf_lo(u.w); f[7] += bf_hi(u.w);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += (double)f[k];
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] += (double)f[k];
-  }
+    for (int o = kGroup; o < 32; o <<= 1)
 #pragma unroll
-  for (int o = kGroup; o < 32; o <<= 1)
+      for (int k = 0; k < 8; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+    if (lane < kGroup && busy) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
-  if (lane < kGroup && busy) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) part[warp][sub * 8 + k] = acc[k];
+      for (int k = 0; k < 8; ++k) part[q][warp][sub * 8 + k] = acc[k];
+    }
   }
   __syncthreads();
+  // with two blocks, half of the threads each
+  constexpr int kHalf = kSumThreads / NB;
+  const int q = tid / kHalf, ch = tid % kHalf, blk = blk0 + q;
+  const int n = max(0, min(BLOCK, left - q * BLOCK));
   double s = 0.0;
-  if (tid < D) {
+  if (ch < D) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][tid];
+    for (int w = 0; w < kWarps; ++w) s += part[q][w][ch];
   }
   double top = isfinite(s) ? fabs(s) : (double)INFINITY;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_top[warp] = top;
+  if (lane == 0) s_top[q][warp % (kWarps / NB)] = top;
   __syncthreads();
-  top = s_top[0];
+  top = s_top[q][0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) top = fmax(top, s_top[w]);
+  for (int w = 1; w < kWarps / NB; ++w) top = fmax(top, s_top[q][w]);
+  if (blk >= p.nb) return;
   const size_t at = ((size_t)b * p.H + h) * p.nb + blk;
   const bool good = top > 0.0 && top < (double)INFINITY;   // else (a value is not finite): score 0
-  if (tid < D) {
-    p.codes[at * D + tid] = good ? (signed char)(int)rint(s * 127.0 / top) : (signed char)0;
-    if (p.mean) p.mean[at * D + tid] = n > 0 ? (float)(s / (double)n) : 0.f;
+  if (ch < D) {
+    p.codes[at * D + ch] = good ? (signed char)(int)rint(s * 127.0 / top) : (signed char)0;
+    if (p.mean) p.mean[at * D + ch] = n > 0 ? (float)(s / (double)n) : 0.f;
   }
-  if (tid == 0) p.scale[at] = good ? (float)(top / (127.0 * n)) : 0.f;
+  if (ch == 0) p.scale[at] = good ? (float)(top / (127.0 * n)) : 0.f;
 }
 
 // ---------------------------------------------------------------- selection
@@ -110,11 +119,11 @@ constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 
 struct SelectParams {
-  int Hkv, G, n_q, n_k, max_blocks, n_pages, k, band, sink, room, rows;
+  int Hkv, G, n_q, n_k, n_pages, k, band, sink, room, rows;
   int own;                      // key blocks of a query block; 0: the query stands at the end
   const signed char *qc, *kc;
   const float *qs, *ks;
-  const int *block_table;       // [B, max_blocks] or null
+  const int *block_table;       // [B, n_k] or null
   const int *k_len;             // [B] tokens, or null
   int *sel, *count, *dev_status;
 };
@@ -136,19 +145,109 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 constexpr uint32_t kForced = 0xffffffffu;
 
-// One block of threads: up to 16 query blocks of one key head.  The scores of
-// all key blocks stand in shared memory; each warp then finds the threshold of
-// its rows by bisection between the least and greatest score (it ends as soon
-// as the count is met, after 12 to 14 steps on a thousand different scores)
-// and writes the list in ascending order.
-template <int D>
+// Warp-wide choice of one row: the threshold between what is taken and what is
+// not, by bisection between the least and greatest score that ends as soon as
+// the count is met (12 to 14 steps on a thousand different scores), then the
+// list in ascending order.  REG > 0: the row (at most 32 REG entries) stays in
+// registers; 0: it is read from shared memory in every step.
+template <int REG>
+__device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, int room, int *dst, int *count) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[REG > 0 ? REG : 1];
+  int n_forced = 0;
+  uint32_t least = kForced, most = 0;
+  auto look = [&](uint32_t x) {
+    if (x == kForced) {
+      ++n_forced;
+    } else if (x != 0u) {
+      least = min(least, x);
+      most = max(most, x);
+    }
+  };
+  if constexpr (REG > 0) {
+#pragma unroll
+    for (int a = 0; a < REG; ++a) {
+      const int j = a * 32 + lane;
+      v[a] = j < nk ? key[j] : 0u;      // 0: no entry
+      look(v[a]);
+    }
+  } else {
+    for (int j = lane; j < nk; j += 32) look(key[j]);
+  }
+  n_forced = __reduce_add_sync(0xffffffffu, n_forced);
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  const int need = min(nk, max(n_forced, k));
+  // entries above `above` are taken, and the first `ties` of those equal to it
+  uint32_t above = 0;
+  int ties = 0;
+  if (need == n_forced) {
+    above = kForced - 1;
+  } else if (need < nk) {
+    // at least `need` entries are >= lo, fewer are >= hi
+    uint32_t lo = least, hi = most + 1;
+    int at_hi = n_forced;
+    bool met = false;
+    while (hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      int c = 0;
+      if constexpr (REG > 0) {
+#pragma unroll
+        for (int a = 0; a < REG; ++a) c += v[a] >= mid;
+      } else {
+        for (int j = lane; j < nk; j += 32) c += key[j] >= mid;
+      }
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c == need) {
+        above = mid - 1;
+        met = true;
+        break;
+      }
+      if (c > need) {
+        lo = mid;
+      } else {
+        hi = mid;
+        at_hi = c;
+      }
+    }
+    if (!met) {
+      above = lo;
+      ties = need - at_hi;
+    }
+  }
+  int out = 0;
+  auto emit = [&](int j, uint32_t x) {
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, ties > 0 && x == above);
+    const bool take = x > above || (((eq >> lane) & 1u) && __popc(eq & below) < ties);
+    const uint32_t got = __ballot_sync(0xffffffffu, take);
+    const int at = out + __popc(got & below);
+    if (take && at < room) dst[at] = j;
+    out += __popc(got);
+    ties -= min(ties, __popc(eq));
+  };
+  if constexpr (REG > 0) {
+#pragma unroll
+    for (int a = 0; a < REG; ++a) emit(a * 32 + lane, v[a]);
+  } else {
+    for (int j0 = 0; j0 < nk; j0 += 32) emit(j0 + lane, j0 + lane < nk ? key[j0 + lane] : 0u);
+  }
+  for (int j = out + lane; j < room; j += 32) dst[j] = -1;
+  if (lane == 0) *count = min(out, room);
+}
+
+// One block of threads: up to 16 query blocks of one key head, whose scores of
+// all key blocks stand in shared memory.  HEADS: a single query block, and the
+// 16 rows of the product are the query heads of the key head instead, so that
+// the key codes are read once and not once a head.
+template <int D, int REG, bool HEADS>
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int KS = D / 32;
   extern __shared__ uint32_t score[];        // [rows][n_k] (fp32 sums, then their order)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = lane & 3, n8 = lane >> 2;
-  const int i0 = blockIdx.x * p.rows, h = blockIdx.y, b = blockIdx.z;
-  const int rows = min(p.rows, p.n_q - i0);
+  const int i0 = HEADS ? 0 : blockIdx.x * p.rows, h = blockIdx.y, b = blockIdx.z;
+  const int rows = HEADS ? p.G : min(p.rows, p.n_q - i0);
   int nk = p.n_k;
   if (p.k_len) {
     const long long len = __ldg(p.k_len + b);
@@ -165,15 +264,26 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
     const int f = p.own ? i * p.own : nk - 1, l = p.own ? f + p.own - 1 : nk - 1;
     return j >= f - p.band && j <= l + p.band;
   };
-  for (int g = 0; g < p.G; ++g) {
-    const int head = h * p.G + g;
+  auto page_of = [&](int j) -> int {         // -1: a page number out of range, which scores 0
+    const int page = __ldg(p.block_table + (size_t)b * p.n_k + j);
+    if (page >= 0 && page < p.n_pages) return page;
+    set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+    return -1;
+  };
+  auto scale_of = [&](int j) -> float {
+    if (!p.block_table) return __ldg(p.ks + ((size_t)b * p.Hkv + h) * p.n_k + j);
+    const int page = page_of(j);
+    return page < 0 ? 0.f : __ldg(p.ks + (size_t)page * p.Hkv + h);
+  };
+  for (int g = 0; g < (HEADS ? 1 : p.G); ++g) {
     uint32_t a[KS][4];
     float qs[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int row = n8 + 8 * x;
       const bool live = row < rows;
-      const size_t at = ((size_t)b * p.Hkv * p.G + head) * p.n_q + i0 + (live ? row : 0);
+      const size_t at = HEADS ? ((size_t)b * p.Hkv + h) * p.G + (live ? row : 0)
+                              : (((size_t)b * p.Hkv + h) * p.G + g) * p.n_q + i0 + (live ? row : 0);
       qs[x] = live ? __ldg(p.qs + at) : 0.f;
       const uint2 *src = reinterpret_cast<const uint2 *>(p.qc + at * D + t * (D / 4));
 #pragma unroll
@@ -186,25 +296,24 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
     constexpr int kAhead = 4;      // key tiles in flight
     for (int u0 = warp; u0 < tiles; u0 += kSelWarps * kAhead) {
       uint2 kb[kAhead][KS];
+      const signed char *src[kAhead];
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         const int j = (u0 + e * kSelWarps) * 8 + n8;
-        const signed char *src = nullptr;
-        if (j < nk) {
-          if (p.block_table) {
-            const int page = __ldg(p.block_table + (size_t)b * p.max_blocks + j);
-            if (page >= 0 && page < p.n_pages)
-              src = p.kc + ((size_t)page * p.Hkv + h) * D;
-            else
-              set_status(p.dev_status, DITANGO_ERR_BOUNDS);
-          } else {
-            src = p.kc + (((size_t)b * p.Hkv + h) * p.n_k + j) * D;
-          }
+        src[e] = nullptr;
+        if (j >= nk) continue;
+        if (p.block_table) {
+          const int page = page_of(j);
+          if (page >= 0) src[e] = p.kc + ((size_t)page * p.Hkv + h) * D;
+        } else {
+          src[e] = p.kc + (((size_t)b * p.Hkv + h) * p.n_k + j) * D;
         }
+      }
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-          kb[e][s] = src ? __ldg(reinterpret_cast<const uint2 *>(src + t * (D / 4)) + s) : make_uint2(0, 0);
-      }
+          kb[e][s] = src[e] ? __ldg(reinterpret_cast<const uint2 *>(src[e] + t * (D / 4)) + s) : make_uint2(0, 0);
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         const int u = u0 + e * kSelWarps;
@@ -218,96 +327,35 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
           if (row >= rows || j >= nk) continue;
           uint32_t *dst = score + (size_t)row * p.n_k + j;
           float x = __fmul_rn(qs[q >> 1], (float)c[q]);
-          if (g > 0) x = __fadd_rn(__uint_as_float(*dst), x);
-          if (g + 1 < p.G) {
+          if (!HEADS && g > 0) x = __fadd_rn(__uint_as_float(*dst), x);
+          if (HEADS || g + 1 < p.G)
             *dst = __float_as_uint(x);
-          } else if (forced(i0 + row, j)) {
-            *dst = kForced;
-          } else {
-            float ks;
-            if (p.block_table) {
-              const int page = __ldg(p.block_table + (size_t)b * p.max_blocks + j);
-              ks = (page >= 0 && page < p.n_pages) ? __ldg(p.ks + (size_t)page * p.Hkv + h) : 0.f;
-            } else {
-              ks = __ldg(p.ks + ((size_t)b * p.Hkv + h) * p.n_k + j);
-            }
-            *dst = order_of(__fmul_rn(x, ks));
-          }
+          else
+            *dst = forced(i0 + row, j) ? kForced : order_of(__fmul_rn(x, scale_of(j)));
         }
       }
     }
   }
   __syncthreads();
-  for (int row = warp; row < rows; row += kSelWarps) {
-    const uint32_t *key = score + (size_t)row * p.n_k;
-    int n_forced = 0;
-    uint32_t least = kForced, most = 0;
-    for (int j = lane; j < nk; j += 32) {
-      const uint32_t v = key[j];
-      if (v == kForced) {
-        ++n_forced;
-      } else {
-        least = min(least, v);
-        most = max(most, v);
-      }
+  if constexpr (HEADS) {
+    for (int j = tid; j < nk; j += kSelThreads) {
+      float x = __uint_as_float(score[j]);
+      for (int g = 1; g < rows; ++g) x = __fadd_rn(x, __uint_as_float(score[(size_t)g * p.n_k + j]));
+      score[j] = forced(0, j) ? kForced : order_of(__fmul_rn(x, scale_of(j)));
     }
-    n_forced = __reduce_add_sync(0xffffffffu, n_forced);
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
-    const int need = min(nk, max(n_forced, p.k));
-    // entries above `above` are taken, and the first `ties` of those equal to it
-    uint32_t above = 0;
-    int ties = 0;
-    if (need == n_forced) {
-      above = kForced - 1;
-    } else if (need < nk) {
-      // lo: at least `need` entries are >= lo; hi: fewer are >= hi
-      uint32_t lo = least, hi = most + 1;
-      int at_hi = n_forced;
-      bool met = false;
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        int c = 0;
-        for (int j = lane; j < nk; j += 32) c += key[j] >= mid;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (c == need) {
-          above = mid - 1;
-          met = true;
-          break;
-        }
-        if (c > need) lo = mid;
-        else {
-          hi = mid;
-          at_hi = c;
-        }
-      }
-      if (!met) {
-        above = lo;
-        ties = need - at_hi;
-      }
-    }
-    int *dst = p.sel + (((size_t)b * p.Hkv + h) * p.n_q + i0 + row) * p.room;
-    int out = 0;
-    for (int j0 = 0; j0 < nk; j0 += 32) {
-      const int j = j0 + lane;
-      const uint32_t v = j < nk ? key[j] : 0u;
-      const uint32_t eq = __ballot_sync(0xffffffffu, j < nk && v == above && ties > 0);
-      const bool tie = ((eq >> lane) & 1u) && __popc(eq & ((1u << lane) - 1u)) < ties;
-      const bool take = (j < nk && v > above) || tie;
-      const uint32_t got = __ballot_sync(0xffffffffu, take);
-      const int at = out + __popc(got & ((1u << lane) - 1u));
-      if (take && at < p.room) dst[at] = j;
-      out += __popc(got);
-      ties -= min(ties, __popc(eq));
-    }
-    for (int j = out + lane; j < p.room; j += 32) dst[j] = -1;
-    if (lane == 0) p.count[((size_t)b * p.Hkv + h) * p.n_q + i0 + row] = min(out, p.room);
+    __syncthreads();
+  }
+  for (int row = warp; row < (HEADS ? 1 : rows); row += kSelWarps) {
+    const size_t at = ((size_t)b * p.Hkv + h) * p.n_q + i0 + row;
+    choose_row<REG>(score + (size_t)row * p.n_k, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
   }
 }
 
-template <int D>
+constexpr int kMaxScoreBytes = 200 * 1024;
+
+template <int D, int REG, bool HEADS>
 cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t stream) {
-  auto kfn = block_select_kernel<D>;
+  auto kfn = block_select_kernel<D, REG, HEADS>;
   static std::mutex mu;
   static std::set<int> ready;
   int dev = 0;
@@ -316,26 +364,35 @@ cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t 
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready.count(dev)) {
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxScoreBytes);
       if (e != cudaSuccess) return e;
       ready.insert(dev);
     }
   }
-  const dim3 grid((unsigned)((p.n_q + p.rows - 1) / p.rows), (unsigned)p.Hkv, (unsigned)B);
+  const dim3 grid((unsigned)(HEADS ? 1 : (p.n_q + p.rows - 1) / p.rows), (unsigned)p.Hkv, (unsigned)B);
   kfn<<<grid, kSelThreads, bytes, stream>>>(p);
   return cudaGetLastError();
+}
+
+// The row in registers up to 1536 entries (98304 tokens), in 16 or 48 of them a
+// lane; a longer one is read from shared memory.
+template <int D, bool HEADS>
+cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t stream) {
+  if (p.n_k <= 32 * 16) return launch_select<D, 16, HEADS>(p, B, bytes, stream);
+  if (p.n_k <= 32 * 48) return launch_select<D, 48, HEADS>(p, B, bytes, stream);
+  return launch_select<D, 0, HEADS>(p, B, bytes, stream);
 }
 
 }  // namespace sel
 
 // Most key blocks of a selection: one row of scores in shared memory.
-int select_max_blocks() { return 200 * 1024 / 4; }
+int select_max_blocks() { return sel::kMaxScoreBytes / 4; }
 
 cudaError_t launch_block_summary(int B, int H, int N, int d, int block, const uint16_t *x, const int64_t *s,
                                  const int *len, signed char *codes, float *scale, float *mean,
                                  cudaStream_t stream) {
-  sel::SummaryParams p{H, N, block, (N + block - 1) / block, x, s[0], s[1], s[2], len, codes, scale, mean};
-  const dim3 grid((unsigned)p.nb, (unsigned)H, (unsigned)B);
+  sel::SummaryParams p{H, N, (N + block - 1) / block, x, s[0], s[1], s[2], len, codes, scale, mean};
+  const dim3 grid((unsigned)((N + kQBlock - 1) / kQBlock), (unsigned)H, (unsigned)B);
 #define DITANGO_SUM(D)                                                                              \
   case D:                                                                                           \
     if (block == kPage)                                                                             \
@@ -363,7 +420,6 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
   p.G = H / Hkv;
   p.n_q = n_q;
   p.n_k = n_k;
-  p.max_blocks = n_k;
   p.n_pages = n_pages;
   p.k = k;
   p.band = band;
@@ -382,12 +438,18 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
   // as many query blocks as the scores leave room for, 16 (one product) at most
   int rows = 16;
   while (rows > 1 && (rows / 2 >= n_q || (long long)rows * n_k * 4 > 100 * 1024)) rows /= 2;
+  const bool heads = n_q == 1 && p.G <= 16 && (long long)p.G * n_k * 4 <= sel::kMaxScoreBytes;
   p.rows = rows;
-  const int bytes = rows * n_k * 4;
+  const int bytes = (heads ? p.G : rows) * n_k * 4;
   switch (d) {
-    case 64: return sel::launch_select<64>(p, B, bytes, stream);
-    case 96: return sel::launch_select<96>(p, B, bytes, stream);
-    case 128: return sel::launch_select<128>(p, B, bytes, stream);
+#define DITANGO_SEL(D)                                                     \
+  case D:                                                                  \
+    return heads ? sel::launch_select<D, true>(p, B, bytes, stream)        \
+                 : sel::launch_select<D, false>(p, B, bytes, stream)
+    DITANGO_SEL(64);
+    DITANGO_SEL(96);
+    DITANGO_SEL(128);
+#undef DITANGO_SEL
     default: return cudaErrorInvalidValue;
   }
 }
