@@ -20,8 +20,9 @@ CSRC = os.path.join(HERE, "csrc")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libditango.so")
 SOURCES = ["ditango_api.cu", "attn_partial.cu", "plan.cu", "merge.cu", "selftest.cu",
-           "history.cu", "history_attn.cu", "select.cu", "block_attn.cu"]
-HEADERS = ["common.cuh", "weights.cuh", "blocks.cuh"]
+           "history.cu", "history_attn.cu", "history_chunk.cu",
+           "select.cu", "block_attn.cu"]
+HEADERS = ["common.cuh", "weights.cuh", "blocks.cuh", "history_attn.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [

@@ -36,7 +36,6 @@ constexpr int kLaunchRegs = 128;     // 65536 / (2 * 256)
 // block is launched with: 128 * 200 + 128 * 56 = 256 * 128.
 constexpr int kSoftmaxRegs = 200, kControlRegs = 56;
 static_assert(128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
-constexpr float kRescaleLog2 = 8.0f;
 constexpr int kTmemCols = 256;
 
 template <int D>
@@ -321,7 +320,13 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
     }
     const float neg = m_used > -INFINITY ? -m_used : 0.f;   // no key so far: exponentiate against 0
-    const uint64_t sl2x2 = f2(sl2, sl2), negx2 = f2(neg, neg);
+    uint64_t sl2x2 = f2(sl2, sl2);
+    const uint64_t negx2 = f2(neg, neg);
+    if (__any_sync(0xffffffffu, fabsf(neg) > kHuge)) {
+#pragma unroll
+      for (int c = 0; c < BN; ++c) sv[c] = __float_as_uint(__fmul_rn(__uint_as_float(sv[c]), sl2));
+      sl2x2 = f2(1.f, 1.f);
+    }
     uint64_t lsum0 = 0, lsum1 = 0;
 #pragma unroll
     for (int g8 = 0; g8 < BN / 16; ++g8) {

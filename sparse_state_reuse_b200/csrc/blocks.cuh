@@ -41,6 +41,13 @@ struct FastDiv {
 
 #ifdef __CUDACC__
 
+// A running maximum is left as it is until it grew by more than 2^8.
+constexpr float kRescaleLog2 = 8.0f;
+// p = 2^(x mul - m) is formed by one FMA, which does not round x mul as m was
+// rounded: past this size of m the difference could reach 1 and more (an
+// overflow), and x mul is rounded first, in a path of its own.
+constexpr float kHuge = 1048576.0f;   // 2^20: at most 2^-4 off
+
 __device__ __forceinline__ void set_status(int *dev_status, int code) {
   if (dev_status) atomicExch(dev_status, code);
 }

@@ -25,18 +25,11 @@
 // it; no block-wide barrier until the end of a range.  With so few rows the
 // legacy tensor instructions are not what bounds it (30% of their rate), and a
 // tcgen05 tile of 128 rows would be mostly padding.
-//
-// Work split: the pages of all (request, key head, row tile) items are one
-// line of work that is cut into equal ranges, one a block, so that a single
-// long request and a ragged batch fill the GPU alike.  An item cut by a
-// boundary is joined by the block that finishes it last, from the partial
-// states in block order (a fixed order: the result does not depend on which
-// block is last).
 #include <mutex>
 #include <set>
 #include <utility>
 
-#include "blocks.cuh"
+#include "history_attn.cuh"
 
 namespace ditango {
 namespace hattn {
@@ -45,29 +38,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // rows of a tile, at most
 constexpr int kMaxBlocks = 768;      // most blocks of a launch (the workspace has room for them)
-constexpr float kRescaleLog2 = 8.0f;
 // p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
 // 2^6 more uses the range that is left.
 constexpr float kWeightScale = 64.f;
-
-struct Params {
-  int R, H, Hkv, G, T, max_blocks, n_pages, max_sel, causal;
-  const uint16_t *Q;
-  long long qt, qh;                  // token and head strides
-  const int *q_off, *kv_len, *block_table, *sel, *sel_count;
-  const uint8_t *data;
-  float scale_log2;
-  void *out;
-  int out_fp32;
-  long long ot, oh;
-  float *out_lse;
-  long long lt, lh;
-  float *partial;                    // [2 * kMaxBlocks][kRows * (d + 2)]
-  int *counters;                     // [kMaxBlocks]
-  int max_rows;                      // requests of more rows are left to the other kernel
-  int *dev_status;
-  long long wait_limit_ns;
-};
 
 // Key of row n of an 8-key tile.  The order within a tile is free (scores and
 // values use the same); this one spreads the rows that a warp reads at once
@@ -88,79 +61,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-// Codes i and i + 4 of a word, i = 0..3, less 8, as fp16 pairs.
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&pair)[4]) {
-  const uint32_t kOne = 0x3c003c00u, k16th = 0x2c002c00u;            // 1, 1/16
-  const uint32_t kEven = 0xe408e408u, kOdd = 0xd480d480u;            // -1032, -72
-  const uint32_t v = w >> 8;
-  pair[0] = hfma2((w & 0x000f000fu) | 0x64006400u, kOne, kEven);     // 1024 + c
-  pair[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, k16th, kOdd);     // 1024 + 16 c
-  pair[2] = hfma2((v & 0x000f000fu) | 0x64006400u, kOne, kEven);
-  pair[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, k16th, kOdd);
-}
-
-struct Request {
-  int n_q, kv, q0, tiles, pages;   // pages: work units of one item, at least 1
-};
-
-template <int TR>
-__device__ __forceinline__ Request request_of(const Params &p, int r) {
-  Request q;
-  q.q0 = __ldg(p.q_off + r);
-  const int q1 = __ldg(p.q_off + r + 1);
-  q.kv = __ldg(p.kv_len + r);
-  const long long most = (long long)p.max_blocks * kPage;
-  q.n_q = q1 - q.q0;
-  if (q.q0 < 0 || q1 < q.q0 || q1 > p.T || q.kv < 0 || q.kv > most) {
-    set_status(p.dev_status, DITANGO_ERR_BOUNDS);
-    q.kv = (int)max(0LL, min((long long)q.kv, most));
-    if (q.q0 < 0 || q1 < q.q0 || q1 > p.T) q.n_q = 0;
-  }
-  const long long rows = (long long)q.n_q * p.G;
-  q.tiles = rows > p.max_rows ? 0 : (int)((rows + TR - 1) / TR);
-  q.pages = p.sel ? p.max_sel : (q.kv + kPage - 1) / kPage;
-  if (q.pages < 1) q.pages = 1;
-  return q;
-}
-
-__device__ __forceinline__ long long work_of(const Params &p, const Request &q) {
-  return (long long)q.tiles * p.Hkv * q.pages;
-}
-
-// Sum and exclusive prefix over the block.
-__device__ __forceinline__ long long block_scan(long long v, long long &total, long long *sm) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) sm[warp] = x;
-  __syncthreads();
-  total = 0;
-  long long before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm[w];
-    total += sm[w];
-  }
-  return before + x - v;
 }
 
 template <int D, int NS>
@@ -299,9 +199,25 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const uint8_t *st,
       }
     }
   }
-  float neg[2 * NR];
+  float neg[2 * NR], mul[2 * NR];
+  bool huge = false;
 #pragma unroll
-  for (int y = 0; y < 2 * NR; ++y) neg[y] = w.m[y] > -INFINITY ? -w.m[y] : 0.f;   // no key so far: against 0
+  for (int y = 0; y < 2 * NR; ++y) {
+    neg[y] = w.m[y] > -INFINITY ? -w.m[y] : 0.f;   // no key so far: against 0
+    mul[y] = w.mul[y];
+    huge = huge || fabsf(neg[y]) > kHuge;
+  }
+  if (__any_sync(0xffffffffu, huge)) {
+#pragma unroll
+    for (int y = 0; y < 2 * NR; ++y) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sc[u][y >> 1][y & 1] = __fmul_rn(sc[u][y >> 1][y & 1], mul[y]);
+        sc[u][y >> 1][2 + (y & 1)] = __fmul_rn(sc[u][y >> 1][2 + (y & 1)], mul[y]);
+      }
+      mul[y] = 1.f;
+    }
+  }
   const float vs = kWeightScale / w.vref;
   // 16 keys at a time: p, the weights p s', and the second product
 #pragma unroll
@@ -318,7 +234,7 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const uint8_t *st,
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int y = 2 * x + (q & 1);
-        e[q] = fast_ex2(fmaf(sc[u][x][q], w.mul[y], neg[y]));
+        e[q] = fast_ex2(fmaf(sc[u][x][q], mul[y], neg[y]));
         g[q] = e[q] * (q < 2 ? wa : wb);
         float c = e[q] * (q < 2 ? ha : hb);
         if constexpr (MASKED) {       // a masked token's scale may be anything
@@ -383,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   constexpr int TR = 8 * NR;         // rows of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) unsigned long long bars[kWarps][NS];
-  __shared__ long long s_scan[kWarps], s_before;
+  __shared__ long long s_scan[kWarps + 1];
   __shared__ int s_request, s_abort, s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -397,37 +313,8 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
     fence_barrier_init();
   }
 
-  // this block's range [w0, w1) of the line of work
-  long long total = 0;
-  for (int base = 0; base < p.R; base += kThreads) {
-    const int r = base + tid;
-    long long sum;
-    block_scan(r < p.R ? work_of(p, request_of<TR>(p, r)) : 0, sum, s_scan);
-    total += sum;
-  }
-  const long long n_blk = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-  if ((long long)blockIdx.x >= n_blk) return;
-  const long long w0 = total * blockIdx.x / n_blk, w1 = total * (blockIdx.x + 1) / n_blk;
-  {
-    long long before = 0;
-    for (int base = 0; base < p.R; base += kThreads) {
-      const int r = base + tid;
-      const long long v = r < p.R ? work_of(p, request_of<TR>(p, r)) : 0;
-      long long sum;
-      const long long at = before + block_scan(v, sum, s_scan);
-      if (v > 0 && at <= w0 && w0 < at + v) {
-        s_request = r;
-        s_before = at;
-      }
-      before += sum;
-      if (before > w0) break;       // uniform: every thread has the same sum
-    }
-    __syncthreads();
-  }
-  int r = s_request;
-  long long r_start = s_before;
-  if (r < 0) return;                // cannot happen: w0 < total
-  Request rq = request_of<TR>(p, r);
+  Range g;
+  if (!find_range<TR, 1, kThreads>(p, 1, g, s_scan, &s_request)) return;
 
   uint8_t *ring = smem + warp * S::kWarpBytes;
   const uint32_t ring_s = smem_u32(ring);
@@ -435,25 +322,15 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   uint32_t it = 0;                  // pages this warp has consumed (ring position and phase)
   bool ok = true;
 
-  for (long long pos = w0; pos < w1;) {
-    while (pos >= r_start + work_of(p, rq)) {
-      r_start += work_of(p, rq);
-      ++r;
-      rq = request_of<TR>(p, r);
-    }
-    // the segment: pages [p0, p1) of one item
-    const long long item = (pos - r_start) / rq.pages;
-    const long long item_start = r_start + item * rq.pages;
-    const int p0 = (int)(pos - item_start);
-    const int p1 = (int)(w1 - item_start < rq.pages ? w1 - item_start : rq.pages);
-    const int tile = (int)(item / p.Hkv), h = (int)(item % p.Hkv);
-    const int row0 = tile * TR;
+  Walk<TR, 1> walk;
+  walk.start(p, g);
+  Segment sg;
+  while (walk.next(p, sg)) {
+    const Request rq = sg.rq;
+    const int h = sg.h, row0 = sg.tile * TR;
     const int rows = min(TR, rq.n_q * p.G - row0);
-    const int *table = p.block_table + (size_t)r * p.max_blocks;
-    const int *sel = p.sel ? p.sel + ((size_t)r * p.Hkv + h) * p.max_sel : nullptr;
-    const int n_list = sel ? max(0, min(p.max_sel, __ldg(p.sel_count + (size_t)r * p.Hkv + h)))
-                           : (rq.kv + kPage - 1) / kPage;
-    const int end = min(p1, n_list);
+    const Pages pages(p, sg);
+    const int end = min(sg.u1, pages.n);
 
     WT w;
     // Q: the lane holds row n8 (+ 8) as the second operand, channels in the
@@ -470,9 +347,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       for (int i = 0; i < W; ++i) {
         u[i] = make_uint4(0, 0, 0, 0);
         if (live) u[i] = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf_lo(v[e])), fabsf(bf_hi(v[e]))));
+        big = fmaxf(big, max_abs8(u[i]));
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -481,19 +356,12 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[2 * e] = bf_lo(v[e]) * down;
-          f[2 * e + 1] = bf_hi(v[e]) * down;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += f[e];
-        w.q[x][2 * i][0] = pack_f16x2(f[0], f[4]);
-        w.q[x][2 * i][1] = pack_f16x2(f[1], f[5]);
-        w.q[x][2 * i + 1][0] = pack_f16x2(f[2], f[6]);
-        w.q[x][2 * i + 1][1] = pack_f16x2(f[3], f[7]);
+        uint32_t pair[4];
+        q_pairs(u[i], down, pair, sum);
+        w.q[x][2 * i][0] = pair[0];
+        w.q[x][2 * i][1] = pair[1];
+        w.q[x][2 * i + 1][0] = pair[2];
+        w.q[x][2 * i + 1][1] = pair[3];
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -525,23 +393,16 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
                   S::kStage, bar);
       }
     };
-    // The next page of this warp and its block, -1 at the end.  Blocks without
-    // tokens are passed over, block and page numbers out of range recorded.
+    // the next page of this warp and its block, -1 at the end
     auto next_page = [&](int &i, int &blk) -> int {
       while (i < end) {
-        blk = sel ? __ldg(sel + i) : i;
+        const int page = pages.page(i, blk, lane == 0);
         i += kWarps;
-        bool bad = blk < 0 || blk >= p.max_blocks;
-        if (!bad && blk * kPage < rq.kv) {
-          const int page = __ldg(table + blk);
-          if (page >= 0 && page < p.n_pages) return page;
-          bad = true;
-        }
-        if (bad && lane == 0) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+        if (page >= 0) return page;
       }
       return -1;
     };
-    int li = p0 + warp;
+    int li = sg.u0 + warp;
     int blk[NS];                    // blocks in flight, oldest first; -1: none
     uint32_t issued = it;
 #pragma unroll
@@ -661,9 +522,8 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       }
       return v;
     };
-    const bool whole = p0 == 0 && p1 == rq.pages;
     constexpr int kVec = D / 4;
-    if (whole) {
+    if (sg.whole()) {
       for (int i = tid; i < rows * kVec; i += kThreads) {
         float mt_, lt_;
         const float4 v = joined(i / kVec, (i % kVec) * 4, mt_, lt_);
@@ -673,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       // a part: the block whose range begins inside the item uses its first
       // slot, the one in whose range the item begins its second
       constexpr int kSlot = kRows * (D + 2);
-      float *mine = p.partial + ((size_t)blockIdx.x * 2 + (p0 == 0 ? 1 : 0)) * kSlot;
+      float *mine = p.partial + ((size_t)blockIdx.x * 2 + (sg.u0 == 0 ? 1 : 0)) * kSlot;
       for (int i = tid; i < rows * kVec; i += kThreads) {
         const int row = i / kVec, ch = (i % kVec) * 4;
         float mt_, lt_;
@@ -686,10 +546,8 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
           mine[row * (D + 2) + D + 1] = lt_;
         }
       }
-      // first block boundary inside the item, and the last block that shares it
-      const long long iend = item_start + rq.pages;
-      const long long c1 = ((item_start + 1) * n_blk + total - 1) / total;
-      const long long cl = (iend * n_blk + total - 1) / total - 1;
+      long long c1, cl;
+      sharers(g, sg, c1, cl);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -722,7 +580,6 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
     }
     fence_proxy_async();            // the ring was written by stores; copies follow
     __syncthreads();
-    pos = item_start + p1;
   }
 }
 
@@ -758,8 +615,15 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
 
 }  // namespace hattn
 
+// Parts of items (either kernel's) and then both kernels' counters.
+static size_t partial_floats(int d) {
+  const size_t few = (size_t)hattn::kMaxBlocks * 2 * hattn::kRows * (d + 2);
+  const size_t many = kv4_chunk_partial_floats(d);
+  return few > many ? few : many;
+}
+
 size_t kv4_attn_workspace_bytes(int d) {
-  return (size_t)hattn::kMaxBlocks * (2 * hattn::kRows * (size_t)(d + 2) * sizeof(float) + sizeof(int));
+  return partial_floats(d) * sizeof(float) + (hattn::kMaxBlocks + kv4_chunk_blocks()) * sizeof(int);
 }
 
 cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int max_blocks, int n_pages,
@@ -797,22 +661,32 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   p.lt = lse_strides[0];
   p.lh = lse_strides[1];
   p.partial = static_cast<float *>(workspace);
-  p.counters = reinterpret_cast<int *>(p.partial + (size_t)hattn::kMaxBlocks * 2 * hattn::kRows * (d + 2));
-  p.max_rows = 0x7fffffff;
+  p.counters = reinterpret_cast<int *>(p.partial + partial_floats(d));
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
-  const bool low = (long long)max_q * p.G <= 8;
+  // Up to 16 rows of a key head go to the kernel of few rows, more to the one
+  // of tcgen05 tiles of 128 rows.
+  const long long most = (long long)max_q * p.G;
+  p.min_rows = 0;
+  p.max_rows = most > hattn::kRows ? hattn::kRows : 0x7fffffffffffLL;
+  const bool low = most <= 8;
+  cudaError_t e = cudaErrorInvalidValue;
   switch (d) {
-#define DITANGO_KV4(D)                                                                     \
-  case D:                                                                                  \
-    return low ? hattn::launch<D, 1>(p, num_sms, stream) : hattn::launch<D, 2>(p, num_sms, stream)
+#define DITANGO_KV4(D)                                                                                \
+  case D:                                                                                             \
+    e = low ? hattn::launch<D, 1>(p, num_sms, stream) : hattn::launch<D, 2>(p, num_sms, stream);      \
+    break
     DITANGO_KV4(64);
     DITANGO_KV4(96);
     DITANGO_KV4(128);
 #undef DITANGO_KV4
-    default:
-      return cudaErrorInvalidValue;
+    default: break;
   }
+  if (e != cudaSuccess || most <= hattn::kRows) return e;
+  p.min_rows = hattn::kRows + 1;
+  p.max_rows = 0x7fffffffffffLL;
+  p.counters += hattn::kMaxBlocks;
+  return launch_kv4_chunk(p, d, num_sms, stream);
 }
 
 }  // namespace ditango

@@ -1,0 +1,263 @@
+// What the two kernels of attention over the 4-bit history share: their
+// parameters and the line of work.
+//
+// The units (runs of pages) of all (request, row tile, key head) items are one
+// line of work that is cut into equal ranges, one a block, so that a single
+// long request and a ragged batch fill the GPU alike.  An item cut by a
+// boundary is joined by the block that finishes it last, from the partial
+// states in block order (a fixed order: the result does not depend on which
+// block is last).
+#pragma once
+
+#include "blocks.cuh"
+
+namespace ditango {
+namespace hattn {
+
+struct Params {
+  int R, H, Hkv, G, T, max_blocks, n_pages, max_sel, causal;
+  const uint16_t *Q;
+  long long qt, qh;                  // token and head strides
+  const int *q_off, *kv_len, *block_table, *sel, *sel_count;
+  const uint8_t *data;
+  float scale_log2;
+  void *out;
+  int out_fp32;
+  long long ot, oh;
+  float *out_lse;
+  long long lt, lh;
+  float *partial;                    // two parts of items a block
+  int *counters;                     // one a block, all zero between launches
+  long long min_rows, max_rows;      // requests of fewer or more rows are left to the other kernel
+  int *dev_status;
+  long long wait_limit_ns;
+};
+
+struct Request {
+  int n_q, kv, q0, tiles, units;   // units: work of one item, at least 1
+};
+
+// Request r in row tiles of TR rows and units of UNIT pages.  Offsets and lengths
+// that cannot be are recorded and clipped.
+template <int TR, int UNIT>
+__device__ __forceinline__ Request request_of(const Params &p, int r) {
+  Request q;
+  q.q0 = __ldg(p.q_off + r);
+  const int q1 = __ldg(p.q_off + r + 1);
+  q.kv = __ldg(p.kv_len + r);
+  const long long most = (long long)p.max_blocks * kPage;
+  q.n_q = q1 - q.q0;
+  if (q.q0 < 0 || q1 < q.q0 || q1 > p.T || q.kv < 0 || q.kv > most) {
+    set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+    q.kv = (int)max(0LL, min((long long)q.kv, most));
+    if (q.q0 < 0 || q1 < q.q0 || q1 > p.T) q.n_q = 0;
+  }
+  const long long rows = (long long)q.n_q * p.G;
+  q.tiles = rows < p.min_rows || rows > p.max_rows ? 0 : (int)((rows + TR - 1) / TR);
+  q.units = p.sel ? p.max_sel : (q.kv + kPage - 1) / kPage;
+  q.units = q.units < 1 ? 1 : (q.units + UNIT - 1) / UNIT;
+  return q;
+}
+
+__device__ __forceinline__ long long work_of(const Params &p, const Request &q) {
+  return (long long)q.tiles * p.Hkv * q.units;
+}
+
+// Sum and exclusive prefix over the block.
+template <int WARPS>
+__device__ __forceinline__ long long block_scan(long long v, long long &total, long long *sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  total = 0;
+  long long before = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sm[w];
+    total += sm[w];
+  }
+  return before + x - v;
+}
+
+// This block's range [w0, w1) of the line and the request in which it begins.
+struct Range {
+  long long total, n_blk, w0, w1, r_start;
+  int r;
+};
+
+// All THREADS threads take part; sm: WARPS + 1 long longs and an int.
+template <int TR, int UNIT, int THREADS>
+__device__ __forceinline__ bool find_range(const Params &p, long long min_units, Range &g, long long *sm, int *sm_r) {
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x;
+  g.total = 0;
+  for (int base = 0; base < p.R; base += THREADS) {
+    const int r = base + tid;
+    long long sum;
+    block_scan<WARPS>(r < p.R ? work_of(p, request_of<TR, UNIT>(p, r)) : 0, sum, sm);
+    g.total += sum;
+  }
+  const long long most = (g.total + min_units - 1) / min_units;
+  g.n_blk = most < (long long)gridDim.x ? most : (long long)gridDim.x;
+  if ((long long)blockIdx.x >= g.n_blk) return false;
+  g.w0 = g.total * blockIdx.x / g.n_blk;
+  g.w1 = g.total * (blockIdx.x + 1) / g.n_blk;
+  long long before = 0;
+  for (int base = 0; base < p.R; base += THREADS) {
+    const int r = base + tid;
+    const long long v = r < p.R ? work_of(p, request_of<TR, UNIT>(p, r)) : 0;
+    long long sum;
+    const long long at = before + block_scan<WARPS>(v, sum, sm);
+    if (v > 0 && at <= g.w0 && g.w0 < at + v) {
+      *sm_r = r;
+      sm[WARPS] = at;
+    }
+    before += sum;
+    if (before > g.w0) break;       // uniform: every thread has the same sum
+  }
+  __syncthreads();
+  g.r = *sm_r;
+  g.r_start = sm[WARPS];
+  return true;
+}
+
+// The part of one item that lies in a block's range.
+struct Segment {
+  Request rq;
+  int r, h, tile, u0, u1;           // units [u0, u1) of the item
+  long long start;                  // of the item, on the line
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == rq.units; }
+};
+
+template <int TR, int UNIT>
+struct Walk {
+  long long pos, w1, r_start;
+  int r;
+  Request rq;
+  __device__ __forceinline__ void start(const Params &p, const Range &g) {
+    pos = g.w0;
+    w1 = g.w1;
+    r_start = g.r_start;
+    r = g.r;
+    rq = request_of<TR, UNIT>(p, r);
+  }
+  __device__ __forceinline__ bool next(const Params &p, Segment &s) {
+    if (pos >= w1) return false;
+    while (pos >= r_start + work_of(p, rq)) {
+      r_start += work_of(p, rq);
+      ++r;
+      rq = request_of<TR, UNIT>(p, r);
+    }
+    const long long item = (pos - r_start) / rq.units;
+    s.rq = rq;
+    s.r = r;
+    s.start = r_start + item * rq.units;
+    s.tile = (int)(item / p.Hkv);
+    s.h = (int)(item % p.Hkv);
+    s.u0 = (int)(pos - s.start);
+    s.u1 = (int)(w1 - s.start < rq.units ? w1 - s.start : rq.units);
+    pos = s.start + s.u1;
+    return true;
+  }
+};
+
+// The blocks that share a cut item: the first boundary inside it belongs to
+// block `first`, so the parts are those of first - 1 (its second slot) and of
+// first ... last (their first slots).
+__device__ __forceinline__ void sharers(const Range &g, const Segment &s, long long &first, long long &last) {
+  first = ((s.start + 1) * g.n_blk + g.total - 1) / g.total;
+  last = ((s.start + s.rq.units) * g.n_blk + g.total - 1) / g.total - 1;
+}
+
+// Pages of a request (or of its list): block e, its page or -1.  Blocks without
+// tokens have none; block and page numbers out of range are recorded.
+struct Pages {
+  const int *table, *sel;
+  int n, kv, max_blocks, n_pages;
+  int *dev_status;
+  __device__ __forceinline__ Pages(const Params &p, const Segment &s) {
+    table = p.block_table + (size_t)s.r * p.max_blocks;
+    kv = s.rq.kv;
+    max_blocks = p.max_blocks;
+    n_pages = p.n_pages;
+    dev_status = p.dev_status;
+    sel = nullptr;
+    n = (kv + kPage - 1) / kPage;
+    if (p.sel) {
+      const size_t at = (size_t)s.r * p.Hkv + s.h;
+      sel = p.sel + at * p.max_sel;
+      n = max(0, min(p.max_sel, __ldg(p.sel_count + at)));
+    }
+  }
+  __device__ __forceinline__ int page(int e, int &block, bool record) const {
+    block = -1;
+    if (e >= n) return -1;
+    block = sel ? __ldg(sel + e) : e;
+    bool bad = block < 0 || block >= max_blocks;
+    if (!bad) {
+      if (block * kPage >= kv) return -1;
+      const int q = __ldg(table + block);
+      if (q >= 0 && q < n_pages) return q;
+      bad = true;
+    }
+    if (record) set_status(dev_status, DITANGO_ERR_BOUNDS);
+    return -1;
+  }
+};
+
+// Two codes a register: codes i and i + 4 of a word, i = 0..3, less 8, as fp16.
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&pair)[4]) {
+  const uint32_t kOne = 0x3c003c00u, k16th = 0x2c002c00u;            // 1, 1/16
+  const uint32_t kEven = 0xe408e408u, kOdd = 0xd480d480u;            // -1032, -72
+  const uint32_t v = w >> 8;
+  pair[0] = hfma2((w & 0x000f000fu) | 0x64006400u, kOne, kEven);     // 1024 + c
+  pair[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, k16th, kOdd);     // 1024 + 16 c
+  pair[2] = hfma2((v & 0x000f000fu) | 0x64006400u, kOne, kEven);
+  pair[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, k16th, kOdd);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight values of a row of Q (16 bytes) times `down`, paired as unpack8 pairs codes.
+__device__ __forceinline__ void q_pairs(const uint4 &u, float down, uint32_t (&pair)[4], float &sum) {
+  const float f0 = bf_lo(u.x) * down, f1 = bf_hi(u.x) * down, f2 = bf_lo(u.y) * down, f3 = bf_hi(u.y) * down;
+  const float f4 = bf_lo(u.z) * down, f5 = bf_hi(u.z) * down, f6 = bf_lo(u.w) * down, f7 = bf_hi(u.w) * down;
+  sum += ((f0 + f1) + (f2 + f3)) + ((f4 + f5) + (f6 + f7));
+  pair[0] = pack_f16x2(f0, f4);
+  pair[1] = pack_f16x2(f1, f5);
+  pair[2] = pack_f16x2(f2, f6);
+  pair[3] = pack_f16x2(f3, f7);
+}
+
+__device__ __forceinline__ float max_abs8(const uint4 &u) {
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+  float big = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf_lo(v[e])), fabsf(bf_hi(v[e]))));
+  return big;
+}
+
+}  // namespace hattn
+
+cudaError_t launch_kv4_chunk(const hattn::Params &p, int d, int num_sms, cudaStream_t stream);
+size_t kv4_chunk_partial_floats(int d);
+int kv4_chunk_blocks();
+
+}  // namespace ditango

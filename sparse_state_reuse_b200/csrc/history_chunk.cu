@@ -1,0 +1,742 @@
+// Attention of many query rows over the paged 4-bit history: tcgen05 tiles.
+//
+// The arithmetic of the kernel of few rows (history_attn.cu) with 128 rows,
+// (token, query head) pairs of one key head, against tiles of two pages (128
+// keys), but with the scales inside the products, so that the softmax has
+// nothing to do for them:
+//   K  s (c - 8) over a power of two of the tile: a significand of 8 bits times
+//      a number of -8 ... 7 has 11 bits, so it is exact in fp16.  What is left,
+//      h sum(q), is one more step of the product: h and sum(q) are split into
+//      three fp16 parts each, and six of the 16 columns of that step hold the
+//      pairs that matter (the rest is below 2^-32 of it).
+//   V  s' (c' - 8) + h' in fp16 (2^-11, four times finer than the bf16 it was
+//      made from) over a power of two that no value of the item so far exceeds.
+// P is fp16.
+//
+// Pages cannot come by TMA (their codes have to be unpacked), so three warps
+// are producers: they read codes 16 bytes at a time one step ahead, unpack them
+// and write the two operands in the 128-byte swizzled form of the descriptors.
+// Within a group of 8 channels the order is the unpacked one (0 4 1 5 2 6 3 7);
+// Q is written in the same order, O put back at the end.
+//
+// Two blocks of threads share an SM (256 TMEM columns and at most 113 KB each):
+// one's exponentials run under the other's products.
+//   warps 0-3  softmax, a thread a row; they also write Q and store O
+//   warp  4    TMEM owner, MMA issuer (one thread)
+//   warp  5    producer, and a tile's references, one tile ahead
+//   warps 6-7  producers
+// TMEM: S [0, 128), O [128, 128 + d); the fp16 P overwrites the first 64
+// columns of S.  Each block takes an equal share of the line of work.
+#include <mutex>
+#include <set>
+
+#include <cuda_fp16.h>
+
+#include "history_attn.cuh"
+
+namespace ditango {
+namespace hchunk {
+
+using hattn::Params;
+
+constexpr int BM = 128;              // rows of a tile
+constexpr int BN = 2 * kPage;        // keys of a tile
+constexpr int kThreads = 256;
+constexpr int kLaunchRegs = 128;     // 65536 / (2 * 256)
+constexpr int kSoftmaxRegs = 192, kControlRegs = 64;
+static_assert(128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr int kProducers = 96;
+constexpr int kTmemCols = 256;
+constexpr int kMaxBlocks = 320;      // most blocks of a launch (the workspace has room for them)
+// A block's share is at least this many tiles: below, joining the parts of an
+// item costs more than the shorter share saves.
+constexpr int kMinUnits = 4;
+
+// What is known of a tile before its codes are unpacked.
+constexpr int kRing = 4;
+struct Tile {
+  uint32_t k[BN], v[BN];        // (scale, least) of its keys, 0 where there is no token
+  float kref, vref;             // the powers of two over which K and V are held
+  int pos[2];                   // first token of each page, past every length where there is none
+  uint32_t bad[4];              // keys whose V is not finite (written as 0: the softmax marks who sees it)
+};
+static_assert(sizeof(Tile) % 16 == 0, "records");
+
+template <int D>
+struct Cfg {
+  static constexpr int NCH = (D + 63) / 64;
+  static constexpr int CHUNK = 128 * 128;            // 128 rows of 128 bytes
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int OFF_Q = 0, OFF_K = TILE, OFF_V = 2 * TILE;
+  // the additional step of Q K^T: 128 rows of 16 columns, unswizzled (8 rows of
+  // 16 bytes are 128 bytes together, the two column halves next to each other)
+  static constexpr int AUG = 128 * 32, OFF_QA = 3 * TILE, OFF_KA = OFF_QA + AUG;
+  static constexpr int OFF_TILE = OFF_KA + AUG;      // ring of kRing tiles' records
+  static constexpr int OFF_BAR = OFF_TILE + kRing * (int)sizeof(Tile);
+  static constexpr int USED = OFF_BAR + 128;
+  static constexpr int SMEM = (USED + 1024 > 100 * 1024) ? USED + 1024 : 100 * 1024;
+  static constexpr int PARTS = D / 32;               // 16-byte pieces of a key's codes
+  // a producer takes piece pt % PARTS of every STEP-th key from pt / PARTS on
+  static constexpr int STEP = kProducers / PARTS;
+  static constexpr int LOADS = (BN + STEP - 1) / STEP;
+  static_assert(kProducers % PARTS == 0 && STEP % 8 == 0, "the swizzle is the same for all keys of a thread");
+  static constexpr int SLOT = BM * (D + 2);          // floats of a part of an item
+  static_assert(SMEM <= 113 * 1024, "two blocks an SM");
+};
+
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 16-byte piece of row r of the additional step's operands, columns 0 to 7
+// (columns 8 to 15 are 8 pieces on).
+__device__ __forceinline__ int aug_at(int r) { return (r >> 3) * 16 + (r & 7); }
+
+// x as the sum of three fp16 numbers.
+__device__ __forceinline__ void split3(float x, float &a, float &b, float &c) {
+  a = __half2float(__float2half_rn(x));
+  b = __half2float(__float2half_rn(x - a));
+  c = x - a - b;
+}
+
+// Shared-memory matrix descriptor of an unswizzled operand: lbo between the two
+// 16-byte columns, sbo between groups of 8 rows.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// Instruction descriptor of kind::f16 with fp16 A/B and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ long long s_scan[kThreads / 32 + 1];
+  __shared__ int s_request, s_last;
+  // each warp's place on the line; in shared memory, since the registers hold
+  // scores and codes
+  using WalkT = hattn::Walk<BM, 2>;
+  __shared__ hattn::Range s_range;
+  __shared__ WalkT s_walk[kThreads / 32];
+  __shared__ hattn::Segment s_seg[kThreads / 32];
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + C::OFF_Q, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
+  const uint32_t bar = sbase + C::OFF_BAR;
+  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 16, v_full = bar + 24, v_empty = bar + 32,
+                 s_full = bar + 40, p_full = bar + 48, o_full = bar + 56, drain_bar = bar + 64;
+  auto meta_full = [&](uint32_t n) { return bar + 72 + 8 * (n % kRing); };
+  // the softmax warps meet here when a part of an item is written (barriers
+  // with a limit, since any of them may have given up)
+  const uint32_t part_bar = bar + 104, join_bar = bar + 112;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 120);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 124);
+  Tile *tiles = reinterpret_cast<Tile *>(smem + C::OFF_TILE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
+
+  {
+    hattn::Range g;
+    if (!hattn::find_range<BM, 2, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
+    if (lane == 0) s_walk[warp].start(p, g);
+    if (threadIdx.x == 0) s_range = g;
+  }
+  const hattn::Segment &sg = s_seg[warp];
+  auto next_segment = [&]() -> bool {
+    bool more = false;
+    __syncwarp();
+    if (lane == 0) more = s_walk[warp].next(p, s_seg[warp]);
+    return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);        // one arrival per softmax warp
+    mbar_init(k_full, 3);        // one per producer warp
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 3);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(drain_bar, 1);
+    for (int k = 0; k < kRing; ++k) mbar_init(meta_full(k), 1);
+    mbar_init(part_bar, 4);
+    mbar_init(join_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  // columns 8 to 15 of the additional step stay zero
+  reinterpret_cast<uint4 *>(smem + (threadIdx.x < 128 ? C::OFF_QA : C::OFF_KA))[aug_at(threadIdx.x & 127) + 8] =
+      make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    bool ok = true;
+    uint32_t n = 0;              // tiles so far
+    if (warp >= 5) {
+      // ---------------------------------------------------------- producers
+      const int pt = threadIdx.x - 160;
+      const int row0 = pt / C::PARTS, part = pt % C::PARTS;
+      // 8 channels (word w of the piece) of key row0, 128-byte swizzled.  Pieces
+      // of the second 64 channels go in another order of words, so that 8
+      // threads write 8 different 16-byte columns.
+      const int turn = part >= 2 ? 2 : 0;
+      auto place = [&](int off, int w) {
+        const int atom = (part & 1) * 4 + (w ^ turn);
+        return smem + off + (part >> 1) * C::CHUNK + row0 * 128 + ((atom ^ (row0 & 7)) << 4);
+      };
+      while (ok && next_segment()) {
+        const hattn::Pages pages(p, sg);
+        const int u_end = sg.u1, head = sg.h;
+        uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
+        auto page_base = [&](int page) {
+          return p.data + ((size_t)max(page, 0) * p.Hkv + head) * page_bytes(D);
+        };
+        // ---- a tile's record (warp 5): scales in registers, then the ring
+        uint32_t mk[4], mv[4];
+        int mpos[2];
+        auto fetch_meta = [&](int u) {
+          int blk[2], page[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            page[e] = pages.page(2 * u + e, blk[e], lane == 0);
+            mpos[e] = page[e] >= 0 ? blk[e] * kPage : 0x7fffffff;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = k >> 1, key = (k & 1) * 32 + lane;
+            mk[k] = mv[k] = 0;
+            if (page[e] >= 0 && mpos[e] + key < pages.kv) {
+              const uint32_t *src = reinterpret_cast<const uint32_t *>(page_base(page[e]) + kPage * D) + key;
+              mk[k] = __ldg(src);
+              mv[k] = __ldg(src + kPage);
+            }
+          }
+        };
+        // bound of |x|: 8 s + |least + 8 s|; not finite: the row stands for NaN
+        auto bound = [](uint32_t m) { return fmaf(8.f, bf_lo(m), fabsf(fmaf(8.f, bf_lo(m), bf_hi(m)))); };
+        auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
+        auto put_meta = [&](uint32_t at) {
+          Tile &tile = tiles[at % kRing];
+          uint32_t ktop = 0, vtop = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float kb = bound(mk[k]), vb = bound(mv[k]);
+            if (kb < INFINITY) ktop = max(ktop, __float_as_uint(kb));
+            const bool bad = !(vb < INFINITY);
+            if (bad) mv[k] = 0; else vtop = max(vtop, __float_as_uint(vb));
+            tile.k[k * 32 + lane] = mk[k];
+            tile.v[k * 32 + lane] = mv[k];
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) tile.bad[k] = word;
+          }
+          ktop = __reduce_max_sync(0xffffffffu, ktop);
+          vtop = __reduce_max_sync(0xffffffffu, vtop);
+          vref_bits = max(vref_bits, reference(vtop));
+          if (lane == 0) {
+            tile.kref = __uint_as_float(reference(ktop));
+            tile.vref = __uint_as_float(vref_bits);
+            tile.pos[0] = mpos[0];
+            tile.pos[1] = mpos[1];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(meta_full(at));
+        };
+        if (warp == 5) {
+          // the ring's place is free: K of tile n - 1 was written, so S of tile
+          // n - 2 is complete and the softmax done with tile n - 3
+          fetch_meta(sg.u0);
+          put_meta(n);
+        }
+        for (int u = sg.u0; u < u_end && ok; ++u, ++n) {
+          int blk, page[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) page[e] = pages.page(2 * u + e, blk, false);
+          const uint8_t *b0 = page_base(page[0]), *b1 = page_base(page[1]);
+          auto codes = [&](int which, uint4 (&c)[C::LOADS]) {
+            const int at = which * (kPage * D / 2) + row0 * (D / 2) + part * 16;
+#pragma unroll
+            for (int k = 0; k < C::LOADS; ++k) {
+              const int row = row0 + k * C::STEP;
+              c[k] = make_uint4(0, 0, 0, 0);
+              if (row < BN && (row >= kPage ? page[1] : page[0]) >= 0)
+                c[k] = __ldg(reinterpret_cast<const uint4 *>(
+                    (row >= kPage ? b1 - kPage * (D / 2) : b0) + at + k * C::STEP * (D / 2)));
+            }
+          };
+          auto words = [&](const uint4 &c, uint32_t (&w)[4]) {
+            w[0] = turn ? c.z : c.x;
+            w[1] = turn ? c.w : c.y;
+            w[2] = turn ? c.x : c.z;
+            w[3] = turn ? c.y : c.w;
+          };
+          uint4 c[C::LOADS];
+          codes(0, c);
+          if (warp == 5 && u + 1 < u_end) fetch_meta(u + 1);
+          if (!(ok = wait_warp(meta_full(n), (n / kRing) & 1, ctl))) break;
+          const Tile &tile = tiles[n % kRing];
+          if (!(ok = wait_warp(k_empty, (n & 1) ^ 1, ctl))) break;
+          {
+            const float down = 1.f / tile.kref;
+#pragma unroll
+            for (int k = 0; k < C::LOADS; ++k) {
+              const int row = row0 + k * C::STEP;
+              if (row < BN) {
+                const uint32_t m = tile.k[row];
+                const float s = bf_lo(m) * down;
+                const uint32_t s2 = hattn::pack_f16x2(s, s);
+                uint32_t w[4];
+                words(c[k], w);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t x[4];
+                  hattn::unpack8(w[q], x);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], s2, 0x80008000u);
+                  *reinterpret_cast<uint4 *>(place(C::OFF_K, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+                if (part == 0) {       // h against sum(q) = (1 1 2 1 3 2): 1 2 1 3 1 2
+                  float h1, h2, h3;
+                  split3(fmaf(8.f, bf_lo(m), bf_hi(m)) * down, h1, h2, h3);
+                  const uint32_t h12 = hattn::pack_f16x2(h1, h2), h13 = hattn::pack_f16x2(h1, h3);
+                  reinterpret_cast<uint4 *>(smem + C::OFF_KA)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
+                }
+              }
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full);
+          codes(1, c);
+          if (warp == 5 && u + 1 < u_end) put_meta(n + 1);
+          if (!(ok = wait_warp(v_empty, (n & 1) ^ 1, ctl))) break;
+          {
+            const float down = 1.f / tile.vref;
+#pragma unroll
+            for (int k = 0; k < C::LOADS; ++k) {
+              const int row = row0 + k * C::STEP;
+              if (row < BN) {
+                const uint32_t m = tile.v[row];
+                const float s = bf_lo(m) * down, hh = fmaf(8.f, bf_lo(m), bf_hi(m)) * down;
+                const uint32_t s2 = hattn::pack_f16x2(s, s), h2 = hattn::pack_f16x2(hh, hh);
+                uint32_t w[4];
+                words(c[k], w);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t x[4];
+                  hattn::unpack8(w[q], x);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], s2, h2);
+                  *reinterpret_cast<uint4 *>(place(C::OFF_V, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+              }
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full);
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_qk = idesc_f16_f32(BM, BN, 0);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(BM, D, 1);
+      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t dK = smem_desc_sw128(sK, 16, 1024);
+      const uint64_t dV = smem_desc_sw128(sV, C::CHUNK, 1024);
+      const uint64_t dQA = smem_desc_plain(sbase + C::OFF_QA, 128, 256);
+      const uint64_t dKA = smem_desc_plain(sbase + C::OFF_KA, 128, 256);
+      uint32_t segs = 0;
+      while (ok && next_segment()) {
+        if (!(ok = wait_warp(q_full, segs & 1, ctl))) break;
+        ++segs;
+        const int u_begin = sg.u0, u_end = sg.u1;
+        for (int u = u_begin; u < u_end && ok; ++u, ++n) {
+          if (!(ok = wait_warp(k_full, n & 1, ctl))) break;
+          tc_fence_after();
+          if (leader) {
+            // P of the tile before lives in S: its product was issued before,
+            // and one thread's products run in order
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
+              mma_ss(tmem, dQ + off, dK + off, idesc_qk, kk > 0);
+            }
+            mma_ss(tmem, dQA, dKA, idesc_qk, 1);
+            tc_commit(s_full);
+            tc_commit(k_empty);
+          }
+          if (!(ok = wait_warp(v_full, n & 1, ctl))) break;
+          if (!(ok = wait_warp(p_full, n & 1, ctl))) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              mma_ts(tmem + 128, tmem + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, u > u_begin || kk > 0);
+            tc_commit(v_empty);
+            if (u + 1 == u_end) tc_commit(o_full);
+          }
+        }
+      }
+      // what was issued ends before TMEM is released, on both paths
+      volatile int never = 0;
+      WaitCtl drain{&never, nullptr, 100000000LL};
+      if (leader) tc_commit(drain_bar);
+      wait_bounded(drain_bar, 0, drain);
+      __syncwarp();
+    }
+    if (warp == 4) {
+      named_bar_sync(1, kThreads);
+      tc_fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+    } else {
+      tc_fence_before();
+      named_bar_arrive(1, kThreads);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- softmax
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  const int r = threadIdx.x;                    // row of the tile = TMEM lane
+  const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16);
+  const uint32_t tO = tS + 128;
+  bool ok = true;
+  uint32_t n = 0, segs = 0, parts = 0;
+  while (ok && next_segment()) {
+    const int row0 = sg.tile * BM;
+    const int rows = (int)min((long long)BM, (long long)sg.rq.n_q * p.G - row0);
+    // ---- Q of this row: fp16 below 2, channels in the codes' order
+    float qsum = 0.f, mul;
+    int vis = sg.rq.kv;                         // keys that the row sees
+    {
+      const bool live = r < rows;
+      const int tok = live ? (row0 + r) / p.G : 0, head = live ? (row0 + r) % p.G : 0;
+      if (p.causal && live) vis -= sg.rq.n_q - 1 - tok;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + (sg.rq.q0 + tok) * p.qt + (sg.h * p.G + head) * p.qh);
+      uint4 u[D / 8];
+      float big = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        u[k] = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+        big = fmaxf(big, hattn::max_abs8(u[k]));
+      }
+      const uint32_t ex = min(max(__float_as_uint(big) >> 23, 1u), 253u);
+      const float down = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        uint32_t x[4];
+        hattn::q_pairs(u[k], down, x, qsum);
+        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + (k >> 3) * C::CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+            make_uint4(x[0], x[1], x[2], x[3]);
+      }
+      mul = p.scale_log2 * __uint_as_float(ex << 23);
+      float q1, q2, q3;
+      split3(qsum, q1, q2, q3);
+      reinterpret_cast<uint4 *>(smem + C::OFF_QA)[aug_at(r)] =
+          make_uint4(hattn::pack_f16x2(q1, q1), hattn::pack_f16x2(q2, q1), hattn::pack_f16x2(q3, q2), 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    vis = max(vis, 0);
+    float m_used = -INFINITY, l = 0.f, vref = 1.f;
+    bool poison = false;            // the row sees a key whose V is not finite
+    const int units = sg.u1 - sg.u0;
+    for (int u = 0; u < units; ++u, ++n) {
+      if (!(ok = wait_bounded(meta_full(n), (n / kRing) & 1, ctl))) break;
+      const Tile &tile = tiles[n % kRing];
+      const int n0 = max(0, min(kPage, vis - tile.pos[0])), n1 = max(0, min(kPage, vis - tile.pos[1]));
+      if (!(ok = wait_bounded(s_full, n & 1, ctl))) break;
+      tc_fence_after();
+      uint32_t sv[BN];
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c) tmem_ld16p(tS + c * 16, &sv[c * 16]);
+      tc_wait_ld();
+      const float v_now = tile.vref, mulk = mul * tile.kref;
+      if (n0 + n1 < BN) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          if (c < kPage ? c >= n0 : c - kPage >= n1) sv[c] = __float_as_uint(-INFINITY);
+      }
+      if (tile.bad[0] | tile.bad[1] | tile.bad[2] | tile.bad[3]) {
+        auto low = [](int k) { return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u); };
+        poison = poison || ((tile.bad[0] & low(n0)) | (tile.bad[1] & low(n0 - 32)) | (tile.bad[2] & low(n1)) |
+                            (tile.bad[3] & low(n1 - 32))) != 0u;
+      }
+      float m8[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        m8[q] = max3(__uint_as_float(sv[q]), __uint_as_float(sv[q + 8]), __uint_as_float(sv[q + 16]));
+#pragma unroll
+      for (int c = 24; c + 16 <= BN; c += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          m8[q] = max3(m8[q], __uint_as_float(sv[c + q]), __uint_as_float(sv[c + q + 8]));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m8[q] = fmaxf(m8[q], __uint_as_float(sv[BN - 8 + q]));
+      const float mx2 =
+          max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * mulk;
+      if (u == 0) {
+        m_used = mx2;
+      } else {
+        // S of this tile is complete, and with it every product issued before:
+        // O may be rescaled, when a maximum grew by more than 2^8 or V's reference did
+        const bool need = mx2 > m_used + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need || v_now != vref)) {
+          const float m_new = need ? mx2 : m_used;
+          const float alpha = need ? fast_ex2(m_used - m_new) : 1.f;
+          l *= alpha;
+          m_used = m_new;
+          const float ao = alpha * (vref / v_now);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tO + c * 32, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * ao);
+            tmem_st32(tO + c * 32, v);
+          }
+        }
+      }
+      vref = v_now;
+      const float neg = m_used > -INFINITY ? -m_used : 0.f;   // no key so far: exponentiate against 0
+      const uint64_t neg2 = f2(neg, neg);
+      uint64_t factor = f2(mulk, mulk);
+      if (__any_sync(0xffffffffu, fabsf(neg) > kHuge)) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c) sv[c] = __float_as_uint(__fmul_rn(__uint_as_float(sv[c]), mulk));
+        factor = f2(1.f, 1.f);
+      }
+      uint64_t lsum0 = 0, lsum1 = 0;
+#pragma unroll
+      for (int g8 = 0; g8 < BN / 16; ++g8) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = g8 * 16 + 2 * e;
+          float xa, xb;
+          unf2(fma2(f2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), factor, neg2), xa, xb);
+          const float a = fast_ex2(xa), b = fast_ex2(xb);
+          if (e & 1) lsum1 = add2(lsum1, f2(a, b)); else lsum0 = add2(lsum0, f2(a, b));
+          pk[e] = hattn::pack_f16x2(a, b);
+        }
+        tmem_st8(tS + g8 * 8, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+      }
+      {
+        float s0, s1, s2, s3;
+        unf2(lsum0, s0, s1);
+        unf2(lsum1, s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    if (!ok) break;
+    if (!(ok = wait_bounded(o_full, segs & 1, ctl))) break;
+    ++segs;
+    tc_fence_after();
+    // ---- O: every product of the segment is done, so this warp's rows of the
+    // Q tile are free to stage 32 columns at a time
+    const bool whole = sg.whole();
+    float *part = p.partial + ((size_t)blockIdx.x * 2 + (sg.u0 == 0 ? 1 : 0)) * C::SLOT;
+    const bool none = !(l > 0.f) && l == l;
+    float fac = whole ? (l > 0.f ? vref / l : 0.f) : vref;
+    if (!(l == l) || poison) fac = __uint_as_float(0x7fc00000u);
+    float4 *epi = reinterpret_cast<float4 *>(smem + C::OFF_Q + warp * 4096);
+    auto out_row = [&](int row) -> long long {      // element offset of a row of the tile in out
+      const int at = row0 + row;
+      return (sg.rq.q0 + at / p.G) * p.ot + (sg.h * p.G + at % p.G) * p.oh;
+    };
+    const int wrow = r & ~31;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t ov[32];
+      tmem_ld32(tO + c * 32, ov);
+      tc_wait_ld();
+      if (none) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = 0u;
+      }
+      // columns 8 g + 2 i and 8 g + 2 i + 1 are channels 8 g + i and 8 g + 4 + i
+      auto val = [&](int ch) { return __uint_as_float(ov[(ch & ~7) + ((ch & 3) << 1) + ((ch >> 2) & 1)]) * fac; };
+      if (!whole || p.out_fp32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          epi[lane * 8 + (q ^ (lane & 7))] = make_float4(val(4 * q), val(4 * q + 1), val(4 * q + 2), val(4 * q + 3));
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int row = (lane >> 3) + 4 * q, seg = lane & 7;
+          if (wrow + row < rows) {
+            float *dst = whole ? static_cast<float *>(p.out) + out_row(wrow + row) : part + (wrow + row) * D;
+            reinterpret_cast<float4 *>(dst + c * 32)[seg] = epi[row * 8 + (seg ^ (row & 7))];
+          }
+        }
+      } else {
+        uint2 *ep = reinterpret_cast<uint2 *>(epi);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          ep[lane * 8 + (q ^ (lane & 7))] = make_uint2(pack_bf16x2(val(4 * q), val(4 * q + 1)),
+                                                       pack_bf16x2(val(4 * q + 2), val(4 * q + 3)));
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int row = (lane >> 3) + 4 * q, seg = lane & 7;
+          if (wrow + row < rows)
+            reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + out_row(wrow + row) + c * 32)[seg] =
+                ep[row * 8 + (seg ^ (row & 7))];
+        }
+      }
+      __syncwarp();
+    }
+    auto store_lse = [&](int row, float m_, float l_) {
+      const int at = row0 + row;
+      if (p.out_lse)
+        p.out_lse[(sg.rq.q0 + at / p.G) * p.lt + (sg.h * p.G + at % p.G) * p.lh] =
+            l_ > 0.f ? (m_ + log2f(l_)) * 0.69314718055994531f : (l_ == l_ ? -INFINITY : l_);
+    };
+    if (whole) {
+      if (r < rows) store_lse(r, m_used, l);
+      continue;
+    }
+    // ---- a part of an item: the block that finishes it last joins the parts
+    if (r < rows) {
+      part[BM * D + 2 * r] = m_used;
+      part[BM * D + 2 * r + 1] = l;
+    }
+    long long first, last;
+    hattn::sharers(s_range, sg, first, last);
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(part_bar);
+    if (warp == 0) {
+      if (!(ok = wait_warp(part_bar, parts & 1, ctl))) break;
+      if (lane == 0) {
+        const int before = atomicAdd(p.counters + first, 1);
+        s_last = before == (int)(last - first + 1);
+        if (s_last) p.counters[first] = 0;    // left at zero for the next launch
+        mbar_arrive(join_bar);
+      }
+    }
+    if (!(ok = wait_warp(join_bar, parts & 1, ctl))) break;
+    ++parts;
+    const bool join = *static_cast<volatile int *>(&s_last) != 0;   // written again only after all four warps came back
+    if (!join) continue;
+    __threadfence();
+    constexpr int kVec = D / 4;
+    for (int i = r; i < rows * kVec; i += 128) {
+      const int row = i / kVec, ch = (i % kVec) * 4;
+      float mt = -INFINITY, lt = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (long long c = first - 1; c <= last; ++c) {
+        const float *src = p.partial + (c * 2 + (c == first - 1 ? 1 : 0)) * C::SLOT;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + BM * D + 2 * row));
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + row * D + ch));
+        const float mn = fmaxf(mt, ml.x), sub = mn > -INFINITY ? mn : 0.f;
+        const float f0 = fast_ex2(mt - sub), f1 = fast_ex2(ml.x - sub);
+        lt = lt * f0 + ml.y * f1;
+        v = make_float4(v.x * f0 + a.x * f1, v.y * f0 + a.y * f1, v.z * f0 + a.z * f1, v.w * f0 + a.w * f1);
+        mt = mn;
+      }
+      const float inv = lt > 0.f ? 1.f / lt : (lt == lt ? 0.f : lt);
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      if (p.out_fp32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + out_row(row) + ch) = v;
+      else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + out_row(row) + ch) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (ch == 0) store_lse(row, mt, lt);
+    }
+  }
+  tc_fence_before();
+  named_bar_arrive(1, kThreads);
+}
+
+template <int D>
+cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
+  auto kfn = kv4_chunk_kernel<D>;
+  static std::mutex mu;
+  static std::set<int> ready;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready.count(dev)) {
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kfn);
+      if (e != cudaSuccess) return e;
+      // another count would leave setmaxnreg waiting for registers that do not come
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+      if (e != cudaSuccess) return e;
+      ready.insert(dev);
+    }
+  }
+  const int blocks = 2 * num_sms < kMaxBlocks ? 2 * num_sms : kMaxBlocks;
+  kfn<<<blocks, kThreads, Cfg<D>::SMEM, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace hchunk
+
+size_t kv4_chunk_partial_floats(int d) { return (size_t)hchunk::kMaxBlocks * 2 * hchunk::BM * (d + 2); }
+int kv4_chunk_blocks() { return hchunk::kMaxBlocks; }
+
+cudaError_t launch_kv4_chunk(const hattn::Params &p, int d, int num_sms, cudaStream_t stream) {
+  switch (d) {
+    case 64: return hchunk::launch<64>(p, num_sms, stream);
+    case 96: return hchunk::launch<96>(p, num_sms, stream);
+    case 128: return hchunk::launch<128>(p, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace ditango

@@ -250,6 +250,8 @@ def attend(c, q_lens, Q, out, lse, **kw):
     (3, 3, [130, 64], [20, 1], False),
     (16, 1, [190], [1], False),
     (4, 2, [333, 90], [70, 90], True),
+    (2, 1, [700, 0, 65], [129, 20, 1], True),     # many rows, none of them and few in one batch
+    (3, 1, [1000], [300], False),
 ])
 def test_attend_matches_the_oracle(d, H, Hkv, kv, q_lens, causal):
     rng = np.random.default_rng(d + H * 7 + sum(kv))
@@ -280,7 +282,7 @@ def test_attend_takes_strided_rows_and_leaves_the_others():
     assert (out[:, 5:] == 5).all() and (lse[:, 5:] == 5).all()
 
 
-@pytest.mark.parametrize("H,Hkv,q", [(2, 2, 1), (10, 2, 1), (4, 1, 40)])
+@pytest.mark.parametrize("H,Hkv,q", [(2, 2, 1), (10, 2, 1), (16, 1, 1), (4, 1, 40), (2, 2, 200)])
 def test_one_long_request_is_split_and_joined_alike_every_time(H, Hkv, q):
     """More pages than blocks of the launch: every item is cut, and the joined
     result is the same bits run after run."""
@@ -379,6 +381,54 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()     # row 0 does not see it
     assert torch.isnan(out[1]).all()
     assert torch.isnan(lse[1, 1]) and torch.isfinite(lse[1, 0])
+    n = 40                                                  # the same with many rows
+    c, host, table = filled(rng, kv, H, d, H, 2 * n, fill=0xff)
+    slot = int(table[0, 1]) * PAGE + 3                      # token 67: seen by the last 3 rows of 40
+    c.write(K, V, ints([slot], torch.int64))
+    Q = HC.up(HC.bf16_round(rng.standard_normal((2 * n, H, d))))
+    out, lse = torch.empty((2 * n, H, d), device="cuda"), torch.empty((2 * n, H), device="cuda")
+    attend(c, [n, n], Q, out, lse, causal=True, max_q=n)
+    assert torch.isfinite(out[:n - 3]).all() and torch.isfinite(out[n:]).all()
+    assert torch.isnan(out[n - 3:n]).all()
+    assert torch.isnan(lse[n - 3:n, 1]).all() and torch.isfinite(lse[n - 3:n, 0]).all()
+
+
+@pytest.mark.parametrize("q", [1, 60])
+def test_scales_of_any_size(q):
+    """V rows from 2^-60 to 2^60 of each other, and Q rows as far apart: what
+    is small beside what it is added to may be lost, nothing overflows."""
+    rng = np.random.default_rng(q)
+    d, H, n = 64, 2, 400
+    c, host, table = filled(rng, [n], H, d, H, q)
+    K, V = HC.keys_values(rng, n, H, d)
+    V = HC.bf16_round(V * 2.0 ** np.linspace(-60, 60, n).round()[:, None, None])
+    for t in range(n):
+        for h in range(H):
+            host.put(table[0, t // PAGE], t % PAGE, h, 1, V[t, h])
+    c.data.copy_(torch.from_numpy(host.data))
+    Q = HC.bf16_round(rng.standard_normal((q, H, d)))
+    Q[0, 1] = HC.bf16_round(Q[0, 1] * 2.0 ** 40)       # one key takes all
+    if q > 1:
+        Q[1] = HC.bf16_round(Q[1] * 2.0 ** -100)       # all keys alike
+        Q[2] = 0
+    Q = HC.up(Q)
+    out, lse = torch.empty((q, H, d), device="cuda"), torch.empty((q, H), device="cuda")
+    attend(c, [q], Q, out, lse, max_q=q)
+    # against the largest V at all: fp16 keeps 2^-25 of it
+    got = out.cpu().numpy().astype(np.float64)
+    qf = Q.float().cpu().numpy().astype(np.float64)
+    for t in range(q):
+        for h in range(H):
+            parts = [host.get(p, h) for p in table[0]]
+            k, v, y, x = (np.concatenate([p[i] for p in parts])[:n] for i in range(4))
+            o, e, P = OH.attend_rows(qf[t, h:h + 1], k, v, d ** -0.5)
+            dS = HC.logit_bound(qf[t, h:h + 1], y, d ** -0.5, d)
+            if dS > 0.1:
+                continue                                   # the logits themselves are not known to a unit
+            tol = HC.EPS * (P @ np.abs(v)) + 2 * dS * (P @ np.abs(v)) + 2.0 ** -22 * np.abs(v).max()
+            assert (np.abs(got[t, h] - o[0]) <= tol[0]).all(), (t, h)
+            assert abs(lse[t, h].item() - e[0]) <= dS + 2.0 ** -18 * (1 + abs(e[0]))
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
 # ---------------------------------------------------------------- summaries, selection
