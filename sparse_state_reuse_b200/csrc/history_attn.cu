@@ -623,7 +623,7 @@ static size_t partial_floats(int d) {
 }
 
 size_t kv4_attn_workspace_bytes(int d) {
-  return partial_floats(d) * sizeof(float) + (hattn::kMaxBlocks + kv4_chunk_blocks()) * sizeof(int);
+  return partial_floats(d) * sizeof(float) + (hattn::kMaxBlocks + kv4_chunk_counters()) * sizeof(int);
 }
 
 cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int max_blocks, int n_pages,

@@ -258,6 +258,6 @@ __device__ __forceinline__ float max_abs8(const uint4 &u) {
 
 cudaError_t launch_kv4_chunk(const hattn::Params &p, int d, int num_sms, cudaStream_t stream);
 size_t kv4_chunk_partial_floats(int d);
-int kv4_chunk_blocks();
+int kv4_chunk_counters();
 
 }  // namespace ditango

@@ -13,20 +13,23 @@
 //      made from) over a power of two that no value of the item so far exceeds.
 // P is fp16.
 //
-// Pages cannot come by TMA (their codes have to be unpacked), so three warps
-// are producers: they read codes 16 bytes at a time one step ahead, unpack them
-// and write the two operands in the 128-byte swizzled form of the descriptors.
+// One block of threads an SM takes two row tiles (256 rows) against the same
+// keys, so that a page is unpacked once for both: with one tile a block, and two
+// blocks an SM, unpacking alone took as long as the products.  The codes come
+// by bulk copies, one to two tiles ahead, into rings of their own for K, V and
+// scales; three warps unpack them and write the two operands in the 128-byte
+// swizzled form of the descriptors, K one tile ahead of V, K twice buffered.
 // Within a group of 8 channels the order is the unpacked one (0 4 1 5 2 6 3 7);
 // Q is written in the same order, O put back at the end.
-//
-// Two blocks of threads share an SM (256 TMEM columns and at most 113 KB each):
-// one's exponentials run under the other's products.
-//   warps 0-3  softmax, a thread a row; they also write Q and store O
-//   warp  4    TMEM owner, MMA issuer (one thread)
-//   warp  5    producer, and a tile's references, one tile ahead
-//   warps 6-7  producers
-// TMEM: S [0, 128), O [128, 128 + d); the fp16 P overwrites the first 64
-// columns of S.  Each block takes an equal share of the line of work.
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread a row; they also write
+//                   Q and store O
+//   warp  8         TMEM owner, MMA issuer (one thread): while one tile is
+//                   exponentiated, the other's products run
+//   warp  9         producer; also issues the copies and finds a tile's references
+//   warps 10-11     producers
+// TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 384), O1 [384, 512); the fp16 P
+// overwrites the first 64 columns of its S.  Each block takes an equal share of
+// the line of work.
 #include <mutex>
 #include <set>
 
@@ -40,48 +43,52 @@ namespace hchunk {
 using hattn::Params;
 
 constexpr int BM = 128;              // rows of a tile
+constexpr int TR = 2 * BM;           // rows of an item
 constexpr int BN = 2 * kPage;        // keys of a tile
-constexpr int kThreads = 256;
-constexpr int kLaunchRegs = 128;     // 65536 / (2 * 256)
-constexpr int kSoftmaxRegs = 192, kControlRegs = 64;
-static_assert(128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;     // 65536 / 384, rounded down to a multiple of 8
+constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
 constexpr int kProducers = 96;
-constexpr int kTmemCols = 256;
-constexpr int kMaxBlocks = 320;      // most blocks of a launch (the workspace has room for them)
+constexpr int kTmemCols = 512;
+constexpr int kMaxBlocks = 160;      // most blocks of a launch (the workspace has room for them)
 // A block's share is at least this many tiles: below, joining the parts of an
 // item costs more than the shorter share saves.
 constexpr int kMinUnits = 4;
 
-// What is known of a tile before its codes are unpacked.
+// What the softmax has to know of a tile.
 constexpr int kRing = 4;
 struct Tile {
-  uint32_t k[BN], v[BN];        // (scale, least) of its keys, 0 where there is no token
   float kref, vref;             // the powers of two over which K and V are held
   int pos[2];                   // first token of each page, past every length where there is none
   uint32_t bad[4];              // keys whose V is not finite (written as 0: the softmax marks who sees it)
 };
-static_assert(sizeof(Tile) % 16 == 0, "records");
 
 template <int D>
 struct Cfg {
   static constexpr int NCH = (D + 63) / 64;
   static constexpr int CHUNK = 128 * 128;            // 128 rows of 128 bytes
   static constexpr int TILE = NCH * CHUNK;
-  static constexpr int OFF_Q = 0, OFF_K = TILE, OFF_V = 2 * TILE;
+  static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE;   // Q0 Q1, K twice, V once
   // the additional step of Q K^T: 128 rows of 16 columns, unswizzled (8 rows of
   // 16 bytes are 128 bytes together, the two column halves next to each other)
-  static constexpr int AUG = 128 * 32, OFF_QA = 3 * TILE, OFF_KA = OFF_QA + AUG;
-  static constexpr int OFF_TILE = OFF_KA + AUG;      // ring of kRing tiles' records
+  static constexpr int AUG = 128 * 32, OFF_QA = 5 * TILE, OFF_KA = OFF_QA + 2 * AUG;
+  // the rings of copies: codes of two tiles each, scales of four
+  static constexpr int CODES = kPage * D / 2;        // bytes of K's (or V's) codes of a page
+  static constexpr int META = kPage * 8;             // of its scales, K's then V's
+  static constexpr int OFF_RK = OFF_KA + 2 * AUG, OFF_RV = OFF_RK + 4 * CODES, OFF_RM = OFF_RV + 4 * CODES;
+  static constexpr int OFF_TILE = OFF_RM + 2 * kRing * META;
   static constexpr int OFF_BAR = OFF_TILE + kRing * (int)sizeof(Tile);
-  static constexpr int USED = OFF_BAR + 128;
-  static constexpr int SMEM = (USED + 1024 > 100 * 1024) ? USED + 1024 : 100 * 1024;
+  static constexpr int USED = OFF_BAR + 256;
+  // more than half of the SM's, since a block allocates all TMEM columns
+  static constexpr int SMEM = (USED + 1024 > 120 * 1024) ? USED + 1024 : 120 * 1024;
   static constexpr int PARTS = D / 32;               // 16-byte pieces of a key's codes
   // a producer takes piece pt % PARTS of every STEP-th key from pt / PARTS on
   static constexpr int STEP = kProducers / PARTS;
   static constexpr int LOADS = (BN + STEP - 1) / STEP;
   static_assert(kProducers % PARTS == 0 && STEP % 8 == 0, "the swizzle is the same for all keys of a thread");
-  static constexpr int SLOT = BM * (D + 2);          // floats of a part of an item
-  static_assert(SMEM <= 113 * 1024, "two blocks an SM");
+  static constexpr int SLOT = TR * (D + 2);          // floats of a part of an item
+  static_assert(SMEM <= 227 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
@@ -141,37 +148,47 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ long long s_scan[kThreads / 32 + 1];
-  __shared__ int s_request, s_last;
+  __shared__ int s_request, s_last[2];
   // each warp's place on the line; in shared memory, since the registers hold
   // scores and codes
-  using WalkT = hattn::Walk<BM, 2>;
+  using WalkT = hattn::Walk<TR, 2>;
   __shared__ hattn::Range s_range;
   __shared__ WalkT s_walk[kThreads / 32];
   __shared__ hattn::Segment s_seg[kThreads / 32];
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t sQ = sbase + C::OFF_Q, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
   const uint32_t bar = sbase + C::OFF_BAR;
-  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 16, v_full = bar + 24, v_empty = bar + 32,
-                 s_full = bar + 40, p_full = bar + 48, o_full = bar + 56, drain_bar = bar + 64;
-  auto meta_full = [&](uint32_t n) { return bar + 72 + 8 * (n % kRing); };
-  // the softmax warps meet here when a part of an item is written (barriers
-  // with a limit, since any of them may have given up)
-  const uint32_t part_bar = bar + 104, join_bar = bar + 112;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 120);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 124);
+  auto q_full = [&](int k) { return bar + 8 * k; };
+  auto k_full = [&](uint32_t n) { return bar + 16 + 8 * (n & 1); };
+  auto k_empty = [&](uint32_t n) { return bar + 32 + 8 * (n & 1); };
+  const uint32_t v_full = bar + 48, v_empty = bar + 56;
+  auto s_full = [&](int k) { return bar + 64 + 8 * k; };
+  auto p_full = [&](int k) { return bar + 80 + 8 * k; };
+  auto o_full = [&](int k) { return bar + 96 + 8 * k; };
+  const uint32_t drain_bar = bar + 112;
+  auto rk_full = [&](uint32_t n) { return bar + 120 + 8 * (n & 1); };    // copies: K codes and scales
+  auto rv_full = [&](uint32_t n) { return bar + 136 + 8 * (n & 1); };    // V codes
+  auto rk_empty = [&](uint32_t n) { return bar + 152 + 8 * (n & 1); };
+  auto rv_empty = [&](uint32_t n) { return bar + 168 + 8 * (n & 1); };
+  auto tile_full = [&](uint32_t n) { return bar + 184 + 8 * (n % kRing); };
+  // the softmax warps of a row tile meet here when a part of an item is written
+  // (barriers with a limit, since any of them may have given up)
+  auto part_bar = [&](int k) { return bar + 216 + 8 * k; };
+  auto join_bar = [&](int k) { return bar + 232 + 8 * k; };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 248);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 252);
   Tile *tiles = reinterpret_cast<Tile *>(smem + C::OFF_TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
 
   {
     hattn::Range g;
-    if (!hattn::find_range<BM, 2, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
+    if (!hattn::find_range<TR, 2, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
     if (lane == 0) s_walk[warp].start(p, g);
     if (threadIdx.x == 0) s_range = g;
   }
@@ -180,44 +197,52 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
     bool more = false;
     __syncwarp();
     if (lane == 0) more = s_walk[warp].next(p, s_seg[warp]);
+    __syncwarp();
     return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);        // one arrival per softmax warp
-    mbar_init(k_full, 3);        // one per producer warp
-    mbar_init(k_empty, 1);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(q_full(k), 4);        // one arrival per softmax warp
+      mbar_init(k_full(k), 3);        // one per producer warp
+      mbar_init(k_empty(k), 1);
+      mbar_init(s_full(k), 1);
+      mbar_init(p_full(k), 4);
+      mbar_init(o_full(k), 1);
+      mbar_init(rk_full(k), 1);
+      mbar_init(rv_full(k), 1);
+      mbar_init(rk_empty(k), 3);
+      mbar_init(rv_empty(k), 3);
+      mbar_init(part_bar(k), 4);
+      mbar_init(join_bar(k), 1);
+    }
     mbar_init(v_full, 3);
     mbar_init(v_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(o_full, 1);
     mbar_init(drain_bar, 1);
-    for (int k = 0; k < kRing; ++k) mbar_init(meta_full(k), 1);
-    mbar_init(part_bar, 4);
-    mbar_init(join_bar, 1);
+    for (int k = 0; k < kRing; ++k) mbar_init(tile_full(k), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
   // columns 8 to 15 of the additional step stay zero
-  reinterpret_cast<uint4 *>(smem + (threadIdx.x < 128 ? C::OFF_QA : C::OFF_KA))[aug_at(threadIdx.x & 127) + 8] =
-      make_uint4(0, 0, 0, 0);
+  for (int k = threadIdx.x; k < 4 * 128; k += kThreads)
+    reinterpret_cast<uint4 *>(smem + C::OFF_QA + (k >> 7) * C::AUG)[aug_at(k & 127) + 8] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp >= 4) {
+
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     bool ok = true;
-    uint32_t n = 0;              // tiles so far
-    if (warp >= 5) {
+    uint32_t n0 = 0;             // tiles of the segments before
+    if (warp >= 9) {
       // ---------------------------------------------------------- producers
-      const int pt = threadIdx.x - 160;
+      const int pt = threadIdx.x - 288;
       const int row0 = pt / C::PARTS, part = pt % C::PARTS;
       // 8 channels (word w of the piece) of key row0, 128-byte swizzled.  Pieces
       // of the second 64 channels go in another order of words, so that 8
@@ -227,142 +252,149 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
         const int atom = (part & 1) * 4 + (w ^ turn);
         return smem + off + (part >> 1) * C::CHUNK + row0 * 128 + ((atom ^ (row0 & 7)) << 4);
       };
+      auto words = [&](const uint8_t *src, uint32_t (&w)[4]) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(src);
+        w[0] = turn ? c.z : c.x;
+        w[1] = turn ? c.w : c.y;
+        w[2] = turn ? c.x : c.z;
+        w[3] = turn ? c.y : c.w;
+      };
+      // bound of |x|: 8 s + |least + 8 s|; not finite: the row stands for NaN
+      auto bound = [](uint32_t m) { return fmaf(8.f, bf_lo(m), fabsf(fmaf(8.f, bf_lo(m), bf_hi(m)))); };
+      auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
+      uint32_t rk_sent = 0, rv_sent = 0;       // tiles whose copies were issued
       while (ok && next_segment()) {
         const hattn::Pages pages(p, sg);
-        const int u_end = sg.u1, head = sg.h;
+        const int T = sg.u1 - sg.u0, first = 2 * sg.u0, kv = sg.rq.kv, head = sg.h;
         uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
-        auto page_base = [&](int page) {
-          return p.data + ((size_t)max(page, 0) * p.Hkv + head) * page_bytes(D);
-        };
-        // ---- a tile's record (warp 5): scales in registers, then the ring
-        uint32_t mk[4], mv[4];
-        int mpos[2];
-        auto fetch_meta = [&](int u) {
+        // ---- copies (warp 9): tile j of the segment.  The ring's place is free
+        // once all producers are done with the tile two before it.
+        auto send = [&](int j, bool is_v) -> bool {
+          const uint32_t n = n0 + j;
+          if (!wait_warp(is_v ? rv_empty(n) : rk_empty(n), ((n >> 1) & 1) ^ 1, ctl)) return false;
+          const uint32_t full = is_v ? rv_full(n) : rk_full(n);
           int blk[2], page[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            page[e] = pages.page(2 * u + e, blk[e], lane == 0);
-            mpos[e] = page[e] >= 0 ? blk[e] * kPage : 0x7fffffff;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = k >> 1, key = (k & 1) * 32 + lane;
-            mk[k] = mv[k] = 0;
-            if (page[e] >= 0 && mpos[e] + key < pages.kv) {
-              const uint32_t *src = reinterpret_cast<const uint32_t *>(page_base(page[e]) + kPage * D) + key;
-              mk[k] = __ldg(src);
-              mv[k] = __ldg(src + kPage);
-            }
-          }
-        };
-        // bound of |x|: 8 s + |least + 8 s|; not finite: the row stands for NaN
-        auto bound = [](uint32_t m) { return fmaf(8.f, bf_lo(m), fabsf(fmaf(8.f, bf_lo(m), bf_hi(m)))); };
-        auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
-        auto put_meta = [&](uint32_t at) {
-          Tile &tile = tiles[at % kRing];
-          uint32_t ktop = 0, vtop = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float kb = bound(mk[k]), vb = bound(mv[k]);
-            if (kb < INFINITY) ktop = max(ktop, __float_as_uint(kb));
-            const bool bad = !(vb < INFINITY);
-            if (bad) mv[k] = 0; else vtop = max(vtop, __float_as_uint(vb));
-            tile.k[k * 32 + lane] = mk[k];
-            tile.v[k * 32 + lane] = mv[k];
-            const uint32_t word = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) tile.bad[k] = word;
-          }
-          ktop = __reduce_max_sync(0xffffffffu, ktop);
-          vtop = __reduce_max_sync(0xffffffffu, vtop);
-          vref_bits = max(vref_bits, reference(vtop));
+          for (int e = 0; e < 2; ++e) page[e] = pages.page(first + 2 * j + e, blk[e], !is_v && lane == 0);
           if (lane == 0) {
-            tile.kref = __uint_as_float(reference(ktop));
-            tile.vref = __uint_as_float(vref_bits);
-            tile.pos[0] = mpos[0];
-            tile.pos[1] = mpos[1];
+            const uint32_t each = C::CODES + (is_v ? 0 : C::META);
+            mbar_arrive_expect_tx(full, ((page[0] >= 0) + (page[1] >= 0)) * each);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (page[e] < 0) continue;
+              const uint8_t *src = p.data + ((size_t)page[e] * p.Hkv + head) * page_bytes(D);
+              bulk_load(sbase + (is_v ? C::OFF_RV : C::OFF_RK) + (2 * (n & 1) + e) * C::CODES,
+                        src + (is_v ? C::CODES : 0), C::CODES, full);
+              if (!is_v)
+                bulk_load(sbase + C::OFF_RM + (2 * (n % kRing) + e) * C::META, src + 2 * C::CODES, C::META, full);
+            }
+            if (!is_v) {
+              tiles[n % kRing].pos[0] = page[0] >= 0 ? blk[0] * kPage : 0x7fffffff;
+              tiles[n % kRing].pos[1] = page[1] >= 0 ? blk[1] * kPage : 0x7fffffff;
+            }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(meta_full(at));
+          if (is_v) ++rv_sent; else ++rk_sent;
+          return true;
         };
-        if (warp == 5) {
-          // the ring's place is free: K of tile n - 1 was written, so S of tile
-          // n - 2 is complete and the softmax done with tile n - 3
-          fetch_meta(sg.u0);
-          put_meta(n);
+        // (scale, least) of key `key` of tile n, 0 where there is no token
+        auto meta = [&](uint32_t n, int key, int is_v) -> uint32_t {
+          const int e = key >= kPage ? 1 : 0;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + C::OFF_RM + (2 * (n % kRing) + e) * C::META);
+          const uint32_t m = src[is_v * kPage + key % kPage];
+          return key % kPage < kv - tiles[n % kRing].pos[e] ? m : 0u;
+        };
+        if (warp == 9) {
+          for (int j = 0; j < 2 && j < T && ok; ++j) ok = send(j, false) && send(j, true);
+          if (!ok) break;
         }
-        for (int u = sg.u0; u < u_end && ok; ++u, ++n) {
-          int blk, page[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) page[e] = pages.page(2 * u + e, blk, false);
-          const uint8_t *b0 = page_base(page[0]), *b1 = page_base(page[1]);
-          auto codes = [&](int which, uint4 (&c)[C::LOADS]) {
-            const int at = which * (kPage * D / 2) + row0 * (D / 2) + part * 16;
-#pragma unroll
-            for (int k = 0; k < C::LOADS; ++k) {
-              const int row = row0 + k * C::STEP;
-              c[k] = make_uint4(0, 0, 0, 0);
-              if (row < BN && (row >= kPage ? page[1] : page[0]) >= 0)
-                c[k] = __ldg(reinterpret_cast<const uint4 *>(
-                    (row >= kPage ? b1 - kPage * (D / 2) : b0) + at + k * C::STEP * (D / 2)));
+        for (int j = 0; j <= T && ok; ++j) {
+          if (j < T) {
+            // ---- K of tile j
+            const uint32_t n = n0 + j;
+            if (warp == 9 && j >= 1 && j + 1 < T) {
+              // K's place was freed by K of tile j - 1, V's by V of tile j - 2
+              if (!(ok = send(j + 1, false))) break;
+              if (j >= 2 && !(ok = send(j, true))) break;
             }
-          };
-          auto words = [&](const uint4 &c, uint32_t (&w)[4]) {
-            w[0] = turn ? c.z : c.x;
-            w[1] = turn ? c.w : c.y;
-            w[2] = turn ? c.x : c.z;
-            w[3] = turn ? c.y : c.w;
-          };
-          uint4 c[C::LOADS];
-          codes(0, c);
-          if (warp == 5 && u + 1 < u_end) fetch_meta(u + 1);
-          if (!(ok = wait_warp(meta_full(n), (n / kRing) & 1, ctl))) break;
-          const Tile &tile = tiles[n % kRing];
-          if (!(ok = wait_warp(k_empty, (n & 1) ^ 1, ctl))) break;
-          {
-            const float down = 1.f / tile.kref;
+            if (warp == 9 && j >= 2 && j + 1 == T && !(ok = send(j, true))) break;
+            if (!(ok = wait_warp(rk_full(n), (n >> 1) & 1, ctl))) break;
+            if (warp == 9) {
+              Tile &tile = tiles[n % kRing];
+              uint32_t ktop = 0, vtop = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float kb = bound(meta(n, k * 32 + lane, 0)), vb = bound(meta(n, k * 32 + lane, 1));
+                if (kb < INFINITY) ktop = max(ktop, __float_as_uint(kb));
+                const bool bad = !(vb < INFINITY);
+                if (!bad) vtop = max(vtop, __float_as_uint(vb));
+                const uint32_t word = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) tile.bad[k] = word;
+              }
+              ktop = __reduce_max_sync(0xffffffffu, ktop);
+              vtop = __reduce_max_sync(0xffffffffu, vtop);
+              vref_bits = max(vref_bits, reference(vtop));
+              if (lane == 0) {
+                tile.kref = __uint_as_float(reference(ktop));
+                tile.vref = __uint_as_float(vref_bits);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tile_full(n));
+            }
+            if (!(ok = wait_warp(tile_full(n), (n / kRing) & 1, ctl))) break;
+            if (!(ok = wait_warp(k_empty(n), ((n >> 1) & 1) ^ 1, ctl))) break;
+            const float down = 1.f / tiles[n % kRing].kref;
+            const uint8_t *src = smem + C::OFF_RK + 2 * (n & 1) * C::CODES + row0 * (D / 2) + part * 16;
+            const int off = C::OFF_K + (n & 1) * C::TILE;
 #pragma unroll
             for (int k = 0; k < C::LOADS; ++k) {
               const int row = row0 + k * C::STEP;
               if (row < BN) {
-                const uint32_t m = tile.k[row];
+                const uint32_t m = meta(n, row, 0);
                 const float s = bf_lo(m) * down;
                 const uint32_t s2 = hattn::pack_f16x2(s, s);
                 uint32_t w[4];
-                words(c[k], w);
+                words(src + k * C::STEP * (D / 2), w);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   uint32_t x[4];
                   hattn::unpack8(w[q], x);
 #pragma unroll
                   for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], s2, 0x80008000u);
-                  *reinterpret_cast<uint4 *>(place(C::OFF_K, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+                  *reinterpret_cast<uint4 *>(place(off, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
                 if (part == 0) {       // h against sum(q) = (1 1 2 1 3 2): 1 2 1 3 1 2
                   float h1, h2, h3;
                   split3(fmaf(8.f, bf_lo(m), bf_hi(m)) * down, h1, h2, h3);
                   const uint32_t h12 = hattn::pack_f16x2(h1, h2), h13 = hattn::pack_f16x2(h1, h3);
-                  reinterpret_cast<uint4 *>(smem + C::OFF_KA)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
+                  reinterpret_cast<uint4 *>(smem + C::OFF_KA + (n & 1) * C::AUG)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
                 }
               }
             }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(k_full(n));
+              mbar_arrive(rk_empty(n));
+            }
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_full);
-          codes(1, c);
-          if (warp == 5 && u + 1 < u_end) put_meta(n + 1);
-          if (!(ok = wait_warp(v_empty, (n & 1) ^ 1, ctl))) break;
-          {
-            const float down = 1.f / tile.vref;
+          if (j >= 1) {
+            // ---- V of tile j - 1
+            const uint32_t n = n0 + j - 1;
+            if (!(ok = wait_warp(rv_full(n), (n >> 1) & 1, ctl))) break;
+            if (!(ok = wait_warp(v_empty, (n & 1) ^ 1, ctl))) break;
+            const float down = 1.f / tiles[n % kRing].vref;
+            const uint8_t *src = smem + C::OFF_RV + 2 * (n & 1) * C::CODES + row0 * (D / 2) + part * 16;
 #pragma unroll
             for (int k = 0; k < C::LOADS; ++k) {
               const int row = row0 + k * C::STEP;
               if (row < BN) {
-                const uint32_t m = tile.v[row];
+                uint32_t m = meta(n, row, 1);
+                if (!(bound(m) < INFINITY)) m = 0;
                 const float s = bf_lo(m) * down, hh = fmaf(8.f, bf_lo(m), bf_hi(m)) * down;
                 const uint32_t s2 = hattn::pack_f16x2(s, s), h2 = hattn::pack_f16x2(hh, hh);
                 uint32_t w[4];
-                words(c[k], w);
+                words(src + k * C::STEP * (D / 2), w);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   uint32_t x[4];
@@ -373,53 +405,95 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
                 }
               }
             }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(v_full);
+              mbar_arrive(rv_empty(n));
+            }
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_full);
         }
+        n0 += T;
+      }
+      // every copy issued lands before the warp exits, on both paths
+      if (warp == 9) {
+        volatile int never = 0;
+        WaitCtl drain{&never, nullptr, 100000000LL};
+        for (uint32_t n = rk_sent > 2 ? rk_sent - 2 : 0; n < rk_sent; ++n) wait_bounded(rk_full(n), (n >> 1) & 1, drain);
+        for (uint32_t n = rv_sent > 2 ? rv_sent - 2 : 0; n < rv_sent; ++n) wait_bounded(rv_full(n), (n >> 1) & 1, drain);
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
       const bool leader = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16_f32(BM, BN, 0);
       constexpr uint32_t idesc_pv = idesc_f16_f32(BM, D, 1);
-      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dK = smem_desc_sw128(sK, 16, 1024);
-      const uint64_t dV = smem_desc_sw128(sV, C::CHUNK, 1024);
-      const uint64_t dQA = smem_desc_plain(sbase + C::OFF_QA, 128, 256);
-      const uint64_t dKA = smem_desc_plain(sbase + C::OFF_KA, 128, 256);
-      uint32_t segs = 0;
-      while (ok && next_segment()) {
-        if (!(ok = wait_warp(q_full, segs & 1, ctl))) break;
-        ++segs;
-        const int u_begin = sg.u0, u_end = sg.u1;
-        for (int u = u_begin; u < u_end && ok; ++u, ++n) {
-          if (!(ok = wait_warp(k_full, n & 1, ctl))) break;
-          tc_fence_after();
-          if (leader) {
-            // P of the tile before lives in S: its product was issued before,
-            // and one thread's products run in order
+      auto qk = [&](int k, uint32_t n) {
+        uint64_t a = smem_desc_sw128(sbase + C::OFF_Q + k * C::TILE, 16, 1024);
+        uint64_t b = smem_desc_sw128(sbase + C::OFF_K + (n & 1) * C::TILE, 16, 1024);
+        // S_k = Q_k K^T.  P of the tile before lives in S_k: its product was
+        // issued before, and one thread's products run in order.
+        if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
-              mma_ss(tmem, dQ + off, dK + off, idesc_qk, kk > 0);
-            }
-            mma_ss(tmem, dQA, dKA, idesc_qk, 1);
-            tc_commit(s_full);
-            tc_commit(k_empty);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + 128 * k, a + off, b + off, idesc_qk, kk > 0);
           }
-          if (!(ok = wait_warp(v_full, n & 1, ctl))) break;
-          if (!(ok = wait_warp(p_full, n & 1, ctl))) break;
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(tmem + 128, tmem + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, u > u_begin || kk > 0);
-            tc_commit(v_empty);
-            if (u + 1 == u_end) tc_commit(o_full);
-          }
+          mma_ss(tmem + 128 * k, smem_desc_plain(sbase + C::OFF_QA + k * C::AUG, 128, 256),
+                 smem_desc_plain(sbase + C::OFF_KA + (n & 1) * C::AUG, 128, 256), idesc_qk, 1);
+          tc_commit(s_full(k));
         }
+      };
+      auto pv = [&](int k, bool acc) {
+        const uint64_t b = smem_desc_sw128(sbase + C::OFF_V, C::CHUNK, 1024);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + 256 + 128 * k, tmem + 128 * k + kk * 8, b + (uint64_t)((kk * 2048) >> 4), idesc_pv, acc || kk > 0);
+        }
+      };
+      uint32_t segs = 0, segs1 = 0, pc1 = 0;
+      while (ok && next_segment()) {
+        const int T = sg.u1 - sg.u0;
+        const bool has1 = (long long)sg.rq.n_q * p.G - (long long)sg.tile * TR > BM;
+        if (!(ok = wait_warp(q_full(0), segs & 1, ctl))) break;
+        ++segs;
+        if (has1) {
+          if (!(ok = wait_warp(q_full(1), segs1 & 1, ctl))) break;
+          ++segs1;
+        }
+        if (!(ok = wait_warp(k_full(n0), (n0 >> 1) & 1, ctl))) break;
+        tc_fence_after();
+        qk(0, n0);
+        if (has1) qk(1, n0);
+        commit_by(leader, k_empty(n0));
+        for (int t = 0; t < T && ok; ++t) {
+          const uint32_t n = n0 + t;
+          const bool more = t + 1 < T;
+          if (!(ok = wait_warp(v_full, n & 1, ctl))) break;
+          if (!(ok = wait_warp(p_full(0), n & 1, ctl))) break;
+          tc_fence_after();
+          pv(0, t > 0);
+          if (!more) commit_by(leader, o_full(0));
+          if (more) {
+            if (!(ok = wait_warp(k_full(n + 1), ((n + 1) >> 1) & 1, ctl))) break;
+            tc_fence_after();
+            qk(0, n + 1);
+            if (!has1) commit_by(leader, k_empty(n + 1));
+          }
+          if (has1) {
+            if (!(ok = wait_warp(p_full(1), pc1 & 1, ctl))) break;
+            ++pc1;
+            tc_fence_after();
+            pv(1, t > 0);
+            if (!more) commit_by(leader, o_full(1));
+            if (more) {
+              qk(1, n + 1);
+              commit_by(leader, k_empty(n + 1));
+            }
+          }
+          commit_by(leader, v_empty);
+        }
+        n0 += T;
       }
       // what was issued ends before TMEM is released, on both paths
       volatile int never = 0;
@@ -428,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
       wait_bounded(drain_bar, 0, drain);
       __syncwarp();
     }
-    if (warp == 4) {
+    if (warp == 8) {
       named_bar_sync(1, kThreads);
       tc_fence_after();
       tmem_dealloc(tmem, kTmemCols);
@@ -441,14 +515,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
 
   // -------------------------------------------------------------- softmax
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-  const int r = threadIdx.x;                    // row of the tile = TMEM lane
-  const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16);
-  const uint32_t tO = tS + 128;
+  const int kt = warp >> 2;                     // row tile
+  const int r = threadIdx.x & 127;              // row of the tile = TMEM lane
+  const uint32_t tS = tmem + 128 * kt + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t tO = tS + 256;
   bool ok = true;
-  uint32_t n = 0, segs = 0, parts = 0;
+  uint32_t n = 0;                               // tiles of all segments
+  uint32_t sc = 0, segs = 0, parts = 0;         // of those with rows of this tile
   while (ok && next_segment()) {
-    const int row0 = sg.tile * BM;
+    const int row0 = sg.tile * TR + kt * BM;
     const int rows = (int)min((long long)BM, (long long)sg.rq.n_q * p.G - row0);
+    const int units = sg.u1 - sg.u0;
+    if (rows <= 0) {                            // a tile of rows that are not there
+      n += units;
+      continue;
+    }
     // ---- Q of this row: fp16 below 2, channels in the codes' order
     float qsum = 0.f, mul;
     int vis = sg.rq.kv;                         // keys that the row sees
@@ -470,34 +551,38 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
       for (int k = 0; k < D / 8; ++k) {
         uint32_t x[4];
         hattn::q_pairs(u[k], down, x, qsum);
-        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + (k >> 3) * C::CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + kt * C::TILE + (k >> 3) * C::CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
             make_uint4(x[0], x[1], x[2], x[3]);
       }
       mul = p.scale_log2 * __uint_as_float(ex << 23);
       float q1, q2, q3;
       split3(qsum, q1, q2, q3);
-      reinterpret_cast<uint4 *>(smem + C::OFF_QA)[aug_at(r)] =
+      reinterpret_cast<uint4 *>(smem + C::OFF_QA + kt * C::AUG)[aug_at(r)] =
           make_uint4(hattn::pack_f16x2(q1, q1), hattn::pack_f16x2(q2, q1), hattn::pack_f16x2(q3, q2), 0);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(q_full(kt));
     }
     vis = max(vis, 0);
     float m_used = -INFINITY, l = 0.f, vref = 1.f;
     bool poison = false;            // the row sees a key whose V is not finite
-    const int units = sg.u1 - sg.u0;
-    for (int u = 0; u < units; ++u, ++n) {
-      if (!(ok = wait_bounded(meta_full(n), (n / kRing) & 1, ctl))) break;
+    for (int u = 0; u < units; ++u, ++n, ++sc) {
+      // S first: then the record of tile n is there and the ring not yet round
+      // (warps that passed over segments may come early)
+      if (!(ok = wait_bounded(s_full(kt), sc & 1, ctl))) break;
+      if (!(ok = wait_bounded(tile_full(n), (n / kRing) & 1, ctl))) break;
       const Tile &tile = tiles[n % kRing];
       const int n0 = max(0, min(kPage, vis - tile.pos[0])), n1 = max(0, min(kPage, vis - tile.pos[1]));
-      if (!(ok = wait_bounded(s_full, n & 1, ctl))) break;
+      __syncwarp();
       tc_fence_after();
       uint32_t sv[BN];
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c) tmem_ld16p(tS + c * 16, &sv[c * 16]);
       tc_wait_ld();
       const float v_now = tile.vref, mulk = mul * tile.kref;
-      if (n0 + n1 < BN) {
+      // rows of a warp may see different keys: the branch is the warp's, so that it
+      // stays together for the tensor memory instructions
+      if (__any_sync(0xffffffffu, n0 + n1 < BN)) {
 #pragma unroll
         for (int c = 0; c < BN; ++c)
           if (c < kPage ? c >= n0 : c - kPage >= n1) sv[c] = __float_as_uint(-INFINITY);
@@ -576,20 +661,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(p_full(kt));
     }
     if (!ok) break;
-    if (!(ok = wait_bounded(o_full, segs & 1, ctl))) break;
+    if (!(ok = wait_bounded(o_full(kt), segs & 1, ctl))) break;
     ++segs;
     tc_fence_after();
     // ---- O: every product of the segment is done, so this warp's rows of the
     // Q tile are free to stage 32 columns at a time
     const bool whole = sg.whole();
-    float *part = p.partial + ((size_t)blockIdx.x * 2 + (sg.u0 == 0 ? 1 : 0)) * C::SLOT;
+    float *part = p.partial + ((size_t)blockIdx.x * 2 + (sg.u0 == 0 ? 1 : 0)) * C::SLOT + kt * BM * (D + 2);
     const bool none = !(l > 0.f) && l == l;
     float fac = whole ? (l > 0.f ? vref / l : 0.f) : vref;
     if (!(l == l) || poison) fac = __uint_as_float(0x7fc00000u);
-    float4 *epi = reinterpret_cast<float4 *>(smem + C::OFF_Q + warp * 4096);
+    float4 *epi = reinterpret_cast<float4 *>(smem + C::OFF_Q + kt * C::TILE + (warp & 3) * 4096);
     auto out_row = [&](int row) -> long long {      // element offset of a row of the tile in out
       const int at = row0 + row;
       return (sg.rq.q0 + at / p.G) * p.ot + (sg.h * p.G + at % p.G) * p.oh;
@@ -655,19 +740,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
     hattn::sharers(s_range, sg, first, last);
     __threadfence();
     __syncwarp();
-    if (lane == 0) mbar_arrive(part_bar);
-    if (warp == 0) {
-      if (!(ok = wait_warp(part_bar, parts & 1, ctl))) break;
+    if (lane == 0) mbar_arrive(part_bar(kt));
+    if ((warp & 3) == 0) {
+      if (!(ok = wait_warp(part_bar(kt), parts & 1, ctl))) break;
       if (lane == 0) {
-        const int before = atomicAdd(p.counters + first, 1);
-        s_last = before == (int)(last - first + 1);
-        if (s_last) p.counters[first] = 0;    // left at zero for the next launch
-        mbar_arrive(join_bar);
+        int *counter = p.counters + 2 * first + kt;
+        const int before = atomicAdd(counter, 1);
+        s_last[kt] = before == (int)(last - first + 1);
+        if (s_last[kt]) *counter = 0;         // left at zero for the next launch
+        mbar_arrive(join_bar(kt));
       }
     }
-    if (!(ok = wait_warp(join_bar, parts & 1, ctl))) break;
+    if (!(ok = wait_warp(join_bar(kt), parts & 1, ctl))) break;
     ++parts;
-    const bool join = *static_cast<volatile int *>(&s_last) != 0;   // written again only after all four warps came back
+    const bool join = *static_cast<volatile int *>(&s_last[kt]) != 0;   // written again only after all four warps came back
     if (!join) continue;
     __threadfence();
     constexpr int kVec = D / 4;
@@ -676,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const __grid_con
       float mt = -INFINITY, lt = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       for (long long c = first - 1; c <= last; ++c) {
-        const float *src = p.partial + (c * 2 + (c == first - 1 ? 1 : 0)) * C::SLOT;
+        const float *src = p.partial + (c * 2 + (c == first - 1 ? 1 : 0)) * C::SLOT + kt * BM * (D + 2);
         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + BM * D + 2 * row));
         const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + row * D + ch));
         const float mn = fmaxf(mt, ml.x), sub = mn > -INFINITY ? mn : 0.f;
@@ -720,15 +806,15 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
       ready.insert(dev);
     }
   }
-  const int blocks = 2 * num_sms < kMaxBlocks ? 2 * num_sms : kMaxBlocks;
+  const int blocks = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
   kfn<<<blocks, kThreads, Cfg<D>::SMEM, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace hchunk
 
-size_t kv4_chunk_partial_floats(int d) { return (size_t)hchunk::kMaxBlocks * 2 * hchunk::BM * (d + 2); }
-int kv4_chunk_blocks() { return hchunk::kMaxBlocks; }
+size_t kv4_chunk_partial_floats(int d) { return (size_t)hchunk::kMaxBlocks * 2 * hchunk::TR * (d + 2); }
+int kv4_chunk_counters() { return 2 * hchunk::kMaxBlocks; }
 
 cudaError_t launch_kv4_chunk(const hattn::Params &p, int d, int num_sms, cudaStream_t stream) {
   switch (d) {
