@@ -14,19 +14,24 @@
 // P is fp16.
 //
 // One block of threads an SM takes two row tiles (256 rows) against the same
-// keys, so that a page is unpacked once for both: with one tile a block, and two
-// blocks an SM, unpacking alone took as long as the products.  The codes come
-// by bulk copies, one to two tiles ahead, into rings of their own for K, V and
-// scales; three warps unpack them and write the two operands in the 128-byte
-// swizzled form of the descriptors, K one tile ahead of V, K twice buffered.
-// Within a group of 8 channels the order is the unpacked one (0 4 1 5 2 6 3 7);
-// Q is written in the same order, O put back at the end.
+// keys, so that a page is unpacked once for both.  Six warps unpack the codes
+// and write the two operands in the 128-byte swizzled form of the descriptors,
+// K and V apart and both twice buffered: a V buffer is in use from one row
+// tile's product to the other's, half a step later, so that a single one leaves
+// no time to write it (with it, and with the codes staged in shared memory by
+// bulk copies, history_frame of perf/operators.py took 2.06 ms).  The codes are
+// read 16 bytes at a time into the registers that the tile before just left.
+// Channels keep the unpacked order (0 4 1 5 2 6 3 7 of each 8), and of the
+// second 64 the groups of 16 are exchanged in pairs of groups, which spreads the
+// 16-byte writes of 8 threads over all banks; Q is written in the same order, O
+// put back at the end.
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread a row; they also write
 //                   Q and store O
 //   warp  8         TMEM owner, MMA issuer (one thread): while one tile is
 //                   exponentiated, the other's products run
-//   warp  9         producer; also issues the copies and finds a tile's references
-//   warps 10-11     producers
+//   warp  9         writes the tiles' records
+//   warps 10-12     K producers
+//   warps 13-15     V producers
 // TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 384), O1 [384, 512); the fp16 P
 // overwrites the first 64 columns of its S.  Each block takes an equal share of
 // the line of work.
@@ -45,20 +50,23 @@ using hattn::Params;
 constexpr int BM = 128;              // rows of a tile
 constexpr int TR = 2 * BM;           // rows of an item
 constexpr int BN = 2 * kPage;        // keys of a tile
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168;     // 65536 / 384, rounded down to a multiple of 8
-constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
-constexpr int kProducers = 96;
+constexpr int kThreads = 512;
+constexpr int kLaunchRegs = 128;     // 65536 / 512
+constexpr int kSoftmaxRegs = 176, kControlRegs = 80;
+static_assert(2 * 128 * kSoftmaxRegs + 2 * 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr int kProducers = 96;       // threads that unpack K, and as many for V
 constexpr int kTmemCols = 512;
 constexpr int kMaxBlocks = 160;      // most blocks of a launch (the workspace has room for them)
 // A block's share is at least this many tiles: below, joining the parts of an
 // item costs more than the shorter share saves.
 constexpr int kMinUnits = 4;
 
-// What the softmax has to know of a tile.
+// What is known of a tile before its codes are unpacked.
 constexpr int kRing = 4;
 struct Tile {
+  uint2 v[BN];                  // V's s and h over vref, as fp16 pairs
+  uint32_t ks[BN];              // K's s over kref, as an fp16 pair
+  float kh[BN];                 // K's h over kref
   float kref, vref;             // the powers of two over which K and V are held
   int pos[2];                   // first token of each page, past every length where there is none
   uint32_t bad[4];              // keys whose V is not finite (written as 0: the softmax marks who sees it)
@@ -69,17 +77,13 @@ struct Cfg {
   static constexpr int NCH = (D + 63) / 64;
   static constexpr int CHUNK = 128 * 128;            // 128 rows of 128 bytes
   static constexpr int TILE = NCH * CHUNK;
-  static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE;   // Q0 Q1, K twice, V once
+  static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE;   // each twice
   // the additional step of Q K^T: 128 rows of 16 columns, unswizzled (8 rows of
   // 16 bytes are 128 bytes together, the two column halves next to each other)
-  static constexpr int AUG = 128 * 32, OFF_QA = 5 * TILE, OFF_KA = OFF_QA + 2 * AUG;
-  // the rings of copies: codes of two tiles each, scales of four
-  static constexpr int CODES = kPage * D / 2;        // bytes of K's (or V's) codes of a page
-  static constexpr int META = kPage * 8;             // of its scales, K's then V's
-  static constexpr int OFF_RK = OFF_KA + 2 * AUG, OFF_RV = OFF_RK + 4 * CODES, OFF_RM = OFF_RV + 4 * CODES;
-  static constexpr int OFF_TILE = OFF_RM + 2 * kRing * META;
+  static constexpr int AUG = 128 * 32, OFF_QA = 6 * TILE, OFF_KA = OFF_QA + 2 * AUG;
+  static constexpr int OFF_TILE = OFF_KA + 2 * AUG;
   static constexpr int OFF_BAR = OFF_TILE + kRing * (int)sizeof(Tile);
-  static constexpr int USED = OFF_BAR + 256;
+  static constexpr int USED = OFF_BAR + 240;
   // more than half of the SM's, since a block allocates all TMEM columns
   static constexpr int SMEM = (USED + 1024 > 120 * 1024) ? USED + 1024 : 120 * 1024;
   static constexpr int PARTS = D / 32;               // 16-byte pieces of a key's codes
@@ -166,22 +170,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
   auto q_full = [&](int k) { return bar + 8 * k; };
   auto k_full = [&](uint32_t n) { return bar + 16 + 8 * (n & 1); };
   auto k_empty = [&](uint32_t n) { return bar + 32 + 8 * (n & 1); };
-  const uint32_t v_full = bar + 48, v_empty = bar + 56;
-  auto s_full = [&](int k) { return bar + 64 + 8 * k; };
-  auto p_full = [&](int k) { return bar + 80 + 8 * k; };
-  auto o_full = [&](int k) { return bar + 96 + 8 * k; };
-  const uint32_t drain_bar = bar + 112;
-  auto rk_full = [&](uint32_t n) { return bar + 120 + 8 * (n & 1); };    // copies: K codes and scales
-  auto rv_full = [&](uint32_t n) { return bar + 136 + 8 * (n & 1); };    // V codes
-  auto rk_empty = [&](uint32_t n) { return bar + 152 + 8 * (n & 1); };
-  auto rv_empty = [&](uint32_t n) { return bar + 168 + 8 * (n & 1); };
-  auto tile_full = [&](uint32_t n) { return bar + 184 + 8 * (n % kRing); };
+  auto v_full = [&](uint32_t n) { return bar + 48 + 8 * (n & 1); };
+  auto v_empty = [&](uint32_t n) { return bar + 64 + 8 * (n & 1); };
+  auto s_full = [&](int k) { return bar + 80 + 8 * k; };
+  auto p_full = [&](int k) { return bar + 96 + 8 * k; };
+  auto o_full = [&](int k) { return bar + 112 + 8 * k; };
+  auto tile_full = [&](uint32_t n) { return bar + 128 + 8 * (n % kRing); };
+  auto tile_empty = [&](uint32_t n) { return bar + 160 + 8 * (n % kRing); };
   // the softmax warps of a row tile meet here when a part of an item is written
   // (barriers with a limit, since any of them may have given up)
-  auto part_bar = [&](int k) { return bar + 216 + 8 * k; };
-  auto join_bar = [&](int k) { return bar + 232 + 8 * k; };
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 248);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 252);
+  auto part_bar = [&](int k) { return bar + 192 + 8 * k; };
+  auto join_bar = [&](int k) { return bar + 208 + 8 * k; };
+  const uint32_t drain_bar = bar + 224;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_BAR + 232);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 236);
   Tile *tiles = reinterpret_cast<Tile *>(smem + C::OFF_TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
@@ -209,17 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       mbar_init(s_full(k), 1);
       mbar_init(p_full(k), 4);
       mbar_init(o_full(k), 1);
-      mbar_init(rk_full(k), 1);
-      mbar_init(rv_full(k), 1);
-      mbar_init(rk_empty(k), 3);
-      mbar_init(rv_empty(k), 3);
+      mbar_init(v_full(k), 3);
+      mbar_init(v_empty(k), 1);
       mbar_init(part_bar(k), 4);
       mbar_init(join_bar(k), 1);
     }
-    mbar_init(v_full, 3);
-    mbar_init(v_empty, 1);
     mbar_init(drain_bar, 1);
-    for (int k = 0; k < kRing; ++k) mbar_init(tile_full(k), 1);
+    for (int k = 0; k < kRing; ++k) {
+      mbar_init(tile_full(k), 1);
+      mbar_init(tile_empty(k), 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -240,187 +241,157 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     bool ok = true;
     uint32_t n0 = 0;             // tiles of the segments before
-    if (warp >= 9) {
-      // ---------------------------------------------------------- producers
-      const int pt = threadIdx.x - 288;
-      const int row0 = pt / C::PARTS, part = pt % C::PARTS;
-      // 8 channels (word w of the piece) of key row0, 128-byte swizzled.  Pieces
-      // of the second 64 channels go in another order of words, so that 8
-      // threads write 8 different 16-byte columns.
-      const int turn = part >= 2 ? 2 : 0;
-      auto place = [&](int off, int w) {
-        const int atom = (part & 1) * 4 + (w ^ turn);
-        return smem + off + (part >> 1) * C::CHUNK + row0 * 128 + ((atom ^ (row0 & 7)) << 4);
-      };
-      auto words = [&](const uint8_t *src, uint32_t (&w)[4]) {
-        const uint4 c = *reinterpret_cast<const uint4 *>(src);
-        w[0] = turn ? c.z : c.x;
-        w[1] = turn ? c.w : c.y;
-        w[2] = turn ? c.x : c.z;
-        w[3] = turn ? c.y : c.w;
-      };
+    if (warp == 9) {
+      // ---------------------------------------------------------- records
       // bound of |x|: 8 s + |least + 8 s|; not finite: the row stands for NaN
       auto bound = [](uint32_t m) { return fmaf(8.f, bf_lo(m), fabsf(fmaf(8.f, bf_lo(m), bf_hi(m)))); };
       auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
-      uint32_t rk_sent = 0, rv_sent = 0;       // tiles whose copies were issued
       while (ok && next_segment()) {
         const hattn::Pages pages(p, sg);
-        const int T = sg.u1 - sg.u0, first = 2 * sg.u0, kv = sg.rq.kv, head = sg.h;
+        const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
         uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
-        // ---- copies (warp 9): tile j of the segment.  The ring's place is free
-        // once all producers are done with the tile two before it.
-        auto send = [&](int j, bool is_v) -> bool {
+        // page numbers are read two tiles ahead, scales one
+        int page[2], ppos[2], pos[2];
+        uint32_t mk[4], mv[4];
+        auto look = [&](int j) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            int blk = -1;
+            page[e] = j < T ? pages.page(first + 2 * j + e, blk, lane == 0) : -1;
+            ppos[e] = page[e] >= 0 ? blk * kPage : 0x7fffffff;
+          }
+        };
+        auto fetch = [&]() {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = k >> 1, key = (k & 1) * 32 + lane;
+            mk[k] = mv[k] = 0u;                // tokens past the end: scale and h 0
+            if (page[e] >= 0 && key < pages.kv - ppos[e]) {
+              const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                  p.data + ((size_t)page[e] * p.Hkv + head) * page_bytes(D) + kPage * D) + key;
+              mk[k] = __ldg(src);
+              mv[k] = __ldg(src + kPage);
+            }
+          }
+          pos[0] = ppos[0];
+          pos[1] = ppos[1];
+        };
+        look(0);
+        fetch();
+        look(1);
+        for (int j = 0; j < T; ++j) {
           const uint32_t n = n0 + j;
-          if (!wait_warp(is_v ? rv_empty(n) : rk_empty(n), ((n >> 1) & 1) ^ 1, ctl)) return false;
-          const uint32_t full = is_v ? rv_full(n) : rk_full(n);
-          int blk[2], page[2];
+          if (!(ok = wait_warp(tile_empty(n), ((n / kRing) & 1) ^ 1, ctl))) break;
+          Tile &tile = tiles[n % kRing];
+          uint32_t ktop = 0, vtop = 0;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) page[e] = pages.page(first + 2 * j + e, blk[e], !is_v && lane == 0);
+          for (int k = 0; k < 4; ++k) {
+            const float kb = bound(mk[k]), vb = bound(mv[k]);
+            if (kb < INFINITY) ktop = max(ktop, __float_as_uint(kb));
+            const bool bad = !(vb < INFINITY);
+            if (bad) mv[k] = 0u; else vtop = max(vtop, __float_as_uint(vb));
+            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+            if (lane == 0) tile.bad[k] = word;
+          }
+          const uint32_t kref_bits = reference(__reduce_max_sync(0xffffffffu, ktop));
+          vref_bits = max(vref_bits, reference(__reduce_max_sync(0xffffffffu, vtop)));
+          const float kdown = __uint_as_float((254u << 23) - kref_bits), vdown = __uint_as_float((254u << 23) - vref_bits);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = k * 32 + lane;
+            const float ks = bf_lo(mk[k]), vs = bf_lo(mv[k]);
+            tile.ks[key] = hattn::pack_f16x2(ks * kdown, ks * kdown);
+            tile.kh[key] = fmaf(8.f, ks, bf_hi(mk[k])) * kdown;
+            const float vh = fmaf(8.f, vs, bf_hi(mv[k])) * vdown;
+            tile.v[key] = make_uint2(hattn::pack_f16x2(vs * vdown, vs * vdown), hattn::pack_f16x2(vh, vh));
+          }
           if (lane == 0) {
-            const uint32_t each = C::CODES + (is_v ? 0 : C::META);
-            mbar_arrive_expect_tx(full, ((page[0] >= 0) + (page[1] >= 0)) * each);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (page[e] < 0) continue;
-              const uint8_t *src = p.data + ((size_t)page[e] * p.Hkv + head) * page_bytes(D);
-              bulk_load(sbase + (is_v ? C::OFF_RV : C::OFF_RK) + (2 * (n & 1) + e) * C::CODES,
-                        src + (is_v ? C::CODES : 0), C::CODES, full);
-              if (!is_v)
-                bulk_load(sbase + C::OFF_RM + (2 * (n % kRing) + e) * C::META, src + 2 * C::CODES, C::META, full);
-            }
-            if (!is_v) {
-              tiles[n % kRing].pos[0] = page[0] >= 0 ? blk[0] * kPage : 0x7fffffff;
-              tiles[n % kRing].pos[1] = page[1] >= 0 ? blk[1] * kPage : 0x7fffffff;
-            }
+            tile.kref = __uint_as_float(kref_bits);
+            tile.vref = __uint_as_float(vref_bits);
+            tile.pos[0] = pos[0];
+            tile.pos[1] = pos[1];
           }
           __syncwarp();
-          if (is_v) ++rv_sent; else ++rk_sent;
-          return true;
-        };
-        // (scale, least) of key `key` of tile n, 0 where there is no token
-        auto meta = [&](uint32_t n, int key, int is_v) -> uint32_t {
-          const int e = key >= kPage ? 1 : 0;
-          const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + C::OFF_RM + (2 * (n % kRing) + e) * C::META);
-          const uint32_t m = src[is_v * kPage + key % kPage];
-          return key % kPage < kv - tiles[n % kRing].pos[e] ? m : 0u;
-        };
-        if (warp == 9) {
-          for (int j = 0; j < 2 && j < T && ok; ++j) ok = send(j, false) && send(j, true);
-          if (!ok) break;
-        }
-        for (int j = 0; j <= T && ok; ++j) {
-          if (j < T) {
-            // ---- K of tile j
-            const uint32_t n = n0 + j;
-            if (warp == 9 && j >= 1 && j + 1 < T) {
-              // K's place was freed by K of tile j - 1, V's by V of tile j - 2
-              if (!(ok = send(j + 1, false))) break;
-              if (j >= 2 && !(ok = send(j, true))) break;
-            }
-            if (warp == 9 && j >= 2 && j + 1 == T && !(ok = send(j, true))) break;
-            if (!(ok = wait_warp(rk_full(n), (n >> 1) & 1, ctl))) break;
-            if (warp == 9) {
-              Tile &tile = tiles[n % kRing];
-              uint32_t ktop = 0, vtop = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float kb = bound(meta(n, k * 32 + lane, 0)), vb = bound(meta(n, k * 32 + lane, 1));
-                if (kb < INFINITY) ktop = max(ktop, __float_as_uint(kb));
-                const bool bad = !(vb < INFINITY);
-                if (!bad) vtop = max(vtop, __float_as_uint(vb));
-                const uint32_t word = __ballot_sync(0xffffffffu, bad);
-                if (lane == 0) tile.bad[k] = word;
-              }
-              ktop = __reduce_max_sync(0xffffffffu, ktop);
-              vtop = __reduce_max_sync(0xffffffffu, vtop);
-              vref_bits = max(vref_bits, reference(vtop));
-              if (lane == 0) {
-                tile.kref = __uint_as_float(reference(ktop));
-                tile.vref = __uint_as_float(vref_bits);
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(tile_full(n));
-            }
-            if (!(ok = wait_warp(tile_full(n), (n / kRing) & 1, ctl))) break;
-            if (!(ok = wait_warp(k_empty(n), ((n >> 1) & 1) ^ 1, ctl))) break;
-            const float down = 1.f / tiles[n % kRing].kref;
-            const uint8_t *src = smem + C::OFF_RK + 2 * (n & 1) * C::CODES + row0 * (D / 2) + part * 16;
-            const int off = C::OFF_K + (n & 1) * C::TILE;
-#pragma unroll
-            for (int k = 0; k < C::LOADS; ++k) {
-              const int row = row0 + k * C::STEP;
-              if (row < BN) {
-                const uint32_t m = meta(n, row, 0);
-                const float s = bf_lo(m) * down;
-                const uint32_t s2 = hattn::pack_f16x2(s, s);
-                uint32_t w[4];
-                words(src + k * C::STEP * (D / 2), w);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  uint32_t x[4];
-                  hattn::unpack8(w[q], x);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], s2, 0x80008000u);
-                  *reinterpret_cast<uint4 *>(place(off, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-                if (part == 0) {       // h against sum(q) = (1 1 2 1 3 2): 1 2 1 3 1 2
-                  float h1, h2, h3;
-                  split3(fmaf(8.f, bf_lo(m), bf_hi(m)) * down, h1, h2, h3);
-                  const uint32_t h12 = hattn::pack_f16x2(h1, h2), h13 = hattn::pack_f16x2(h1, h3);
-                  reinterpret_cast<uint4 *>(smem + C::OFF_KA + (n & 1) * C::AUG)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
-                }
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(k_full(n));
-              mbar_arrive(rk_empty(n));
-            }
-          }
-          if (j >= 1) {
-            // ---- V of tile j - 1
-            const uint32_t n = n0 + j - 1;
-            if (!(ok = wait_warp(rv_full(n), (n >> 1) & 1, ctl))) break;
-            if (!(ok = wait_warp(v_empty, (n & 1) ^ 1, ctl))) break;
-            const float down = 1.f / tiles[n % kRing].vref;
-            const uint8_t *src = smem + C::OFF_RV + 2 * (n & 1) * C::CODES + row0 * (D / 2) + part * 16;
-#pragma unroll
-            for (int k = 0; k < C::LOADS; ++k) {
-              const int row = row0 + k * C::STEP;
-              if (row < BN) {
-                uint32_t m = meta(n, row, 1);
-                if (!(bound(m) < INFINITY)) m = 0;
-                const float s = bf_lo(m) * down, hh = fmaf(8.f, bf_lo(m), bf_hi(m)) * down;
-                const uint32_t s2 = hattn::pack_f16x2(s, s), h2 = hattn::pack_f16x2(hh, hh);
-                uint32_t w[4];
-                words(src + k * C::STEP * (D / 2), w);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  uint32_t x[4];
-                  hattn::unpack8(w[q], x);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], s2, h2);
-                  *reinterpret_cast<uint4 *>(place(C::OFF_V, q) + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(v_full);
-              mbar_arrive(rv_empty(n));
-            }
-          }
+          if (lane == 0) mbar_arrive(tile_full(n));
+          fetch();
+          look(j + 2);
         }
         n0 += T;
       }
-      // every copy issued lands before the warp exits, on both paths
-      if (warp == 9) {
-        volatile int never = 0;
-        WaitCtl drain{&never, nullptr, 100000000LL};
-        for (uint32_t n = rk_sent > 2 ? rk_sent - 2 : 0; n < rk_sent; ++n) wait_bounded(rk_full(n), (n >> 1) & 1, drain);
-        for (uint32_t n = rv_sent > 2 ? rv_sent - 2 : 0; n < rv_sent; ++n) wait_bounded(rv_full(n), (n >> 1) & 1, drain);
+    } else if (warp >= 10) {
+      // ---------------------------------------------------------- producers
+      const bool is_v = warp >= 13;
+      const int pt = threadIdx.x - (is_v ? 416 : 320);
+      const int row0 = pt / C::PARTS, part = pt % C::PARTS;
+      // 8 channels (word w of the piece) of key row0, 128-byte swizzled
+      auto place = [&](int w) {
+        const int atom = (part & 1) * 4 + (part >= 2 ? w ^ 2 : w);
+        return (part >> 1) * C::CHUNK + row0 * 128 + ((atom ^ (row0 & 7)) << 4);
+      };
+      const int at[4] = {place(0), place(1), place(2), place(3)};
+      const int from = (is_v ? kPage * D / 2 : 0) + row0 * (D / 2) + part * 16;
+      while (ok && next_segment()) {
+        const hattn::Pages pages(p, sg);
+        const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
+        // page numbers are read two tiles ahead, codes one
+        int page[2];
+        auto look = [&](int j) {
+          int blk;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) page[e] = j < T ? pages.page(first + 2 * j + e, blk, false) : -1;
+        };
+        uint4 c[C::LOADS];
+        auto fetch = [&](int k) {
+          const int row = row0 + k * C::STEP, e = row >= kPage;
+          const int pg = e ? page[1] : page[0];
+          c[k] = make_uint4(0, 0, 0, 0);
+          if (row < BN && pg >= 0)
+            c[k] = __ldg(reinterpret_cast<const uint4 *>(p.data + ((size_t)pg * p.Hkv + head) * page_bytes(D) + from +
+                                                         k * C::STEP * (D / 2) - (e ? kPage * D / 2 : 0)));
+        };
+        look(0);
+#pragma unroll
+        for (int k = 0; k < C::LOADS; ++k) fetch(k);
+        look(1);
+        for (int j = 0; j < T; ++j) {
+          const uint32_t n = n0 + j;
+          if (!(ok = wait_warp(tile_full(n), (n / kRing) & 1, ctl))) break;
+          if (!(ok = wait_warp(is_v ? v_empty(n) : k_empty(n), ((n >> 1) & 1) ^ 1, ctl))) break;
+          const Tile &tile = tiles[n % kRing];
+          uint8_t *dst = smem + (is_v ? C::OFF_V : C::OFF_K) + (n & 1) * C::TILE;
+#pragma unroll
+          for (int k = 0; k < C::LOADS; ++k) {
+            const int row = row0 + k * C::STEP;
+            if (row < BN) {
+              // K: s (c - 8), exactly; V: s (c - 8) + h
+              const uint2 sh = is_v ? tile.v[row] : make_uint2(tile.ks[row], 0x80008000u);
+              const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t x[4];
+                hattn::unpack8(w[q], x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], sh.x, sh.y);
+                *reinterpret_cast<uint4 *>(dst + at[q] + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+            fetch(k);                  // the next tile's
+          }
+          if (!is_v) {
+            // h against sum(q) = (1 1 2 1 3 2): 1 2 1 3 1 2
+            for (int row = pt; row < BN; row += kProducers) {
+              float h1, h2, h3;
+              split3(tile.kh[row], h1, h2, h3);
+              const uint32_t h12 = hattn::pack_f16x2(h1, h2), h13 = hattn::pack_f16x2(h1, h3);
+              reinterpret_cast<uint4 *>(smem + C::OFF_KA + (n & 1) * C::AUG)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(is_v ? v_full(n) : k_full(n));
+          look(j + 2);
+        }
+        n0 += T;
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
@@ -443,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           tc_commit(s_full(k));
         }
       };
-      auto pv = [&](int k, bool acc) {
-        const uint64_t b = smem_desc_sw128(sbase + C::OFF_V, C::CHUNK, 1024);
+      auto pv = [&](int k, uint32_t n, bool acc) {
+        const uint64_t b = smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
@@ -469,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         for (int t = 0; t < T && ok; ++t) {
           const uint32_t n = n0 + t;
           const bool more = t + 1 < T;
-          if (!(ok = wait_warp(v_full, n & 1, ctl))) break;
+          if (!(ok = wait_warp(v_full(n), (n >> 1) & 1, ctl))) break;
           if (!(ok = wait_warp(p_full(0), n & 1, ctl))) break;
           tc_fence_after();
-          pv(0, t > 0);
+          pv(0, n, t > 0);
           if (!more) commit_by(leader, o_full(0));
           if (more) {
             if (!(ok = wait_warp(k_full(n + 1), ((n + 1) >> 1) & 1, ctl))) break;
@@ -484,14 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             if (!(ok = wait_warp(p_full(1), pc1 & 1, ctl))) break;
             ++pc1;
             tc_fence_after();
-            pv(1, t > 0);
+            pv(1, n, t > 0);
             if (!more) commit_by(leader, o_full(1));
             if (more) {
               qk(1, n + 1);
               commit_by(leader, k_empty(n + 1));
             }
           }
-          commit_by(leader, v_empty);
+          commit_by(leader, v_empty(n));
+          commit_by(leader, tile_empty(n));
         }
         n0 += T;
       }
@@ -551,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       for (int k = 0; k < D / 8; ++k) {
         uint32_t x[4];
         hattn::q_pairs(u[k], down, x, qsum);
-        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + kt * C::TILE + (k >> 3) * C::CHUNK + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + kt * C::TILE + (k >> 3) * C::CHUNK + r * 128 +
+                                  ((((k & 7) ^ (k >= 8 ? 2 : 0)) ^ (r & 7)) << 4)) =
             make_uint4(x[0], x[1], x[2], x[3]);
       }
       mul = p.scale_log2 * __uint_as_float(ex << 23);
@@ -617,14 +590,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           l *= alpha;
           m_used = m_new;
           const float ao = alpha * (vref / v_now);
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tO + c * 32, v);
+          // 16 columns at a time, one piece after the other: the scores hold the registers
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t v[16];
+            tmem_ld16p(tO + c, v);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * ao);
-            tmem_st32(tO + c * 32, v);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * ao);
+            tmem_st8(tO + c, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+            tmem_st8(tO + c + 8, v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]);
           }
         }
       }
@@ -689,8 +664,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 32; ++e) ov[e] = 0u;
       }
-      // columns 8 g + 2 i and 8 g + 2 i + 1 are channels 8 g + i and 8 g + 4 + i
-      auto val = [&](int ch) { return __uint_as_float(ov[(ch & ~7) + ((ch & 3) << 1) + ((ch >> 2) & 1)]) * fac; };
+      // columns 8 g + 2 i and 8 g + 2 i + 1 are channels 8 g + i and 8 g + 4 + i,
+      // of the second 64 those of group g ^ 2
+      auto val = [&](int ch) {
+        return __uint_as_float(ov[((ch & ~7) ^ (c >= 2 ? 16 : 0)) + ((ch & 3) << 1) + ((ch >> 2) & 1)]) * fac;
+      };
       if (!whole || p.out_fp32) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)

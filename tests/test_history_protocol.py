@@ -1,6 +1,6 @@
 """CPU model of the barrier protocol of the kernel of many query rows over the
-4-bit history (history_chunk.cu): the producer warps, the copies, the MMA warp
-and the two softmax warpgroups as processes over mbarriers with phases and
+4-bit history (history_chunk.cu): the record warp, the K and V producers, the MMA
+warp and the two softmax warpgroups as processes over mbarriers with phases and
 parities, run under random interleavings.
 
 Checked: every run ends (no deadlock); a wait on a parity that passes passes for
@@ -12,23 +12,15 @@ import pytest
 
 
 class Bar:
-    """An mbarrier: phase counter, arrivals expected per phase, bytes pending."""
+    """An mbarrier: phase counter and the arrivals that the phase still expects."""
 
     def __init__(self, count):
-        self.count, self.left, self.phase, self.pending = count, count, 0, 0
+        self.count, self.left, self.phase = count, count, 0
 
-    def arrive(self, tx=0):
+    def arrive(self):
         assert self.left > 0, "more arrivals than the phase expects"
         self.left -= 1
-        self.pending += tx
-        self._maybe()
-
-    def complete(self, tx):
-        self.pending -= tx
-        self._maybe()
-
-    def _maybe(self):
-        if self.left == 0 and self.pending == 0:
+        if self.left == 0:
             self.phase += 1
             self.left = self.count
 
@@ -44,15 +36,12 @@ class Model:
         two = lambda c: [Bar(c), Bar(c)]  # noqa: E731
         self.q_full, self.k_full, self.k_empty = two(4), two(3), two(1)
         self.s_full, self.p_full, self.o_full = two(1), two(4), two(1)
-        self.rk_full, self.rv_full, self.rk_empty, self.rv_empty = two(1), two(1), two(3), two(3)
-        self.v_full, self.v_empty = Bar(3), Bar(1)
+        self.v_full, self.v_empty = two(3), two(1)
         self.tile_full = [Bar(1) for _ in range(4)]
+        self.tile_empty = [Bar(1) for _ in range(4)]
         self.part, self.join = two(4), two(1)
         self.mma = []            # issued products and commits, in order
-        self.copies = []
-        self.raw_k, self.raw_v, self.meta = {}, {}, {}
-        self.K, self.V, self.S, self.P, self.O, self.Q = {}, {}, {}, {}, {}, {}
-        self.done_tiles = [set(), set()]
+        self.record, self.K, self.V, self.S, self.P, self.O, self.Q = {}, {}, {}, {}, {}, {}, {}
 
     # a wait for phase `index` of the barrier: by parity, and checked
     def wait(self, bar, index):
@@ -61,49 +50,24 @@ class Model:
         assert bar.phase >= index + 1, "a wait passed before its phase"
         assert bar.phase <= index + 2
 
-    def producer(self, w):
-        n0 = 0
-        for T, has1, part in self.segs:
-            def send(j, is_v):
-                n = n0 + j
-                yield from self.wait_free(self.rv_empty[n & 1] if is_v else self.rk_empty[n & 1], n >> 1)
-                full = self.rv_full[n & 1] if is_v else self.rk_full[n & 1]
-                full.arrive(1)
-                self.copies.append((full, n, is_v))
-            if w == 0:
-                for j in range(min(2, T)):
-                    yield from send(j, False)
-                    yield from send(j, True)
-            for j in range(T + 1):
-                if j < T:
-                    n = n0 + j
-                    if w == 0 and j >= 1 and j + 1 < T:
-                        yield from send(j + 1, False)
-                        if j >= 2:
-                            yield from send(j, True)
-                    if w == 0 and j >= 2 and j + 1 == T:
-                        yield from send(j, True)
-                    yield from self.wait(self.rk_full[n & 1], n >> 1)
-                    if w == 0:
-                        assert self.meta[n % 4] == n
-                        self.tile_full[n % 4].arrive()
-                    yield from self.wait(self.tile_full[n % 4], n >> 2)
-                    yield from self.wait_free(self.k_empty[n & 1], n >> 1)
-                    assert self.raw_k[n & 1] == n and self.meta[n % 4] == n
-                    yield
-                    self.K[n & 1] = n
-                    self.k_full[n & 1].arrive()
-                    self.rk_empty[n & 1].arrive()
-                if j >= 1:
-                    n = n0 + j - 1
-                    yield from self.wait(self.rv_full[n & 1], n >> 1)
-                    yield from self.wait_free(self.v_empty, n)
-                    assert self.raw_v[n & 1] == n and self.meta[n % 4] == n
-                    yield
-                    self.V[0] = n
-                    self.v_full.arrive()
-                    self.rv_empty[n & 1].arrive()
-            n0 += T
+    def recorder(self):
+        for n in range(sum(T for T, _, _ in self.segs)):
+            yield from self.wait_free(self.tile_empty[n % 4], n >> 2)
+            yield
+            self.record[n % 4] = n
+            self.tile_full[n % 4].arrive()
+
+    def producer(self, is_v):
+        buf = self.V if is_v else self.K
+        full, empty = (self.v_full, self.v_empty) if is_v else (self.k_full, self.k_empty)
+        for n in range(sum(T for T, _, _ in self.segs)):
+            yield from self.wait(self.tile_full[n % 4], n >> 2)
+            yield from self.wait_free(empty[n & 1], n >> 1)
+            assert self.record[n % 4] == n
+            yield
+            assert self.record[n % 4] == n
+            buf[n & 1] = n
+            full[n & 1].arrive()
 
     def wait_free(self, bar, use):
         """A place's `use`-th use: free once its (use - 1)-th was released."""
@@ -128,7 +92,7 @@ class Model:
             self.mma.append(("commit", self.k_empty[n0 & 1]))
             for t in range(T):
                 n, more = n0 + t, t + 1 < T
-                yield from self.wait(self.v_full, n)
+                yield from self.wait(self.v_full[n & 1], n >> 1)
                 yield from self.wait(self.p_full[0], n)
                 self.mma.append(("pv", 0, n))
                 if not more:
@@ -136,6 +100,8 @@ class Model:
                 if more:
                     yield from self.wait(self.k_full[(n + 1) & 1], (n + 1) >> 1)
                     qk(0, n + 1)
+                    if not has1:
+                        self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
                 if has1:
                     yield from self.wait(self.p_full[1], pc1)
                     pc1 += 1
@@ -144,9 +110,9 @@ class Model:
                         self.mma.append(("commit", self.o_full[1]))
                     if more:
                         qk(1, n + 1)
-                self.mma.append(("commit", self.v_empty))
-                if more:
-                    self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
+                        self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
+                self.mma.append(("commit", self.v_empty[n & 1]))
+                self.mma.append(("commit", self.tile_empty[n % 4]))
             n0 += T
 
     def softmax(self, kt, w):
@@ -160,9 +126,9 @@ class Model:
             for u in range(T):
                 yield from self.wait(self.s_full[kt], sc)
                 yield from self.wait(self.tile_full[n % 4], n >> 2)
-                assert self.meta[n % 4] == n and self.S[kt] == n
+                assert self.record[n % 4] == n and self.S[kt] == n
                 yield
-                assert self.S[kt] == n and self.meta[n % 4] == n
+                assert self.S[kt] == n and self.record[n % 4] == n
                 self.P[kt, w] = n
                 self.p_full[kt].arrive()
                 n += 1
@@ -186,14 +152,8 @@ class Model:
             n -= T
 
     def hardware(self):
-        """Copies land and products run, in order, at any time."""
-        if self.copies and (not self.mma or self.rng.random() < 0.5):
-            full, n, is_v = self.copies.pop(self.rng.randrange(len(self.copies)))
-            (self.raw_v if is_v else self.raw_k)[n & 1] = n
-            if not is_v:
-                self.meta[n % 4] = n
-            full.complete(1)
-        elif self.mma:
+        """Products run in order, at any time."""
+        if self.mma:
             op = self.mma.pop(0)
             if op[0] == "commit":
                 op[1].arrive()
@@ -204,16 +164,17 @@ class Model:
                 self.S[k] = n
             else:
                 _, k, n = op
-                assert self.V[0] == n and all(self.P[k, w] == n for w in range(4))
+                assert self.V[n & 1] == n and all(self.P[k, w] == n for w in range(4))
                 s, t = self.seg_of(n)
                 assert t == 0 or self.O[k] == (s, t)
                 self.O[k] = (s, t + 1)
 
     def run(self):
-        procs = [self.producer(w) for w in range(3)] + [self.issuer()]
+        procs = [self.producer(v) for v in (False, True) for _ in range(3)]
+        procs += [self.recorder(), self.issuer()]
         procs += [self.softmax(kt, w) for kt in range(2) for w in range(4)]
         idle = 0
-        while procs or self.mma or self.copies:
+        while procs or self.mma:
             if self.rng.random() < 0.3:
                 self.hardware()
                 continue
@@ -228,7 +189,7 @@ class Model:
                 procs.remove(p)
                 idle = 0
                 continue
-            idle = 0 if self.state() != before or self.mma or self.copies else idle + 1
+            idle = 0 if self.state() != before or self.mma else idle + 1
             assert idle < 3000, "deadlock"
 
     def state(self):
