@@ -395,12 +395,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
+      // The whole warp runs the loop; one elected lane issues and commits.  What
+      // a product or commit names (descriptors, barriers) is formed by the whole
+      // warp before that lane's branch, and kept from moving into it: these
+      // operands are uniform registers.
       const bool leader = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16_f32(BM, BN, 0);
       constexpr uint32_t idesc_pv = idesc_f16_f32(BM, D, 1);
+      auto fix32 = [](uint32_t x) {
+        asm volatile("mov.b32 %0, %0;" : "+r"(x));
+        return x;
+      };
+      auto fix64 = [](uint64_t x) {
+        asm volatile("mov.b64 %0, %0;" : "+l"(x));
+        return x;
+      };
+      auto commit = [&](uint32_t at) {
+        at = fix32(at);
+        if (leader) tc_commit(at);
+      };
       auto qk = [&](int k, uint32_t n) {
-        uint64_t a = smem_desc_sw128(sbase + C::OFF_Q + k * C::TILE, 16, 1024);
-        uint64_t b = smem_desc_sw128(sbase + C::OFF_K + (n & 1) * C::TILE, 16, 1024);
+        const uint64_t a = fix64(smem_desc_sw128(sbase + C::OFF_Q + k * C::TILE, 16, 1024));
+        const uint64_t b = fix64(smem_desc_sw128(sbase + C::OFF_K + (n & 1) * C::TILE, 16, 1024));
+        const uint64_t qa = fix64(smem_desc_plain(sbase + C::OFF_QA + k * C::AUG, 128, 256));
+        const uint64_t ka = fix64(smem_desc_plain(sbase + C::OFF_KA + (n & 1) * C::AUG, 128, 256));
+        const uint32_t full = fix32(s_full(k));
         // S_k = Q_k K^T.  P of the tile before lives in S_k: its product was
         // issued before, and one thread's products run in order.
         if (leader) {
@@ -409,17 +428,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
             mma_ss(tmem + 128 * k, a + off, b + off, idesc_qk, kk > 0);
           }
-          mma_ss(tmem + 128 * k, smem_desc_plain(sbase + C::OFF_QA + k * C::AUG, 128, 256),
-                 smem_desc_plain(sbase + C::OFF_KA + (n & 1) * C::AUG, 128, 256), idesc_qk, 1);
-          tc_commit(s_full(k));
+          mma_ss(tmem + 128 * k, qa, ka, idesc_qk, 1);
+          tc_commit(full);
         }
       };
       auto pv = [&](int k, uint32_t n, bool acc) {
-        const uint64_t b = smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024);
+        const uint64_t b = fix64(smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024));
+        const uint32_t accumulate = fix32(acc ? 1u : 0u);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + 256 + 128 * k, tmem + 128 * k + kk * 8, b + (uint64_t)((kk * 2048) >> 4), idesc_pv, acc || kk > 0);
+            mma_ts(tmem + 256 + 128 * k, tmem + 128 * k + kk * 8, b + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                   kk > 0 ? 1u : accumulate);
         }
       };
       uint32_t segs = 0, segs1 = 0, pc1 = 0;
@@ -436,41 +456,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         tc_fence_after();
         qk(0, n0);
         if (has1) qk(1, n0);
-        commit_by(leader, k_empty(n0));
-        for (int t = 0; t < T && ok; ++t) {
+        commit(k_empty(n0));
+        for (int t = 0; t < T; ++t) {
           const uint32_t n = n0 + t;
           const bool more = t + 1 < T;
           if (!(ok = wait_warp(v_full(n), (n >> 1) & 1, ctl))) break;
           if (!(ok = wait_warp(p_full(0), n & 1, ctl))) break;
           tc_fence_after();
           pv(0, n, t > 0);
-          if (!more) commit_by(leader, o_full(0));
           if (more) {
             if (!(ok = wait_warp(k_full(n + 1), ((n + 1) >> 1) & 1, ctl))) break;
             tc_fence_after();
             qk(0, n + 1);
-            if (!has1) commit_by(leader, k_empty(n + 1));
+          } else {
+            commit(o_full(0));
           }
           if (has1) {
             if (!(ok = wait_warp(p_full(1), pc1 & 1, ctl))) break;
             ++pc1;
             tc_fence_after();
             pv(1, n, t > 0);
-            if (!more) commit_by(leader, o_full(1));
-            if (more) {
-              qk(1, n + 1);
-              commit_by(leader, k_empty(n + 1));
-            }
+            if (more) qk(1, n + 1);
+            else commit(o_full(1));
           }
-          commit_by(leader, v_empty(n));
-          commit_by(leader, tile_empty(n));
+          if (more) commit(k_empty(n + 1));
+          commit(v_empty(n));
+          commit(tile_empty(n));
         }
         n0 += T;
       }
       // what was issued ends before TMEM is released, on both paths
       volatile int never = 0;
       WaitCtl drain{&never, nullptr, 100000000LL};
-      if (leader) tc_commit(drain_bar);
+      commit(drain_bar);
       wait_bounded(drain_bar, 0, drain);
       __syncwarp();
     }

@@ -100,8 +100,6 @@ class Model:
                 if more:
                     yield from self.wait(self.k_full[(n + 1) & 1], (n + 1) >> 1)
                     qk(0, n + 1)
-                    if not has1:
-                        self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
                 if has1:
                     yield from self.wait(self.p_full[1], pc1)
                     pc1 += 1
@@ -110,7 +108,8 @@ class Model:
                         self.mma.append(("commit", self.o_full[1]))
                     if more:
                         qk(1, n + 1)
-                        self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
+                if more:
+                    self.mma.append(("commit", self.k_empty[(n + 1) & 1]))
                 self.mma.append(("commit", self.v_empty[n & 1]))
                 self.mma.append(("commit", self.tile_empty[n % 4]))
             n0 += T
