@@ -5,9 +5,8 @@
 //   q.k_j = s_j (q.(c_j - 8)) + h_j sum(q)
 //   O     = sum_j (p_j s'_j) (c'_j - 8) + sum_j p_j h'_j
 // so that the 4-bit codes enter the tensor core as they are.  Two codes become
-// a pair of fp16 numbers by one LOP3 (1024 + c, or 1024 + 16 c for every other
-// code; one shift serves four) and one packed FMA that leaves c - 8, exactly;
-// scales and h are applied to scores and probabilities in fp32.  fp16 and not
+// a pair of fp16 numbers by one LOP3 and one packed addition that leaves c - 8,
+// exactly; scales and h are applied to scores and probabilities in fp32.  fp16 and not
 // bf16: its longer significand takes two codes in place, and it rounds p s' to
 // 2^-11.  Q is scaled by a power of two a row to lie below 2 (an exact step for
 // all but values 2^-24 of the row's largest), p s' by one that follows the
@@ -89,7 +88,7 @@ struct WarpTile {
 
 // One page: 64 keys of one head, codes and scales at st.
 template <int D, int NR, bool MASKED>
-__device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const uint8_t *st, int k_base, int kv) {
+__device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base, int kv) {
   using T = WarpTile<D, NR>;
   const int lane = threadIdx.x & 31, t = lane & 3, n8 = lane >> 2;
   const int kn = key_of(n8);
@@ -322,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   uint32_t it = 0;                  // pages this warp has consumed (ring position and phase)
   bool ok = true;
 
+  const Unpack unpack8;
   Walk<TR, 1> walk;
   walk.start(p, g);
   Segment sg;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
 
     WT w;
     // Q: the lane holds row n8 (+ 8) as the second operand, channels in the
-    // order in which unpack8 gives the codes, scaled to lie below 2
+    // order in which Unpack gives the codes, scaled to lie below 2
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const int row = n8 + 8 * x;
@@ -423,9 +423,9 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       const uint8_t *st = ring + (it % NS) * S::kStage;
       const int k_base = blk[0] * kPage;
       if (k_base + kPage > vis_all)
-        page_step<D, NR, true>(w, st, k_base, rq.kv);
+        page_step<D, NR, true>(w, unpack8, st, k_base, rq.kv);
       else
-        page_step<D, NR, false>(w, st, k_base, rq.kv);
+        page_step<D, NR, false>(w, unpack8, st, k_base, rq.kv);
       ++it;
       __syncwarp();                 // every lane has read the page
 #pragma unroll

@@ -212,22 +212,45 @@ struct Pages {
   }
 };
 
-// Two codes a register: codes i and i + 4 of a word, i = 0..3, less 8, as fp16.
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&pair)[4]) {
-  const uint32_t kOne = 0x3c003c00u, k16th = 0x2c002c00u;            // 1, 1/16
-  const uint32_t kEven = 0xe408e408u, kOdd = 0xd480d480u;            // -1032, -72
-  const uint32_t v = w >> 8;
-  pair[0] = hfma2((w & 0x000f000fu) | 0x64006400u, kOne, kEven);     // 1024 + c
-  pair[1] = hfma2((w & 0x00f000f0u) | 0x64006400u, k16th, kOdd);     // 1024 + 16 c
-  pair[2] = hfma2((v & 0x000f000fu) | 0x64006400u, kOne, kEven);
-  pair[3] = hfma2((v & 0x00f000f0u) | 0x64006400u, k16th, kOdd);
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+
+// Two codes a register: codes i and i + 4 of a word, i = 0..3, less 8, as fp16.
+// Codes in bits 0-3 of a half go into the significand of 1024 (1024 + c), those
+// in bits 4-7 into that of 64 (64 + c): one shift serves four codes, one LOP3
+// and one addition two.  The masks and exponents are kept in registers that the
+// compiler cannot form again at each use: as literals they cost one more
+// instruction a pair, a third of the loop.
+struct Unpack {
+  uint32_t mask0, mask1, exp0, exp1;
+  __device__ __forceinline__ Unpack() {
+    asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(mask0));
+    asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(mask1));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(exp0));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(exp1));
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&pair)[4]) const {
+    const uint32_t k1032 = 0xe408e408u, k72 = 0xd480d480u;   // -1032, -72
+    const uint32_t v = w >> 8;
+    pair[0] = hadd2(pick(w, mask0, exp0), k1032);
+    pair[1] = hadd2(pick(w, mask1, exp1), k72);
+    pair[2] = hadd2(pick(v, mask0, exp0), k1032);
+    pair[3] = hadd2(pick(v, mask1, exp1), k72);
+  }
+  static __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t exp) {   // (w & mask) | exp
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(exp));
+    return r;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -235,7 +258,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Eight values of a row of Q (16 bytes) times `down`, paired as unpack8 pairs codes.
+// Eight values of a row of Q (16 bytes) times `down`, paired as Unpack pairs codes.
 __device__ __forceinline__ void q_pairs(const uint4 &u, float down, uint32_t (&pair)[4], float &sum) {
   const float f0 = bf_lo(u.x) * down, f1 = bf_hi(u.x) * down, f2 = bf_lo(u.y) * down, f3 = bf_hi(u.y) * down;
   const float f4 = bf_lo(u.z) * down, f5 = bf_hi(u.z) * down, f6 = bf_lo(u.w) * down, f7 = bf_hi(u.w) * down;

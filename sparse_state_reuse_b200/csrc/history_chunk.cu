@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         const int atom = (part & 1) * 4 + (part >= 2 ? w ^ 2 : w);
         return (part >> 1) * C::CHUNK + row0 * 128 + ((atom ^ (row0 & 7)) << 4);
       };
+      const hattn::Unpack unpack8;
       const int at[4] = {place(0), place(1), place(2), place(3)};
       const int from = (is_v ? kPage * D / 2 : 0) + row0 * (D / 2) + part * 16;
       while (ok && next_segment()) {
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 uint32_t x[4];
-                hattn::unpack8(w[q], x);
+                unpack8(w[q], x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = hattn::hfma2(x[e], sh.x, sh.y);
                 *reinterpret_cast<uint4 *>(dst + at[q] + k * C::STEP * 128) = make_uint4(x[0], x[1], x[2], x[3]);
