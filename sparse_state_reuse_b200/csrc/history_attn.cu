@@ -37,6 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;            // rows of a tile, at most
 constexpr int kMaxBlocks = 768;      // most blocks of a launch (the workspace has room for them)
+constexpr int kSetup = 8;            // pages that beginning and finishing an item counts for
 // p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
 // 2^6 more uses the range that is left.
 constexpr float kWeightScale = 64.f;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   }
 
   Range g;
-  if (!find_range<TR, 1, kThreads>(p, 1, g, s_scan, &s_request)) return;
+  if (!find_range<TR, 1, kSetup, kThreads>(p, 1, g, s_scan, &s_request)) return;
 
   uint8_t *ring = smem + warp * S::kWarpBytes;
   const uint32_t ring_s = smem_u32(ring);
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   bool ok = true;
 
   const Unpack unpack8;
-  Walk<TR, 1> walk;
+  Walk<TR, 1, kSetup> walk;
   walk.start(p, g);
   Segment sg;
   while (walk.next(p, sg)) {
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
         }
       }
       long long c1, cl;
-      sharers(g, sg, c1, cl);
+      sharers<kSetup>(g, sg, c1, cl);
       __threadfence();
       __syncthreads();
       if (tid == 0) {

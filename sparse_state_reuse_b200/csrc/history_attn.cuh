@@ -3,10 +3,13 @@
 //
 // The units (runs of pages) of all (request, row tile, key head) items are one
 // line of work that is cut into equal ranges, one a block, so that a single
-// long request and a ragged batch fill the GPU alike.  An item cut by a
-// boundary is joined by the block that finishes it last, from the partial
-// states in block order (a fixed order: the result does not depend on which
-// block is last).
+// long request and a ragged batch fill the GPU alike.  Each item stands on the
+// line with SETUP units more, what it costs to begin and to finish one (without
+// them a block that got many short requests worked 1.3 times as long as the
+// others); a boundary that falls among those moves to the item's start.  An item
+// cut by a boundary is joined by the block that finishes it last, from the
+// partial states in block order (a fixed order: the result does not depend on
+// which block is last).
 #pragma once
 
 #include "blocks.cuh"
@@ -59,8 +62,9 @@ __device__ __forceinline__ Request request_of(const Params &p, int r) {
   return q;
 }
 
+template <int SETUP>
 __device__ __forceinline__ long long work_of(const Params &p, const Request &q) {
-  return (long long)q.tiles * p.Hkv * q.units;
+  return (long long)q.tiles * p.Hkv * (q.units + SETUP);
 }
 
 // Sum and exclusive prefix over the block.
@@ -93,7 +97,7 @@ struct Range {
 };
 
 // All THREADS threads take part; sm: WARPS + 1 long longs and an int.
-template <int TR, int UNIT, int THREADS>
+template <int TR, int UNIT, int SETUP, int THREADS>
 __device__ __forceinline__ bool find_range(const Params &p, long long min_units, Range &g, long long *sm, int *sm_r) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x;
@@ -101,7 +105,7 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
   for (int base = 0; base < p.R; base += THREADS) {
     const int r = base + tid;
     long long sum;
-    block_scan<WARPS>(r < p.R ? work_of(p, request_of<TR, UNIT>(p, r)) : 0, sum, sm);
+    block_scan<WARPS>(r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0, sum, sm);
     g.total += sum;
   }
   const long long most = (g.total + min_units - 1) / min_units;
@@ -112,7 +116,7 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
   long long before = 0;
   for (int base = 0; base < p.R; base += THREADS) {
     const int r = base + tid;
-    const long long v = r < p.R ? work_of(p, request_of<TR, UNIT>(p, r)) : 0;
+    const long long v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
     long long sum;
     const long long at = before + block_scan<WARPS>(v, sum, sm);
     if (v > 0 && at <= g.w0 && g.w0 < at + v) {
@@ -132,11 +136,11 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
 struct Segment {
   Request rq;
   int r, h, tile, u0, u1;           // units [u0, u1) of the item
-  long long start;                  // of the item, on the line
+  long long start, end;             // of the item, on the line
   __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == rq.units; }
 };
 
-template <int TR, int UNIT>
+template <int TR, int UNIT, int SETUP>
 struct Walk {
   long long pos, w1, r_start;
   int r;
@@ -150,20 +154,24 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const Params &p, Segment &s) {
     if (pos >= w1) return false;
-    while (pos >= r_start + work_of(p, rq)) {
-      r_start += work_of(p, rq);
+    while (pos >= r_start + work_of<SETUP>(p, rq)) {
+      r_start += work_of<SETUP>(p, rq);
       ++r;
       rq = request_of<TR, UNIT>(p, r);
     }
-    const long long item = (pos - r_start) / rq.units;
+    const int cost = rq.units + SETUP;
+    const long long item = (pos - r_start) / cost;
     s.rq = rq;
     s.r = r;
-    s.start = r_start + item * rq.units;
+    s.start = r_start + item * cost;
+    s.end = s.start + cost;
     s.tile = (int)(item / p.Hkv);
     s.h = (int)(item % p.Hkv);
-    s.u0 = (int)(pos - s.start);
-    s.u1 = (int)(w1 - s.start < rq.units ? w1 - s.start : rq.units);
-    pos = s.start + s.u1;
+    const int from = (int)(pos - s.start), to = (int)(w1 < s.end ? w1 - s.start : cost);
+    if (to <= SETUP) return false;              // the boundary moves to the item's start
+    s.u0 = from < SETUP ? 0 : from - SETUP;
+    s.u1 = to - SETUP;
+    pos = s.start + to;
     return true;
   }
 };
@@ -171,9 +179,10 @@ struct Walk {
 // The blocks that share a cut item: the first boundary inside it belongs to
 // block `first`, so the parts are those of first - 1 (its second slot) and of
 // first ... last (their first slots).
+template <int SETUP>
 __device__ __forceinline__ void sharers(const Range &g, const Segment &s, long long &first, long long &last) {
-  first = ((s.start + 1) * g.n_blk + g.total - 1) / g.total;
-  last = ((s.start + s.rq.units) * g.n_blk + g.total - 1) / g.total - 1;
+  first = ((s.start + SETUP + 1) * g.n_blk + g.total - 1) / g.total;
+  last = (s.end * g.n_blk + g.total - 1) / g.total - 1;
 }
 
 // Pages of a request (or of its list): block e, its page or -1.  Blocks without

@@ -59,7 +59,8 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxBlocks = 160;      // most blocks of a launch (the workspace has room for them)
 // A block's share is at least this many tiles: below, joining the parts of an
 // item costs more than the shorter share saves.
-constexpr int kMinUnits = 4;
+constexpr int kMinUnits = 6;
+constexpr int kSetup = 2;            // tiles that beginning and finishing an item counts for
 
 // What is known of a tile before its codes are unpacked.
 constexpr int kRing = 4;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
   __shared__ int s_request, s_last[2];
   // each warp's place on the line; in shared memory, since the registers hold
   // scores and codes
-  using WalkT = hattn::Walk<TR, 2>;
+  using WalkT = hattn::Walk<TR, 2, kSetup>;
   __shared__ hattn::Range s_range;
   __shared__ WalkT s_walk[kThreads / 32];
   __shared__ hattn::Segment s_seg[kThreads / 32];
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 
   {
     hattn::Range g;
-    if (!hattn::find_range<TR, 2, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
+    if (!hattn::find_range<TR, 2, kSetup, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
     if (lane == 0) s_walk[warp].start(p, g);
     if (threadIdx.x == 0) s_range = g;
   }
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       part[BM * D + 2 * r + 1] = l;
     }
     long long first, last;
-    hattn::sharers(s_range, sg, first, last);
+    hattn::sharers<kSetup>(s_range, sg, first, last);
     __threadfence();
     __syncwarp();
     if (lane == 0) mbar_arrive(part_bar(kt));
