@@ -14,14 +14,16 @@
 //
 // Keys and channels are the rows of the products (m16n8k16, S^T = K Q^T and
 // O^T = V^T P^T) and query rows their 8 columns: 8 rows at a time, of which a
-// decode step has few.  P^T goes from the first product's layout to the
+// decode step has few.  A lane holds two neighbouring columns; up to four rows
+// take every other column, so that a lane exponentiates one.  P^T goes from the first product's layout to the
 // second's by a transpose of 8x8 tiles in registers.
 //
 // It is bound by the history's bytes, d + 8 a key and key head, as long as the
 // instructions that unpack them keep up.  Each warp is by itself: it takes
-// every fourth page of its block's range, fetches a page of one head (one
-// contiguous run) with one bulk copy into a ring of its own and works through
-// it; no block-wide barrier until the end of a range.  With so few rows the
+// every fourth page of its block's range and fetches each page of one head (one
+// contiguous run) with one bulk copy into one of two places of its own; no
+// block-wide barrier until the end of a range.  (K and V fetched apart, with
+// their scales, are four copies a page: 10% slower.)  With so few rows the
 // legacy tensor instructions are not what bounds it (30% of their rate), and a
 // tcgen05 tile of 128 rows would be mostly padding.
 #include <mutex>
@@ -63,18 +65,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-template <int D, int NS>
+template <int D>
 struct Smem {
   static constexpr int kStage = page_bytes(D);
-  static constexpr int kWarpBytes = NS * kStage;
+  static constexpr int kV = kPage * D / 2;       // in a page: V's codes,
+  static constexpr int kKMeta = kPage * D, kVMeta = kKMeta + kPage * 4;   // K's and V's (scale, least) pairs
   static constexpr int kMergeStride = D + 4;     // floats of a merged row: O, then m and l
+  static constexpr int kMerge = kRows * kMergeStride * 4;
+  static constexpr int kWarpBytes = 2 * kStage;  // two places; the join reuses them
   static constexpr int kBytes = kWarps * kWarpBytes;
-  static_assert(kRows * kMergeStride * 4 <= kWarpBytes, "the join reuses the ring");
+  static_assert(kWarpBytes >= kMerge, "the join reuses the places");
   static_assert(kStage % 16 == 0, "bulk copies");
 };
 
-// What a warp holds of a row tile of 8 NR rows: Q as the second operand of
-// K Q^T, O^T, and of its rows 2t, 2t + 1 (+ 8) the softmax state.
+// What a warp holds of a row tile: Q as the second operand of K Q^T, O^T, and of
+// its columns 2t, 2t + 1 (+ 8) the softmax state.  NR: groups of 8 columns; E:
+// columns of a lane and group that hold rows (1: the even columns only).
 template <int D, int NR>
 struct WarpTile {
   static constexpr int W = D / 32;   // words of K codes of a lane and key
@@ -87,14 +93,14 @@ struct WarpTile {
   float vref;                        // power of two that no V scale so far exceeds
 };
 
-// One page: 64 keys of one head, codes and scales at st.
-template <int D, int NR, bool MASKED>
-__device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base, int kv) {
+// Scores of the 64 keys of a page (at st) for the lane's columns, before
+// the column's factor: keys 16 u + {key_of(n8), 8 + key_of(n8)}.
+template <int D, int NR, int E, bool MASKED>
+__device__ __forceinline__ void page_scores(const WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base,
+                                            float (&sc)[4][NR][4]) {
   using T = WarpTile<D, NR>;
   const int lane = threadIdx.x & 31, t = lane & 3, n8 = lane >> 2;
   const int kn = key_of(n8);
-  // scores of keys 16 u + {kn, 8 + kn} for rows 2t, 2t + 1, before the row's factor
-  float sc[4][NR][4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
 #pragma unroll
@@ -129,44 +135,53 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpa
         mma16816(sc[u][x], pa[2], pb[2], pa[3], pb[3], w.q[x][2 * i + 1][0], w.q[x][2 * i + 1][1]);
       }
     }
-    const uint8_t *meta = st + kPage * D + (16 * u + kn) * 4;
+    const uint8_t *meta = st + Smem<D>::kKMeta + (16 * u + kn) * 4;
     const uint32_t ma = *reinterpret_cast<const uint32_t *>(meta), mb = *reinterpret_cast<const uint32_t *>(meta + 32);
     const float sa = bf_lo(ma), sb = bf_lo(mb);
     const float ha = fmaf(8.f, sa, bf_hi(ma)), hb = fmaf(8.f, sb, bf_hi(mb));
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      sc[u][x][0] = fmaf(sc[u][x][0], sa, ha * w.qsum[2 * x]);
-      sc[u][x][1] = fmaf(sc[u][x][1], sa, ha * w.qsum[2 * x + 1]);
-      sc[u][x][2] = fmaf(sc[u][x][2], sb, hb * w.qsum[2 * x]);
-      sc[u][x][3] = fmaf(sc[u][x][3], sb, hb * w.qsum[2 * x + 1]);
-    }
-    if constexpr (MASKED) {
-      const int key = k_base + 16 * u + kn;
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int x = 0; x < NR; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key + 8 * (e >> 1) >= w.vis[2 * x + (e & 1)]) sc[u][x][e] = -INFINITY;
-    }
+      for (int e = 0; e < E; ++e) {
+        sc[u][x][e] = fmaf(sc[u][x][e], sa, ha * w.qsum[2 * x + e]);
+        sc[u][x][2 + e] = fmaf(sc[u][x][2 + e], sb, hb * w.qsum[2 * x + e]);
+        if constexpr (MASKED) {
+          const int key = k_base + 16 * u + kn;
+          if (key >= w.vis[2 * x + e]) sc[u][x][e] = -INFINITY;
+          if (key + 8 >= w.vis[2 * x + e]) sc[u][x][2 + e] = -INFINITY;
+        }
+      }
   }
+}
+
+// The softmax step and the second product of a page (at st).
+template <int D, int NR, int E, bool MASKED>
+__device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base, int kv,
+                                            float (&sc)[4][NR][4]) {
+  using T = WarpTile<D, NR>;
+  const int lane = threadIdx.x & 31, t = lane & 3, n8 = lane >> 2;
+  const int kn = key_of(n8);
   // running maximum; O is rescaled only when it grew by more than 2^8
   bool need = false;
   float mx[2 * NR];
 #pragma unroll
-  for (int y = 0; y < 2 * NR; ++y) {
-    float v = -INFINITY;
+  for (int x = 0; x < NR; ++x)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v = fmaxf(v, fmaxf(sc[u][y >> 1][y & 1], sc[u][y >> 1][2 + (y & 1)]));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-    mx[y] = v * w.mul[y];
-    need = need || mx[y] > w.m[y] + kRescaleLog2;
-  }
+    for (int e = 0; e < E; ++e) {
+      const int y = 2 * x + e;
+      float v = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v = fmaxf(v, fmaxf(sc[u][x][e], sc[u][x][2 + e]));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+      mx[y] = v * w.mul[y];
+      need = need || mx[y] > w.m[y] + kRescaleLog2;
+    }
   // the largest V scale of the page (rows that stand for NaN have none)
   uint32_t top;
   {
-    const uint32_t *vm = reinterpret_cast<const uint32_t *>(st + kPage * D + kPage * 4);
+    const uint32_t *vm = reinterpret_cast<const uint32_t *>(st + Smem<D>::kVMeta);
     uint32_t a = vm[lane] & 0xffffu, b = vm[lane + 32] & 0xffffu;
     if constexpr (MASKED) {
       if (k_base + lane >= kv) a = 0u;
@@ -185,44 +200,53 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpa
   }
   if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-    for (int y = 0; y < 2 * NR; ++y) {
-      const float mn = fmaxf(w.m[y], mx[y]);
-      const float al = w.m[y] == mn ? 1.f : fast_ex2(w.m[y] - mn);
-      w.m[y] = mn;
-      w.l[y] *= al;
-      w.z[y] *= al;
-      const float ao = al * vmul;
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int j = 0; j < T::MT; ++j) {
-        w.o[y >> 1][j][y & 1] *= ao;
-        w.o[y >> 1][j][2 + (y & 1)] *= ao;
+      for (int e = 0; e < E; ++e) {
+        const int y = 2 * x + e;
+        const float mn = fmaxf(w.m[y], mx[y]);
+        const float al = w.m[y] == mn ? 1.f : fast_ex2(w.m[y] - mn);
+        w.m[y] = mn;
+        w.l[y] *= al;
+        w.z[y] *= al;
+        const float ao = al * vmul;
+#pragma unroll
+        for (int j = 0; j < T::MT; ++j) {
+          w.o[x][j][e] *= ao;
+          w.o[x][j][2 + e] *= ao;
+        }
       }
-    }
   }
   float neg[2 * NR], mul[2 * NR];
   bool huge = false;
 #pragma unroll
-  for (int y = 0; y < 2 * NR; ++y) {
-    neg[y] = w.m[y] > -INFINITY ? -w.m[y] : 0.f;   // no key so far: against 0
-    mul[y] = w.mul[y];
-    huge = huge || fabsf(neg[y]) > kHuge;
-  }
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int y = 2 * x + e;
+      neg[y] = w.m[y] > -INFINITY ? -w.m[y] : 0.f;   // no key so far: against 0
+      mul[y] = w.mul[y];
+      huge = huge || fabsf(neg[y]) > kHuge;
+    }
   if (__any_sync(0xffffffffu, huge)) {
 #pragma unroll
-    for (int y = 0; y < 2 * NR; ++y) {
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sc[u][y >> 1][y & 1] = __fmul_rn(sc[u][y >> 1][y & 1], mul[y]);
-        sc[u][y >> 1][2 + (y & 1)] = __fmul_rn(sc[u][y >> 1][2 + (y & 1)], mul[y]);
+      for (int e = 0; e < E; ++e) {
+        const int y = 2 * x + e;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          sc[u][x][e] = __fmul_rn(sc[u][x][e], mul[y]);
+          sc[u][x][2 + e] = __fmul_rn(sc[u][x][2 + e], mul[y]);
+        }
+        mul[y] = 1.f;
       }
-      mul[y] = 1.f;
-    }
   }
   const float vs = kWeightScale / w.vref;
-  // 16 keys at a time: p, the weights p s', and the second product
+  // 16 keys at a time: p, the weights p s', and the product
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const uint8_t *meta = st + kPage * D + kPage * 4 + (16 * u + kn) * 4;
+    const uint8_t *meta = st + Smem<D>::kVMeta + (16 * u + kn) * 4;
     const uint32_t ma = *reinterpret_cast<const uint32_t *>(meta), mb = *reinterpret_cast<const uint32_t *>(meta + 32);
     const float sa = bf_lo(ma), sb = bf_lo(mb);
     const float ha = fmaf(8.f, sa, bf_hi(ma)), hb = fmaf(8.f, sb, bf_hi(mb));
@@ -230,25 +254,28 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpa
     uint32_t pb[NR][2];
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      float e[4], g[4];
+      float g[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int y = 2 * x + (q & 1);
-        e[q] = fast_ex2(fmaf(sc[u][x][q], mul[y], neg[y]));
-        g[q] = e[q] * (q < 2 ? wa : wb);
-        float c = e[q] * (q < 2 ? ha : hb);
-        if constexpr (MASKED) {       // a masked token's scale may be anything
-          if (k_base + 16 * u + kn + 8 * (q >> 1) >= w.vis[y]) g[q] = c = 0.f;
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int y = 2 * x + e, q = 2 * half + e;
+          const float ex = fast_ex2(fmaf(sc[u][x][q], mul[y], neg[y]));
+          g[q] = ex * (half ? wb : wa);
+          w.l[y] += ex;
+          if constexpr (MASKED) {       // a masked token's scale may be anything
+            if (k_base + 16 * u + kn + 8 * half >= w.vis[y]) g[q] = 0.f;
+            else w.z[y] = fmaf(ex, half ? hb : ha, w.z[y]);
+          } else {
+            w.z[y] = fmaf(ex, half ? hb : ha, w.z[y]);
+          }
         }
-        w.l[y] += e[q];
-        w.z[y] += c;
-      }
       pb[x][0] = transpose8x8(pack_f16x2(g[0], g[1]));
       pb[x][1] = transpose8x8(pack_f16x2(g[2], g[3]));
     }
     // keys 2t, 2t + 1 (+ 8) of the 16, channels by lane: 8 n8 + i of each 64
-    const uint8_t *r0 = st + kPage * (D / 2) + (16 * u + key_of(2 * t)) * (D / 2);
-    const uint8_t *r1 = st + kPage * (D / 2) + (16 * u + key_of(2 * t + 1)) * (D / 2);
+    const uint8_t *r0 = st + Smem<D>::kV + (16 * u + key_of(2 * t)) * (D / 2);
+    const uint8_t *r1 = st + Smem<D>::kV + (16 * u + key_of(2 * t + 1)) * (D / 2);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
       const int at = 32 * i + 4 * n8;
@@ -285,20 +312,15 @@ __device__ __forceinline__ void page_step(WarpTile<D, NR> &w, const Unpack &unpa
   }
 }
 
-// Blocks of an SM: at d = 96 and 64 a fourth fits beside the rings of three
-// if a thread keeps to 128 registers.
-template <int D, int NR>
-__host__ __device__ constexpr int min_blocks() { return NR == 2 ? 2 : (D == 128 ? 3 : 4); }
-
-// NR: 8-row groups of a tile.
-template <int D, int NR, int NS>
-__global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel(const __grid_constant__ Params p) {
-  using S = Smem<D, NS>;
+// NR, E: as in WarpTile.
+template <int D, int NR, int E>
+__global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv4_attn_kernel(const __grid_constant__ Params p) {
+  using S = Smem<D>;
   using WT = WarpTile<D, NR>;
   constexpr int W = WT::W, MT = WT::MT;
-  constexpr int TR = 8 * NR;         // rows of a tile
+  constexpr int TR = 4 * E * NR;     // rows of a tile
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) unsigned long long bars[kWarps][NS];
+  __shared__ __align__(8) unsigned long long bars[kWarps][2];
   __shared__ long long s_scan[kWarps + 1];
   __shared__ int s_request, s_abort, s_last;
 
@@ -306,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   const int t = lane & 3, n8 = lane >> 2;
   WaitCtl ctl{&s_abort, p.dev_status, p.wait_limit_ns};
 
-  if (tid < kWarps * NS) mbar_init(smem_u32(&bars[0][0]) + 8 * tid, 1);
+  if (tid < kWarps * 2) mbar_init(smem_u32(&bars[0][0]) + 8 * tid, 1);
   if (tid == 0) {
     s_abort = 0;
     s_request = -1;
@@ -316,10 +338,10 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
   Range g;
   if (!find_range<TR, 1, kSetup, kThreads>(p, 1, g, s_scan, &s_request)) return;
 
-  uint8_t *ring = smem + warp * S::kWarpBytes;
-  const uint32_t ring_s = smem_u32(ring);
-  const uint32_t bar0 = smem_u32(&bars[warp][0]);
-  uint32_t it = 0;                  // pages this warp has consumed (ring position and phase)
+  uint8_t *place = smem + warp * S::kWarpBytes;
+  const uint32_t place_s = smem_u32(place);
+  auto full = [&](uint32_t n) { return smem_u32(&bars[warp][0]) + 8 * (n & 1); };
+  uint32_t it = 0;                  // pages this warp has consumed: place and phase
   bool ok = true;
 
   const Unpack unpack8;
@@ -333,13 +355,38 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
     const Pages pages(p, sg);
     const int end = min(sg.u1, pages.n);
 
+    auto issue = [&](uint32_t n, int page) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full(n), S::kStage);
+        bulk_load(place_s + (n & 1) * S::kStage, p.data + ((size_t)page * p.Hkv + h) * S::kStage, S::kStage, full(n));
+      }
+    };
+    // the next page of this warp and its block, -1 at the end
+    auto next_page = [&](int &i, int &blk) -> int {
+      while (i < end) {
+        const int page = pages.page(i, blk, lane == 0);
+        i += kWarps;
+        if (page >= 0) return page;
+      }
+      blk = -1;
+      return -1;
+    };
+    // the first two pages are on their way before anything else
+    int li = sg.u0 + warp, blk[2] = {-1, -1};
+    uint32_t sent = it;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int page = next_page(li, blk[e]);
+      if (page >= 0) issue(sent++, page);
+    }
+
     WT w;
-    // Q: the lane holds row n8 (+ 8) as the second operand, channels in the
+    // Q: the lane holds column n8 (+ 8) as the second operand, channels in the
     // order in which Unpack gives the codes, scaled to lie below 2
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      const int row = n8 + 8 * x;
-      const bool live = row < rows;
+      const int row = E == 2 ? n8 + 8 * x : n8 / 2 + 4 * x;
+      const bool live = row < rows && (E == 2 || (n8 & 1) == 0);
       const int tok = live ? (row0 + row) / p.G : 0, head = live ? (row0 + row) % p.G : 0;
       const uint16_t *src = p.Q + (rq.q0 + tok) * p.qt + (h * p.G + head) * p.qh + t * (D / 4);
       uint4 u[W];
@@ -366,14 +413,15 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      // rows 2t and 2t + 1 belong to lanes 8t and 8t + 4
+      // columns 2t and 2t + 1 belong to lanes 8t and 8t + 4
       const float mul = p.scale_log2 * __uint_as_float(ex << 23);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int y = 2 * x + e, r8 = 2 * t + e;
-        w.qsum[y] = __shfl_sync(0xffffffffu, sum, 4 * r8);
-        w.mul[y] = __shfl_sync(0xffffffffu, mul, 4 * r8);
-        w.vis[y] = p.causal ? rq.kv - (rq.n_q - 1 - min(rq.n_q - 1, (row0 + 8 * x + r8) / p.G)) : rq.kv;
+      for (int e = 0; e < E; ++e) {
+        const int y = 2 * x + e;
+        w.qsum[y] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        w.mul[y] = __shfl_sync(0xffffffffu, mul, 4 * (2 * t + e));
+        const int r8 = E == 2 ? 8 * x + 2 * t + e : 4 * x + t;
+        w.vis[y] = p.causal ? rq.kv - (rq.n_q - 1 - min(rq.n_q - 1, (row0 + r8) / p.G)) : rq.kv;
         w.m[y] = -INFINITY;
         w.l[y] = w.z[y] = 0.f;
       }
@@ -386,84 +434,47 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
     // keys that every row of the tile sees
     const int vis_all = p.causal ? rq.kv - (rq.n_q - 1 - row0 / p.G) : rq.kv;
 
-    auto issue = [&](uint32_t at, int page) {
-      if (lane == 0 && page >= 0) {
-        const uint32_t bar = bar0 + 8 * (at % NS);
-        mbar_arrive_expect_tx(bar, S::kStage);
-        bulk_load(ring_s + (at % NS) * S::kStage, p.data + ((size_t)page * p.Hkv + h) * S::kStage,
-                  S::kStage, bar);
-      }
-    };
-    // the next page of this warp and its block, -1 at the end
-    auto next_page = [&](int &i, int &blk) -> int {
-      while (i < end) {
-        const int page = pages.page(i, blk, lane == 0);
-        i += kWarps;
-        if (page >= 0) return page;
-      }
-      return -1;
-    };
-    int li = sg.u0 + warp;
-    int blk[NS];                    // blocks in flight, oldest first; -1: none
-    uint32_t issued = it;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      blk[s] = -1;
-      int b = -1;
-      const int page = next_page(li, b);
-      if (page >= 0) {
-        blk[s] = b;
-        issue(issued++, page);
-      }
-    }
     while (blk[0] >= 0) {
-      // the next page's number is read under this page's work
-      int nb = -1;
-      const int npage = next_page(li, nb);
-      if (!(ok = wait_warp(bar0 + 8 * (it % NS), (it / NS) & 1, ctl))) break;
-      const uint8_t *st = ring + (it % NS) * S::kStage;
+      // the number of the page after the next is read under this page's work
+      int nblk = -1;
+      const int npage = next_page(li, nblk);
+      const uint8_t *st = place + (it & 1) * S::kStage;
       const int k_base = blk[0] * kPage;
-      if (k_base + kPage > vis_all)
-        page_step<D, NR, true>(w, unpack8, st, k_base, rq.kv);
-      else
-        page_step<D, NR, false>(w, unpack8, st, k_base, rq.kv);
-      ++it;
-      __syncwarp();                 // every lane has read the page
-#pragma unroll
-      for (int s = 0; s + 1 < NS; ++s) blk[s] = blk[s + 1];
-      blk[NS - 1] = -1;
-      if (npage >= 0) {
-        // the free places are taken in order: the oldest -1
-        bool put = false;
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if (!put && blk[s] < 0) {
-            blk[s] = nb;
-            put = true;
-          }
-        issue(issued++, npage);
+      float sc[4][NR][4];
+      if (!(ok = wait_warp(full(it), (it >> 1) & 1, ctl))) break;
+      if (k_base + kPage > vis_all) {
+        page_scores<D, NR, E, true>(w, unpack8, st, k_base, sc);
+        page_values<D, NR, E, true>(w, unpack8, st, k_base, rq.kv, sc);
+      } else {
+        page_scores<D, NR, E, false>(w, unpack8, st, k_base, sc);
+        page_values<D, NR, E, false>(w, unpack8, st, k_base, rq.kv, sc);
       }
+      __syncwarp();                 // every lane has read the page
+      if (npage >= 0) issue(sent++, npage);
+      ++it;
+      blk[0] = blk[1];
+      blk[1] = nblk;
     }
     if (!ok) {
       // gave up: wait, with a limit, for the copies in flight before leaving
       volatile int never = 0;
       WaitCtl drain{&never, nullptr, 100000000LL};
-      for (uint32_t q = it; q < issued; ++q) wait_bounded(bar0 + 8 * (q % NS), (q / NS) & 1, drain);
+      for (uint32_t n = it; n < sent; ++n) wait_bounded(full(n), (n >> 1) & 1, drain);
     }
-    // ---- join the four warps: O + z, m, l of each row into the ring
+    // ---- join the four warps: O + z, m, l of each row into the pages' place
     __syncthreads();
     if (s_abort) return;            // uniform after the barrier: a wait gave up
-    float *mg = reinterpret_cast<float *>(ring);
+    float *mg = reinterpret_cast<float *>(place);
     const float vout = w.vref / kWeightScale;
 #pragma unroll
-    for (int y = 0; y < 2 * NR; ++y) {
+    for (int ye = 0; ye < NR * E; ++ye) {
+      const int x = ye / E, e = ye % E, y = 2 * x + e;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         w.l[y] += __shfl_xor_sync(0xffffffffu, w.l[y], o);
         w.z[y] += __shfl_xor_sync(0xffffffffu, w.z[y], o);
       }
-      const int x = y >> 1, e = y & 1;
-      float *row = mg + (8 * x + 2 * t + e) * S::kMergeStride;
+      float *row = mg + (E == 2 ? 8 * x + 2 * t + e : 4 * x + t) * S::kMergeStride;
       const float z = w.z[y];
       auto val = [&](int j, int up) { return fmaf(w.o[x][j][2 * up + e], vout, z); };
 #pragma unroll
@@ -579,16 +590,15 @@ __global__ void __launch_bounds__(kThreads, min_blocks<D, NR>()) kv4_attn_kernel
         }
       }
     }
-    fence_proxy_async();            // the ring was written by stores; copies follow
+    fence_proxy_async();            // the place was written by stores; copies follow
     __syncthreads();
   }
 }
 
-template <int D, int NR>
+template <int D, int NR, int E>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
-  constexpr int NS = 2;
-  auto kfn = kv4_attn_kernel<D, NR, NS>;
-  constexpr int bytes = Smem<D, NS>::kBytes;
+  auto kfn = kv4_attn_kernel<D, NR, E>;
+  constexpr int bytes = Smem<D>::kBytes;
   static std::mutex mu;
   static std::set<int> ready;
   static int per_sm = 1;
@@ -670,12 +680,13 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   const long long most = (long long)max_q * p.G;
   p.min_rows = 0;
   p.max_rows = most > hattn::kRows ? hattn::kRows : 0x7fffffffffffLL;
-  const bool low = most <= 8;
   cudaError_t e = cudaErrorInvalidValue;
   switch (d) {
-#define DITANGO_KV4(D)                                                                                \
-  case D:                                                                                             \
-    e = low ? hattn::launch<D, 1>(p, num_sms, stream) : hattn::launch<D, 2>(p, num_sms, stream);      \
+#define DITANGO_KV4(D)                                                                  \
+  case D:                                                                               \
+    e = most <= 4   ? hattn::launch<D, 1, 1>(p, num_sms, stream)                        \
+        : most <= 8 ? hattn::launch<D, 1, 2>(p, num_sms, stream)                        \
+                    : hattn::launch<D, 2, 2>(p, num_sms, stream);                       \
     break
     DITANGO_KV4(64);
     DITANGO_KV4(96);

@@ -102,10 +102,12 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x;
   g.total = 0;
+  long long v = 0, at = 0;           // of request tid: its work and place; all there is up to THREADS requests
   for (int base = 0; base < p.R; base += THREADS) {
     const int r = base + tid;
     long long sum;
-    block_scan<WARPS>(r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0, sum, sm);
+    v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
+    at = block_scan<WARPS>(v, sum, sm);
     g.total += sum;
   }
   const long long most = (g.total + min_units - 1) / min_units;
@@ -116,9 +118,11 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
   long long before = 0;
   for (int base = 0; base < p.R; base += THREADS) {
     const int r = base + tid;
-    const long long v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
-    long long sum;
-    const long long at = before + block_scan<WARPS>(v, sum, sm);
+    long long sum = g.total;
+    if (p.R > THREADS) {
+      v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
+      at = before + block_scan<WARPS>(v, sum, sm);
+    }
     if (v > 0 && at <= g.w0 && g.w0 < at + v) {
       *sm_r = r;
       sm[WARPS] = at;
