@@ -574,17 +574,30 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
           const int row = i / kVec, ch = (i % kVec) * 4;
           float mt_ = -INFINITY, lt_ = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (long long c = c1 - 1; c <= cl; ++c) {
-            const float *src = p.partial + (c * 2 + (c == c1 - 1 ? 1 : 0)) * kSlot + row * (D + 2);
-            const float pm = __ldcg(src + D), pl = __ldcg(src + D + 1);
-            const float2 a = __ldcg(reinterpret_cast<const float2 *>(src + ch));
-            const float2 b = __ldcg(reinterpret_cast<const float2 *>(src + ch + 2));
-            const float mn = fmaxf(mt_, pm);
-            const float sub = mn > -INFINITY ? mn : 0.f;
-            const float f0 = fast_ex2(mt_ - sub), f1 = fast_ex2(pm - sub);
-            lt_ = lt_ * f0 + pl * f1;
-            v = make_float4(v.x * f0 + a.x * f1, v.y * f0 + a.y * f1, v.z * f0 + b.x * f1, v.w * f0 + b.y * f1);
-            mt_ = mn;
+          // eight parts at a time: their loads are in flight together
+          for (long long c0 = c1 - 1; c0 <= cl; c0 += 8) {
+            float2 ml[8], a[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const long long c = c0 + e;
+              ml[e] = make_float2(-INFINITY, 0.f);
+              a[e] = b[e] = make_float2(0.f, 0.f);
+              if (c <= cl) {
+                const float *src = p.partial + (c * 2 + (c == c1 - 1 ? 1 : 0)) * kSlot + row * (D + 2);
+                ml[e] = __ldcg(reinterpret_cast<const float2 *>(src + D));
+                a[e] = __ldcg(reinterpret_cast<const float2 *>(src + ch));
+                b[e] = __ldcg(reinterpret_cast<const float2 *>(src + ch + 2));
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float mn = fmaxf(mt_, ml[e].x);
+              const float sub = mn > -INFINITY ? mn : 0.f;
+              const float f0 = fast_ex2(mt_ - sub), f1 = fast_ex2(ml[e].x - sub);
+              lt_ = lt_ * f0 + ml[e].y * f1;
+              v = make_float4(v.x * f0 + a[e].x * f1, v.y * f0 + a[e].y * f1, v.z * f0 + b[e].x * f1, v.w * f0 + b[e].y * f1);
+              mt_ = mn;
+            }
           }
           store(row, ch, v, mt_, lt_);
         }

@@ -759,15 +759,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       const int row = i / kVec, ch = (i % kVec) * 4;
       float mt = -INFINITY, lt = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (long long c = first - 1; c <= last; ++c) {
-        const float *src = p.partial + (c * 2 + (c == first - 1 ? 1 : 0)) * C::SLOT + kt * BM * (D + 2);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + BM * D + 2 * row));
-        const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + row * D + ch));
-        const float mn = fmaxf(mt, ml.x), sub = mn > -INFINITY ? mn : 0.f;
-        const float f0 = fast_ex2(mt - sub), f1 = fast_ex2(ml.x - sub);
-        lt = lt * f0 + ml.y * f1;
-        v = make_float4(v.x * f0 + a.x * f1, v.y * f0 + a.y * f1, v.z * f0 + a.z * f1, v.w * f0 + a.w * f1);
-        mt = mn;
+      // four parts at a time: their loads are in flight together
+      for (long long c0 = first - 1; c0 <= last; c0 += 4) {
+        float2 ml[4];
+        float4 a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const long long c = c0 + e;
+          ml[e] = make_float2(-INFINITY, 0.f);
+          a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c <= last) {
+            const float *src = p.partial + (c * 2 + (c == first - 1 ? 1 : 0)) * C::SLOT + kt * BM * (D + 2);
+            ml[e] = __ldcg(reinterpret_cast<const float2 *>(src + BM * D + 2 * row));
+            a[e] = __ldcg(reinterpret_cast<const float4 *>(src + row * D + ch));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mn = fmaxf(mt, ml[e].x), sub = mn > -INFINITY ? mn : 0.f;
+          const float f0 = fast_ex2(mt - sub), f1 = fast_ex2(ml[e].x - sub);
+          lt = lt * f0 + ml[e].y * f1;
+          v = make_float4(v.x * f0 + a[e].x * f1, v.y * f0 + a[e].y * f1, v.z * f0 + a[e].z * f1, v.w * f0 + a[e].w * f1);
+          mt = mn;
+        }
       }
       const float inv = lt > 0.f ? 1.f / lt : (lt == lt ? 0.f : lt);
       v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
