@@ -22,6 +22,7 @@ for device memory and streams.
 """
 from __future__ import annotations
 
+from . import _abi
 from ._abi import (  # noqa: F401
     DitangoError, Geometry, PLAN_FRESH, PLAN_REUSE, PLAN_SKIP, LIB_PATH, EXPORTED,
     ditango_version, ditango_check_geom, ditango_num_active, ditango_state_rows,
@@ -240,23 +241,45 @@ class ErrorPlanner:
         self.step_index += 1
 
 
-def _launch_on(device):
-    """The device current for a launch: nothing to do when it already is."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
+class _Launcher:
+    """Calls into the library for one device.  The calls of the objects below
+    take a few microseconds on the device, so this is the short way to them:
+    plain addresses, stride arrays made once, the device and its current stream
+    looked up without the objects around them."""
+
+    def __init__(self, device):
+        import torch
+        self.index = device.index
+        self._current, self._guard = torch.cuda.current_device, torch.cuda.device
+        self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._arrays = {}
+
+    def strides(self, t, n):
+        """The first n strides of t as a host array (kept: a program has few)."""
+        key = t.stride()
+        got = self._arrays.get((key, n))
+        if got is None:
+            if len(self._arrays) > 256:
+                self._arrays.clear()
+            got = self._arrays[key, n] = _abi._i64s(key[:n])
+        return got
+
+    def __call__(self, name, stream, *args):
+        """Library function `name` on args (addresses and numbers) and the stream,
+        which comes last; launches on this device whatever the current one is."""
+        if self._current() != self.index:
+            with self._guard(self.index):
+                st = getattr(_abi._lib, name)(*args, _abi._stream(stream))
+        elif stream is None and self._raw is not None:
+            st = getattr(_abi._lib, name)(*args, self._raw(self.index))
+        else:
+            st = getattr(_abi._lib, name)(*args, _abi._stream(stream))
+        if st:
+            raise DitangoError(name, st)
 
 
-class _Here:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, shape, dtypes, device, contiguous=False):
@@ -343,6 +366,8 @@ class KV4Cache:
         self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
         self._lists = {}
         self.kv = kv4(n_pages, Hkv, d, self.data)
+        self._run = _Launcher(dev)
+        self._kv = _abi.C.byref(self.kv)
 
     def _lengths(self, name, t, n=None):
         import torch
@@ -361,11 +386,11 @@ class KV4Cache:
             raise ValueError(f"{R} requests, the tables hold 1 to {self.max_requests}")
         self._lengths("new_len", new_len, R)
         self._lengths("free_pages", free_pages)
-        with _launch_on(self.device):
-            ditango_block_tables(R, self.max_blocks, self.max_tokens, self.n_pages, ctx_len, new_len,
-                                 free_pages if free_pages.shape[0] else None, free_pages.shape[0],
-                                 self.block_table, self.kv_len, self.q_off, self.slot_map,
-                                 self.pages_used, self.status, stream)
+        n_free = free_pages.shape[0]
+        self._run("ditango_block_tables", stream, R, self.max_blocks, self.max_tokens, self.n_pages,
+                  ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr() if n_free else None, n_free,
+                  self.block_table.data_ptr(), self.kv_len.data_ptr(), self.q_off.data_ptr(),
+                  self.slot_map.data_ptr(), self.pages_used.data_ptr(), self.status.data_ptr())
         self.n_requests = R
 
     def _rows(self, K, V, slots):
@@ -380,27 +405,24 @@ class KV4Cache:
             slots = self.slot_map
         else:
             _need(slots, "slots", (T,), (torch.int64,), dev, contiguous=True)
-        return T, slots, K.stride()[:2], V.stride()[:2]
+        run = self._run
+        return T, K.data_ptr(), V.data_ptr(), run.strides(K, 2), run.strides(V, 2), slots.data_ptr()
 
     def write(self, K, V, slots=None, stream=None):
         """Quantise K, V [T, Hkv, d] into the slots (default: the slot map of
         the last tables() call; -1 leaves a token out)."""
-        T, slots, ks, vs = self._rows(K, V, slots)
-        with _launch_on(self.device):
-            ditango_kv4_write(self.kv, T, K, V, ks, vs, slots, self.status, stream)
+        self._run("ditango_kv4_write", stream, self._kv, *self._rows(K, V, slots), self.status.data_ptr())
 
     def read(self, slots, K, V, stream=None):
         """Slots back as bf16 rows of K, V [T, Hkv, d] (rows of -1 are left alone)."""
-        T, slots, ks, vs = self._rows(K, V, slots)
-        with _launch_on(self.device):
-            ditango_kv4_read(self.kv, T, K, V, ks, vs, slots, self.status, stream)
+        self._run("ditango_kv4_read", stream, self._kv, *self._rows(K, V, slots), self.status.data_ptr())
 
     def summarize(self, ctx_len, stream=None):
         """Refresh the summaries of the pages that got tokens behind ctx_len[r]."""
         self._lengths("ctx_len", ctx_len, self.n_requests)
-        with _launch_on(self.device):
-            ditango_kv4_summary(self.kv, self.n_requests, self.max_blocks, ctx_len, self.kv_len,
-                                self.block_table, self.sum_codes, self.sum_scale, self.status, stream)
+        self._run("ditango_kv4_summary", stream, self._kv, self.n_requests, self.max_blocks,
+                  ctx_len.data_ptr(), self.kv_len.data_ptr(), self.block_table.data_ptr(),
+                  self.sum_codes.data_ptr(), self.sum_scale.data_ptr(), self.status.data_ptr())
 
     def select(self, Q, k, band=0, sink=0, stream=None):
         """(sel, count): the k best pages for one query token a request, Q
@@ -418,13 +440,14 @@ class KV4Cache:
                 torch.empty((R, self.Hkv, room), dtype=torch.int32, device=self.device),
                 torch.empty((R, self.Hkv), dtype=torch.int32, device=self.device))
         sel, count = self._lists[R, room]
-        s = Q.stride()
-        with _launch_on(self.device):
-            ditango_block_summary(R, H, 1, d, PAGE, Q, (s[0], s[1], d), self._q_codes, self._q_scale,
-                                  stream=stream)
-            ditango_block_select(R, H, self.Hkv, 1, self.max_blocks, d, k, band, sink, 0, room,
-                                 self._q_codes, self._q_scale, self.sum_codes, self.sum_scale, sel, count,
-                                 self.block_table, self.n_pages, self.kv_len, self.status, stream)
+        run, q_codes, q_scale = self._run, self._q_codes.data_ptr(), self._q_scale.data_ptr()
+        # one token is one row of a block: the (request, head) strides, and any third
+        run("ditango_block_summary", stream, R, H, 1, d, PAGE, Q.data_ptr(), run.strides(Q, 3), None, q_codes,
+            q_scale, None)
+        run("ditango_block_select", stream, R, H, self.Hkv, 1, self.max_blocks, d, k, band, sink, 0, room,
+            q_codes, q_scale, self.sum_codes.data_ptr(), self.sum_scale.data_ptr(),
+            self.block_table.data_ptr(), self.n_pages, self.kv_len.data_ptr(), sel.data_ptr(),
+            count.data_ptr(), self.status.data_ptr())
         return sel, count
 
     def attend(self, Q, out, out_lse=None, max_q=None, causal=False, scale=0.0, sel=None, sel_count=None,
@@ -440,13 +463,11 @@ class KV4Cache:
         dev = self.device
         _need(Q, "Q", shape, (torch.bfloat16,), dev)
         _need(out, "out", shape, (torch.bfloat16, torch.float32), dev)
-        lse_strides = None
         if out_lse is not None:
             if not isinstance(out_lse, torch.Tensor) or out_lse.dtype != torch.float32:
                 raise TypeError("out_lse: a float32 tensor is required")
             if out_lse.shape != (T, self.H) or out_lse.device != dev:
                 raise ValueError(f"out_lse: a tensor of shape {(T, self.H)} on {dev} is required")
-            lse_strides = out_lse.stride()
         if (sel is None) != (sel_count is None):
             raise ValueError("sel and sel_count go together")
         room = 0
@@ -454,12 +475,13 @@ class KV4Cache:
             room = sel.shape[-1]
             _need(sel, "sel", (self.n_requests, self.Hkv, room), (torch.int32,), dev, contiguous=True)
             _need(sel_count, "sel_count", (self.n_requests, self.Hkv), (torch.int32,), dev, contiguous=True)
-        with _launch_on(self.device):
-            ditango_kv4_attn(self.kv, self.n_requests, self.H, T, T if max_q is None else max_q,
-                             self.max_blocks, Q, Q.stride()[:2], self.q_off, self.kv_len,
-                             self.block_table, out, out.dtype == torch.float32, self.workspace,
-                             self.ws_bytes, out.stride()[:2], out_lse, lse_strides, sel,
-                             sel_count, room, scale, causal, self.status, stream)
+        run = self._run
+        run("ditango_kv4_attn", stream, self._kv, self.n_requests, self.H, T, T if max_q is None else max_q,
+            self.max_blocks, Q.data_ptr(), run.strides(Q, 2), self.q_off.data_ptr(), self.kv_len.data_ptr(),
+            self.block_table.data_ptr(), _addr(sel), _addr(sel_count), room, scale, 1 if causal else 0,
+            out.data_ptr(), 1 if out.dtype == torch.float32 else 0, run.strides(out, 2), _addr(out_lse),
+            None if out_lse is None else run.strides(out_lse, 2), self.workspace.data_ptr(), self.ws_bytes,
+            self.status.data_ptr())
 
 
 class BlockSparseAttention:
@@ -506,6 +528,7 @@ class BlockSparseAttention:
         self.sel = torch.full((B, Hkv, self.n_q, self.room), -1, **i32)
         self.sel_count = torch.zeros((B, Hkv, self.n_q), **i32)
         self.status = torch.zeros(1, **i32)
+        self._run = _Launcher(dev)
 
     def _check_len(self, k_len):
         import torch
@@ -520,15 +543,16 @@ class BlockSparseAttention:
         _need(Q, "Q", (B, H, self.Nq, d), (torch.bfloat16,), self.device)
         _need(K, "K", (B, Hkv, self.Nk, d), (torch.bfloat16,), self.device)
         self._check_len(k_len)
-        with _launch_on(self.device):
-            ditango_block_summary(B, H, self.Nq, d, QBLOCK, Q, Q.stride()[:3], self.q_codes, self.q_scale,
-                                  stream=stream)
-            ditango_block_summary(B, Hkv, self.Nk, d, PAGE, K, K.stride()[:3], self.k_codes, self.k_scale,
-                                  self.k_mean, k_len, stream)
-            ditango_block_select(B, H, Hkv, self.n_q, self.n_k, d, self.k, self.band, self.sink,
-                                 QBLOCK // PAGE, self.room, self.q_codes, self.q_scale, self.k_codes,
-                                 self.k_scale, self.sel, self.sel_count, None, 0, k_len, self.status,
-                                 stream)
+        run, length = self._run, _addr(k_len)
+        q_codes, q_scale = self.q_codes.data_ptr(), self.q_scale.data_ptr()
+        k_codes, k_scale = self.k_codes.data_ptr(), self.k_scale.data_ptr()
+        run("ditango_block_summary", stream, B, H, self.Nq, d, QBLOCK, Q.data_ptr(), run.strides(Q, 3), None,
+            q_codes, q_scale, None)
+        run("ditango_block_summary", stream, B, Hkv, self.Nk, d, PAGE, K.data_ptr(), run.strides(K, 3), length,
+            k_codes, k_scale, self.k_mean.data_ptr())
+        run("ditango_block_select", stream, B, H, Hkv, self.n_q, self.n_k, d, self.k, self.band, self.sink,
+            QBLOCK // PAGE, self.room, q_codes, q_scale, k_codes, k_scale, None, 0, length,
+            self.sel.data_ptr(), self.sel_count.data_ptr(), self.status.data_ptr())
         return self.sel, self.sel_count
 
     def attend(self, Q, K, V, out, out_lse=None, sel=None, sel_count=None, k_len=None, scale=0.0,
@@ -552,11 +576,11 @@ class BlockSparseAttention:
             _need(sel, "sel", (B, Hkv, self.n_q, sel.shape[-1]), (torch.int32,), dev, contiguous=True)
             _need(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), dev, contiguous=True)
         self._check_len(k_len)
-        with _launch_on(self.device):
-            ditango_block_attn(B, H, Hkv, Nq, self.Nk, d, Q, K, V, Q.stride()[:3], K.stride()[:3],
-                               V.stride()[:3], sel, sel_count, sel.shape[-1], out,
-                               out.dtype == torch.float32, out.stride()[:3], out_lse, k_len, scale,
-                               self.status, stream)
+        run = self._run
+        run("ditango_block_attn", stream, B, H, Hkv, Nq, self.Nk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+            run.strides(Q, 3), run.strides(K, 3), run.strides(V, 3), sel.data_ptr(), sel_count.data_ptr(),
+            sel.shape[-1], _addr(k_len), scale, out.data_ptr(), 1 if out.dtype == torch.float32 else 0,
+            run.strides(out, 3), _addr(out_lse), self.status.data_ptr())
 
     def step(self, Q, K, V, out, out_lse=None, k_len=None, scale=0.0, stream=None):
         """select, then attend."""

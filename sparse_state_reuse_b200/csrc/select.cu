@@ -115,11 +115,12 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+template <bool HEADS>
+constexpr int kSelThreads = HEADS ? 512 : 256;
 
 struct SelectParams {
   int Hkv, G, n_q, n_k, n_pages, k, band, sink, room, rows;
+  int stride;                   // of a row of scores, see row_stride()
   int own;                      // key blocks of a query block; 0: the query stands at the end
   const signed char *qc, *kc;
   const float *qs, *ks;
@@ -146,10 +147,13 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 constexpr uint32_t kForced = 0xffffffffu;
 
 // Warp-wide choice of one row: the threshold between what is taken and what is
-// not, by bisection between the least and greatest score that ends as soon as
-// the count is met (12 to 14 steps on a thousand different scores), then the
-// list in ascending order.  REG > 0: the row (at most 32 REG entries) stays in
-// registers; 0: it is read from shared memory in every step.
+// not, then the list in ascending order.  The threshold is found by bisection
+// between the least and greatest score, which ends as soon as the count is met:
+// 12 to 18 steps on a thousand different scores, and 32 at most.  (Interpolating
+// between the counts at both ends needs fewer steps, but the chain of each is
+// longer: 540 instead of 501 us for 40 heads of 600 query and 1200 key blocks.)
+// REG > 0: the row (at most 32 REG entries) stays in registers; 0: it is read
+// from shared memory in every step.
 template <int REG>
 __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, int room, int *dst, int *count) {
   const int lane = threadIdx.x & 31;
@@ -216,15 +220,18 @@ __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, i
     }
   }
   int out = 0;
+  const uint32_t below = (1u << lane) - 1u;
   auto emit = [&](int j, uint32_t x) {
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, ties > 0 && x == above);
-    const bool take = x > above || (((eq >> lane) & 1u) && __popc(eq & below) < ties);
+    bool take = x > above;
+    if (ties > 0) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, x == above);
+      take = take || (((eq >> lane) & 1u) && __popc(eq & below) < ties);
+      ties -= min(ties, __popc(eq));
+    }
     const uint32_t got = __ballot_sync(0xffffffffu, take);
     const int at = out + __popc(got & below);
     if (take && at < room) dst[at] = j;
     out += __popc(got);
-    ties -= min(ties, __popc(eq));
   };
   if constexpr (REG > 0) {
 #pragma unroll
@@ -241,9 +248,9 @@ __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, i
 // 16 rows of the product are the query heads of the key head instead, so that
 // the key codes are read once and not once a head.
 template <int D, int REG, bool HEADS>
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int KS = D / 32;
-  extern __shared__ uint32_t score[];        // [rows][n_k] (fp32 sums, then their order)
+__global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int KS = D / 32, kThreads = kSelThreads<HEADS>, kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint32_t score[];   // [rows][stride] (fp32 sums, then their order)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = lane & 3, n8 = lane >> 2;
   const int i0 = HEADS ? 0 : blockIdx.x * p.rows, h = blockIdx.y, b = blockIdx.z;
@@ -258,11 +265,13 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
     nk = (int)max(0LL, min((long long)p.n_k, most));
   }
   const int tiles = (nk + 7) / 8;
-  auto forced = [&](int i, int j) -> bool {
-    if (j < p.sink) return true;
-    if (p.band < 0) return false;
-    const int f = p.own ? i * p.own : nk - 1, l = p.own ? f + p.own - 1 : nk - 1;
-    return j >= f - p.band && j <= l + p.band;
+  // the band of query block i: key blocks [first, last]
+  auto band_of = [&](int i, int &first, int &last) {
+    first = p.own ? i * p.own : nk - 1;
+    last = p.own ? first + p.own - 1 : nk - 1;
+    first -= p.band;
+    last += p.band;
+    if (p.band < 0) last = first - 1;
   };
   auto page_of = [&](int j) -> int {         // -1: a page number out of range, which scores 0
     const int page = __ldg(p.block_table + (size_t)b * p.n_k + j);
@@ -275,6 +284,43 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
     const int page = page_of(j);
     return page < 0 ? 0.f : __ldg(p.ks + (size_t)page * p.Hkv + h);
   };
+  // HEADS: the scale of each key block and its page, read at once and not by
+  // the chain of each product
+  float *scale = reinterpret_cast<float *>(score + rows * p.stride);
+  int *pages = reinterpret_cast<int *>(scale + p.stride);
+  if constexpr (HEADS) {
+    constexpr int kOnce = 4;
+    for (int j0 = tid; j0 < nk; j0 += kThreads * kOnce) {
+      int page[kOnce];
+      float s[kOnce];
+#pragma unroll
+      for (int e = 0; e < kOnce; ++e) {
+        const int j = j0 + e * kThreads;
+        page[e] = j < nk && p.block_table ? __ldg(p.block_table + (size_t)b * p.n_k + j) : j;
+      }
+#pragma unroll
+      for (int e = 0; e < kOnce; ++e) {
+        const int j = j0 + e * kThreads;
+        const bool good = !p.block_table || (page[e] >= 0 && page[e] < p.n_pages);
+        if (j < nk && !good) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+        if (!good) page[e] = -1;
+        const size_t at = p.block_table ? (size_t)page[e] * p.Hkv + h : ((size_t)b * p.Hkv + h) * p.n_k + j;
+        s[e] = j < nk && good ? __ldg(p.ks + at) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kOnce; ++e) {
+        const int j = j0 + e * kThreads;
+        if (j >= nk) break;
+        scale[j] = s[e];
+        pages[j] = page[e];
+      }
+    }
+    __syncthreads();
+  }
+  const int rows_up = (rows + 7) & ~7;
+  int bf[2], bl[2];
+  band_of(i0 + n8, bf[0], bl[0]);
+  band_of(i0 + n8 + 8, bf[1], bl[1]);
   for (int g = 0; g < (HEADS ? 1 : p.G); ++g) {
     uint32_t a[KS][4];
     float qs[2];
@@ -294,16 +340,16 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
       }
     }
     constexpr int kAhead = 4;      // key tiles in flight
-    for (int u0 = warp; u0 < tiles; u0 += kSelWarps * kAhead) {
+    for (int u0 = warp; u0 < tiles; u0 += kWarps * kAhead) {
       uint2 kb[kAhead][KS];
       const signed char *src[kAhead];
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
-        const int j = (u0 + e * kSelWarps) * 8 + n8;
+        const int j = (u0 + e * kWarps) * 8 + n8;
         src[e] = nullptr;
         if (j >= nk) continue;
         if (p.block_table) {
-          const int page = page_of(j);
+          const int page = HEADS ? pages[j] : page_of(j);
           if (page >= 0) src[e] = p.kc + ((size_t)page * p.Hkv + h) * D;
         } else {
           src[e] = p.kc + (((size_t)b * p.Hkv + h) * p.n_k + j) * D;
@@ -316,42 +362,66 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
           kb[e][s] = src[e] ? __ldg(reinterpret_cast<const uint2 *>(src[e] + t * (D / 4)) + s) : make_uint2(0, 0);
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
-        const int u = u0 + e * kSelWarps;
+        const int u = u0 + e * kWarps;
         if (u >= tiles) break;
         int c[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < KS; ++s) imma16832(c, a[s], kb[e][s].x, kb[e][s].y);
+        // columns j and j + 1 of rows n8 and n8 + 8; entries past the end are 0
+        const int j = u * 8 + 2 * t;
+        const bool in0 = j < nk, in1 = j + 1 < nk, last_head = HEADS || g + 1 == p.G;
+        float ks0 = 0.f, ks1 = 0.f;
+        if (!HEADS && last_head) {
+          if (in0) ks0 = scale_of(j);
+          if (in1) ks1 = scale_of(j + 1);
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = n8 + 8 * (q >> 1), j = u * 8 + 2 * t + (q & 1);
-          if (row >= rows || j >= nk) continue;
-          uint32_t *dst = score + (size_t)row * p.n_k + j;
-          float x = __fmul_rn(qs[q >> 1], (float)c[q]);
-          if (!HEADS && g > 0) x = __fadd_rn(__uint_as_float(*dst), x);
-          if (HEADS || g + 1 < p.G)
-            *dst = __float_as_uint(x);
-          else
-            *dst = forced(i0 + row, j) ? kForced : order_of(__fmul_rn(x, scale_of(j)));
+        for (int x = 0; x < 2; ++x) {
+          if (x * 8 >= rows_up) break;
+          uint2 *dst = reinterpret_cast<uint2 *>(score + (n8 + 8 * x) * p.stride + j);
+          float s0 = __fmul_rn(qs[x], (float)c[2 * x]), s1 = __fmul_rn(qs[x], (float)c[2 * x + 1]);
+          if (n8 + 8 * x >= rows) continue;
+          if (!HEADS && g > 0) {
+            const uint2 before = *dst;
+            s0 = __fadd_rn(__uint_as_float(before.x), s0);
+            s1 = __fadd_rn(__uint_as_float(before.y), s1);
+          }
+          uint2 v = make_uint2(__float_as_uint(s0), __float_as_uint(s1));
+          if (!HEADS && last_head) {
+            v.x = order_of(__fmul_rn(s0, ks0));
+            v.y = order_of(__fmul_rn(s1, ks1));
+            if (j < p.sink || (j >= bf[x] && j <= bl[x])) v.x = kForced;
+            if (j + 1 < p.sink || (j + 1 >= bf[x] && j + 1 <= bl[x])) v.y = kForced;
+            if (!in0) v.x = 0u;
+            if (!in1) v.y = 0u;
+          }
+          *dst = v;
         }
       }
     }
   }
   __syncthreads();
   if constexpr (HEADS) {
-    for (int j = tid; j < nk; j += kSelThreads) {
+    int first, last;
+    band_of(0, first, last);
+    for (int j = tid; j < nk; j += kThreads) {
       float x = __uint_as_float(score[j]);
-      for (int g = 1; g < rows; ++g) x = __fadd_rn(x, __uint_as_float(score[(size_t)g * p.n_k + j]));
-      score[j] = forced(0, j) ? kForced : order_of(__fmul_rn(x, scale_of(j)));
+      for (int g = 1; g < rows; ++g) x = __fadd_rn(x, __uint_as_float(score[g * p.stride + j]));
+      score[j] = j < p.sink || (j >= first && j <= last) ? kForced : order_of(__fmul_rn(x, scale[j]));
     }
     __syncthreads();
   }
-  for (int row = warp; row < (HEADS ? 1 : rows); row += kSelWarps) {
+  for (int row = warp; row < (HEADS ? 1 : rows); row += kWarps) {
     const size_t at = ((size_t)b * p.Hkv + h) * p.n_q + i0 + row;
-    choose_row<REG>(score + (size_t)row * p.n_k, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
+    choose_row<REG>(score + row * p.stride, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
   }
 }
 
-constexpr int kMaxScoreBytes = 200 * 1024;
+constexpr int kMaxScoreBytes = 208 * 1024;
+
+// Entries of a row of scores in shared memory: whole tiles of 8, and 8 more than
+// a multiple of 32, so that the rows a warp writes at once lie in other banks.
+int row_stride(int n_k) { return (n_k + 8 - 1) / 8 * 8 + (40 - (n_k + 7) / 8 * 8 % 32) % 32; }
 
 template <int D, int REG, bool HEADS>
 cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t stream) {
@@ -370,7 +440,7 @@ cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t 
     }
   }
   const dim3 grid((unsigned)(HEADS ? 1 : (p.n_q + p.rows - 1) / p.rows), (unsigned)p.Hkv, (unsigned)B);
-  kfn<<<grid, kSelThreads, bytes, stream>>>(p);
+  kfn<<<grid, kSelThreads<HEADS>, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -386,7 +456,7 @@ cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t 
 }  // namespace sel
 
 // Most key blocks of a selection: one row of scores in shared memory.
-int select_max_blocks() { return sel::kMaxScoreBytes / 4; }
+int select_max_blocks() { return 51200; }
 
 cudaError_t launch_block_summary(int B, int H, int N, int d, int block, const uint16_t *x, const int64_t *s,
                                  const int *len, signed char *codes, float *scale, float *mean,
@@ -436,11 +506,12 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
   p.count = count;
   p.dev_status = dev_status;
   // as many query blocks as the scores leave room for, 16 (one product) at most
+  p.stride = sel::row_stride(n_k);
   int rows = 16;
-  while (rows > 1 && (rows / 2 >= n_q || (long long)rows * n_k * 4 > 100 * 1024)) rows /= 2;
-  const bool heads = n_q == 1 && p.G <= 16 && (long long)p.G * n_k * 4 <= sel::kMaxScoreBytes;
+  while (rows > 1 && (rows / 2 >= n_q || (long long)rows * p.stride * 4 > 100 * 1024)) rows /= 2;
+  const bool heads = n_q == 1 && p.G <= 16 && (p.G + 2LL) * p.stride * 4 <= sel::kMaxScoreBytes;
   p.rows = rows;
-  const int bytes = (heads ? p.G : rows) * n_k * 4;
+  const int bytes = (heads ? p.G + 2 : rows) * p.stride * 4;
   switch (d) {
 #define DITANGO_SEL(D)                                                     \
   case D:                                                                  \
