@@ -456,8 +456,9 @@ ditango_status ditango_kv4_summary(const ditango_kv4 *c, int32_t R, int32_t max_
 
 /* Bytes of device scratch of ditango_kv4_attn (0 for an unsupported d).  Zero
  * it once when it is allocated: every launch leaves its counters at zero
- * again.  Launches that may run at the same time (other streams, concurrent
- * graph branches) must not share one. */
+ * again (not one that recorded DITANGO_ERR_TIMEOUT: zero it before the next).
+ * Launches that may run at the same time (other streams, concurrent graph
+ * branches) must not share one. */
 size_t ditango_kv4_attn_workspace_size(int32_t d);
 
 /* Attention of the requests' new tokens over their histories.  Token t of

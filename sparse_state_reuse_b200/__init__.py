@@ -427,19 +427,21 @@ class KV4Cache:
     def select(self, Q, k, band=0, sink=0, stream=None):
         """(sel, count): the k best pages for one query token a request, Q
         [n_requests, H, d]; the last band + 1 pages and the first sink pages
-        are always among them.  The lists are this object's: the next call of
-        the same sizes overwrites them."""
+        are always among them.  The lists are this object's: the next call
+        overwrites them."""
         import torch
         R, H, d = self.n_requests, self.H, self.d
         _need(Q, "Q", (R, H, d), (torch.bfloat16,), self.device)
         if k < 0 or sink < 0 or band < -1:
             raise ValueError("k and sink must be >= 0, band >= -1")
         room = max(1, k, sink + (1 + 2 * band if band >= 0 else 0))
-        if (R, room) not in self._lists:
-            self._lists[R, room] = (
-                torch.empty((R, self.Hkv, room), dtype=torch.int32, device=self.device),
-                torch.empty((R, self.Hkv), dtype=torch.int32, device=self.device))
-        sel, count = self._lists[R, room]
+        if room not in self._lists:          # one pair of buffers a width, for any number of requests
+            self._lists[room] = (
+                torch.empty((self.max_requests, self.Hkv, room), dtype=torch.int32, device=self.device),
+                torch.empty((self.max_requests, self.Hkv), dtype=torch.int32, device=self.device))
+        sel, count = self._lists[room]
+        if R != self.max_requests:
+            sel, count = sel[:R], count[:R]
         run, q_codes, q_scale = self._run, self._q_codes.data_ptr(), self._q_scale.data_ptr()
         # one token is one row of a block: the (request, head) strides, and any third
         run("ditango_block_summary", stream, R, H, 1, d, PAGE, Q.data_ptr(), run.strides(Q, 3), None, q_codes,

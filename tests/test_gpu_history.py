@@ -470,6 +470,62 @@ def test_page_summaries_and_selection_match_the_oracle(d):
                 assert (sel[r, h, len(want):] == -1).all()
 
 
+def test_selection_over_a_long_table_and_with_fewer_requests():
+    """More places than the scores of all heads fit beside one another; then a
+    batch of fewer requests with the same widths."""
+    rng = np.random.default_rng(17)
+    kv, Hkv, H, d, k = [900, 64, 3000], 1, 16, 64, 7
+    c, host, table = filled(rng, kv, Hkv, d, H, 3)
+    long_ = dt.KV4Cache(c.n_pages, Hkv, d, 3, 6000, 3, H=H, data=c.data)
+    long_.block_table[:, :table.shape[1]] = c.block_table
+    long_.kv_len.copy_(c.kv_len)
+    Q = HC.up(HC.bf16_round(rng.standard_normal((3, H, d))))
+    got = []
+    for x in (c, long_):
+        x.summarize(ints([0, 0, 0]))
+        sel, count = x.select(Q, k, band=0, sink=1)
+        torch.cuda.synchronize()
+        assert x.status.item() == 0
+        got.append((sel.cpu(), count.cpu()))
+        x.n_requests = 2
+        sel2, count2 = x.select(Q[:2], k, band=0, sink=1)
+        torch.cuda.synchronize()
+        x.n_requests = 3
+        assert torch.equal(sel2.cpu(), got[-1][0][:2]) and torch.equal(count2.cpu(), got[-1][1][:2])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert got[0][1].tolist() == [[7], [1], [7]]
+
+
+def test_pages_past_four_gib():
+    """The same tokens on the first pages of a small cache and on the last ones of
+    a cache of more than 2^32 bytes: every result is the same."""
+    rng = np.random.default_rng(23)
+    Hkv, H, d, n, many = 8, 16, 128, 700, 62000
+    assert many * Hkv * PAGE * (d + 8) > 2 ** 32
+    need = -(-n // PAGE)
+    K, V = (HC.up(x) for x in HC.keys_values(rng, n, Hkv, d))
+    Q1, Q2 = (HC.up(HC.bf16_round(rng.standard_normal((t, H, d)))) for t in (1, 40))
+    got = []
+    for pages, first in ((need, 0), (many, many - need)):
+        c = dt.KV4Cache(pages, Hkv, d, 1, need, n, H=H)
+        c.tables(ints([0]), ints([n]), torch.arange(first, first + need, dtype=torch.int32, device="cuda"))
+        c.write(K, V)
+        c.summarize(ints([0]))
+        back = torch.zeros((2, n, Hkv, d), dtype=torch.bfloat16, device="cuda")
+        c.read(c.slot_map, back[0], back[1])
+        sel, count = c.select(Q1, 5, band=0, sink=1)
+        res = [back, sel, count]
+        for Q in (Q1, Q2):
+            out = torch.zeros((len(Q), H, d), device="cuda")
+            lse = torch.zeros((len(Q), H), device="cuda")
+            attend(c, [len(Q)], Q, out, lse, causal=True)
+            res += [out, lse]
+        assert c.status.item() == 0
+        got.append([x.cpu() for x in res])
+        del c
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ---------------------------------------------------------------- together
 def test_a_batch_of_steps_together_and_in_a_graph():
     """Tables, write, summaries, selection and attention of a growing batch;
