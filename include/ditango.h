@@ -454,6 +454,25 @@ ditango_status ditango_kv4_summary(const ditango_kv4 *c, int32_t R, int32_t max_
                                    float *sum_scale, int32_t *dev_status,
                                    ditango_stream stream);
 
+/* The pages that one query token a request attends: ditango_block_select
+ * (own_blocks 0) over the page summaries, for Q dev bf16 [R][H][d] ((request,
+ * head) element strides, multiples of 8, 16-byte aligned), whose codes it forms
+ * itself.
+ *   max_blocks   width of block_table, <= 51200 (else UNSUPPORTED).
+ *   q_codes, q_scale  dev int8 [R][H][d] and float32 [R][H]: scratch, used when
+ *                the heads of a key head are more than 16 or max_blocks is too
+ *                wide for all their scores in shared memory.
+ *   sel, sel_count  dev int32 [R][Hkv][max_sel] and [R][Hkv] out, max_sel >=
+ *                max(k, sink + 1 + 2 band) (the band counts with band >= 0). */
+ditango_status ditango_kv4_select(const ditango_kv4 *c, int32_t R, int32_t H, int32_t max_blocks,
+                                  int32_t k, int32_t band, int32_t sink, int32_t max_sel,
+                                  const uint16_t *Q, const int64_t q_strides[2],
+                                  const int8_t *sum_codes, const float *sum_scale,
+                                  const int32_t *block_table, const int32_t *kv_len,
+                                  int8_t *q_codes, float *q_scale, int32_t *sel,
+                                  int32_t *sel_count, int32_t *dev_status,
+                                  ditango_stream stream);
+
 /* Bytes of device scratch of ditango_kv4_attn (0 for an unsupported d).  Zero
  * it once when it is allocated: every launch leaves its counters at zero
  * again (not one that recorded DITANGO_ERR_TIMEOUT: zero it before the next).
@@ -513,6 +532,16 @@ ditango_status ditango_block_summary(int32_t B, int32_t H, int32_t N, int32_t d,
                                      const uint16_t *x, const int64_t strides[3],
                                      const int32_t *len, int8_t *codes, float *scale,
                                      float *mean, ditango_stream stream);
+
+/* Both summaries of a call in one launch: Q's blocks of DITANGO_QBLOCK rows and
+ * K's of DITANGO_PAGE rows (k_len, k_mean as len and mean above).  H + Hkv <=
+ * 65535. */
+ditango_status ditango_block_summaries(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk,
+                                       int32_t d, const uint16_t *Q, const int64_t q_strides[3],
+                                       const uint16_t *K, const int64_t k_strides[3],
+                                       const int32_t *k_len, int8_t *q_codes, float *q_scale,
+                                       int8_t *k_codes, float *k_scale, float *k_mean,
+                                       ditango_stream stream);
 
 /* Selection.  Per (b, key head g, query block i) the score of key block j is
  *   k_scale_j * sum over query heads h of g, ascending, of q_scale_h (q_h . k_j)

@@ -32,7 +32,8 @@ from ._abi import (  # noqa: F401
     ditango_plan_error, error_state, ditango_plan_from_mass, ditango_checked_build,
     ditango_check_status, PAGE, QBLOCK, kv4, ditango_block_tables, ditango_kv4_write,
     ditango_kv4_read, ditango_kv4_summary, ditango_kv4_attn, ditango_kv4_attn_workspace_size,
-    ditango_block_summary, ditango_block_select, ditango_block_attn,
+    ditango_kv4_select, ditango_block_summary, ditango_block_summaries, ditango_block_select,
+    ditango_block_attn,
 )
 
 
@@ -361,7 +362,7 @@ class KV4Cache:
         # the attention's partial states and counters (each launch leaves the counters at zero)
         self.ws_bytes = ditango_kv4_attn_workspace_size(d)
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
-        # the single tokens' 8-bit codes, for select()
+        # room for the single tokens' 8-bit codes, for select()
         self._q_codes = torch.empty((max_requests, H, d), dtype=torch.int8, device=dev)
         self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
         self._lists = {}
@@ -442,13 +443,10 @@ class KV4Cache:
         sel, count = self._lists[room]
         if R != self.max_requests:
             sel, count = sel[:R], count[:R]
-        run, q_codes, q_scale = self._run, self._q_codes.data_ptr(), self._q_scale.data_ptr()
-        # one token is one row of a block: the (request, head) strides, and any third
-        run("ditango_block_summary", stream, R, H, 1, d, PAGE, Q.data_ptr(), run.strides(Q, 3), None, q_codes,
-            q_scale, None)
-        run("ditango_block_select", stream, R, H, self.Hkv, 1, self.max_blocks, d, k, band, sink, 0, room,
-            q_codes, q_scale, self.sum_codes.data_ptr(), self.sum_scale.data_ptr(),
-            self.block_table.data_ptr(), self.n_pages, self.kv_len.data_ptr(), sel.data_ptr(),
+        run = self._run
+        run("ditango_kv4_select", stream, self._kv, R, H, self.max_blocks, k, band, sink, room, Q.data_ptr(),
+            run.strides(Q, 2), self.sum_codes.data_ptr(), self.sum_scale.data_ptr(), self.block_table.data_ptr(),
+            self.kv_len.data_ptr(), self._q_codes.data_ptr(), self._q_scale.data_ptr(), sel.data_ptr(),
             count.data_ptr(), self.status.data_ptr())
         return sel, count
 
@@ -548,10 +546,8 @@ class BlockSparseAttention:
         run, length = self._run, _addr(k_len)
         q_codes, q_scale = self.q_codes.data_ptr(), self.q_scale.data_ptr()
         k_codes, k_scale = self.k_codes.data_ptr(), self.k_scale.data_ptr()
-        run("ditango_block_summary", stream, B, H, self.Nq, d, QBLOCK, Q.data_ptr(), run.strides(Q, 3), None,
-            q_codes, q_scale, None)
-        run("ditango_block_summary", stream, B, Hkv, self.Nk, d, PAGE, K.data_ptr(), run.strides(K, 3), length,
-            k_codes, k_scale, self.k_mean.data_ptr())
+        run("ditango_block_summaries", stream, B, H, Hkv, self.Nq, self.Nk, d, Q.data_ptr(), run.strides(Q, 3),
+            K.data_ptr(), run.strides(K, 3), length, q_codes, q_scale, k_codes, k_scale, self.k_mean.data_ptr())
         run("ditango_block_select", stream, B, H, Hkv, self.n_q, self.n_k, d, self.k, self.band, self.sink,
             QBLOCK // PAGE, self.room, q_codes, q_scale, k_codes, k_scale, None, 0, length,
             self.sel.data_ptr(), self.sel_count.data_ptr(), self.status.data_ptr())

@@ -101,6 +101,8 @@ _SIGS = {
                                    _P, _P, _P, _P, _P, C.c_int32, C.c_float, C.c_int32, _P, C.c_int32,
                                    _P, _P, _P, _P, C.c_size_t, _P, _P]),
     "ditango_block_summary": (C.c_int, [C.c_int32] * 5 + [_P] * 7),
+    "ditango_block_summaries": (C.c_int, [C.c_int32] * 6 + [_P] * 11),
+    "ditango_kv4_select": (C.c_int, [_KV] + [C.c_int32] * 7 + [_P] * 12),
     "ditango_block_select": (C.c_int, [C.c_int32] * 11 + [_P] * 5 + [C.c_int32] + [_P] * 5),
     "ditango_block_attn": (C.c_int, [C.c_int32] * 6 + [_P] * 8 + [C.c_int32, _P, C.c_float, _P,
                                      C.c_int32, _P, _P, _P, _P]),
@@ -387,6 +389,23 @@ def ditango_block_summary(B, H, N, d, block, x, strides, codes, scale, mean=None
     _check("ditango_block_summary", _lib.ditango_block_summary(
         B, H, N, d, block, _ptr(x), _i64s(strides), _ptr(length), _ptr(codes), _ptr(scale), _ptr(mean),
         _stream(stream)))
+
+
+def ditango_block_summaries(B, H, Hkv, Nq, Nk, d, Q, q_strides, K, k_strides, q_codes, q_scale, k_codes,
+                            k_scale, k_mean=None, k_len=None, stream=None):
+    """The summaries of Q's and of K's blocks in one launch."""
+    _check("ditango_block_summaries", _lib.ditango_block_summaries(
+        B, H, Hkv, Nq, Nk, d, _ptr(Q), _i64s(q_strides), _ptr(K), _i64s(k_strides), _ptr(k_len), _ptr(q_codes),
+        _ptr(q_scale), _ptr(k_codes), _ptr(k_scale), _ptr(k_mean), _stream(stream)))
+
+
+def ditango_kv4_select(kv, R, H, max_blocks, k, band, sink, max_sel, Q, q_strides, sum_codes, sum_scale,
+                       block_table, kv_len, q_codes, q_scale, sel, sel_count, dev_status=None, stream=None):
+    """The pages that one query token a request attends."""
+    _check("ditango_kv4_select", _lib.ditango_kv4_select(
+        C.byref(kv), R, H, max_blocks, k, band, sink, max_sel, _ptr(Q), _i64s(q_strides), _ptr(sum_codes),
+        _ptr(sum_scale), _ptr(block_table), _ptr(kv_len), _ptr(q_codes), _ptr(q_scale), _ptr(sel),
+        _ptr(sel_count), _ptr(dev_status), _stream(stream)))
 
 
 def ditango_block_select(B, H, Hkv, n_q, n_k, d, k, band, sink, own_blocks, max_sel, q_codes, q_scale,

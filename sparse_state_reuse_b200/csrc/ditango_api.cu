@@ -62,12 +62,18 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
 cudaError_t launch_block_summary(int B, int H, int N, int d, int block, const uint16_t *x,
                                  const int64_t *s, const int *len, signed char *codes, float *scale,
                                  float *mean, cudaStream_t stream);
+cudaError_t launch_block_summaries(int B, int H, int Hkv, int Nq, int Nk, int d, const uint16_t *Q,
+                                   const int64_t *qst, const uint16_t *K, const int64_t *kst, const int *k_len,
+                                   signed char *q_codes, float *q_scale, signed char *k_codes, float *k_scale,
+                                   float *k_mean, cudaStream_t stream);
 int select_max_blocks();
+bool select_by_heads(int n_q, int G, int n_k);
 cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, int k, int band, int sink,
                                 int room, int own, const signed char *qc, const float *qs,
                                 const signed char *kc, const float *ks, const int *block_table,
                                 int n_pages, const int *k_len, int *sel_out, int *count,
-                                int *dev_status, cudaStream_t stream);
+                                int *dev_status, const uint16_t *q, const int64_t *q_strides,
+                                cudaStream_t stream);
 cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B,
                               int H, int Hkv, int Nq, int Nk, int d, const int *sel, const int *count,
                               int room, const int *k_len, float scale, void *out, int out_fp32,
@@ -698,6 +704,26 @@ bool row_strides(const int64_t *s, long long T, int H, int d, int multiple, int6
   return true;
 }
 
+// (b, h, n) strides in elements, likewise.
+bool block_strides(const int64_t *s, int B, int H, int N, int d, int64_t out[3]) {
+  out[2] = N == 1 ? d : s[2];
+  out[1] = H == 1 ? out[2] * N : s[1];
+  out[0] = B == 1 ? out[1] * H : s[0];
+  return strides_ok(out);
+}
+
+// The forced band's indices fit 31 bits, and the lists hold what is always taken.
+ditango_status check_select(int n_k, int k, int band, int sink, int own, int max_sel) {
+  if (k < 0 || sink < 0 || band < -1 || own < 0 || max_sel < 1) return DITANGO_ERR_INVALID;
+  const long long near = band < 0 ? 0 : (own > 0 ? own : 1) + 2LL * band;
+  long long must = sink + near;
+  if (must < k) must = k;
+  if (must > n_k) must = n_k;
+  if (max_sel < must) return DITANGO_ERR_INVALID;
+  if (n_k > select_max_blocks() || band > (1 << 24) || own > 1024) return DITANGO_ERR_UNSUPPORTED;
+  return DITANGO_OK;
+}
+
 ditango_status kv4_rows(bool write, const ditango_kv4 *c, int64_t T, const uint16_t *K, const uint16_t *V,
                         uint16_t *Ko, uint16_t *Vo, const int64_t *ks, const int64_t *vs,
                         const int64_t *slots, int32_t *dev_status, ditango_stream stream) {
@@ -780,6 +806,42 @@ ditango_status ditango_kv4_summary(const ditango_kv4 *c, int32_t R, int32_t max_
                                         sum_scale, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
+ditango_status ditango_kv4_select(const ditango_kv4 *c, int32_t R, int32_t H, int32_t max_blocks, int32_t k,
+                                  int32_t band, int32_t sink, int32_t max_sel, const uint16_t *Q,
+                                  const int64_t q_strides[2], const int8_t *sum_codes, const float *sum_scale,
+                                  const int32_t *block_table, const int32_t *kv_len, int8_t *q_codes,
+                                  float *q_scale, int32_t *sel, int32_t *sel_count, int32_t *dev_status,
+                                  ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_kv4_select");
+  ditango_status st = check_kv4(c);
+  if (st != DITANGO_OK) return st;
+  if (R < 1 || H < 1 || H % c->Hkv || max_blocks < 1) return DITANGO_ERR_INVALID;
+  if (!Q || !q_strides || !sum_codes || !sum_scale || !block_table || !kv_len || !q_codes || !q_scale || !sel ||
+      !sel_count || !aligned16(Q))
+    return DITANGO_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(q_codes) & 7u) || (reinterpret_cast<uintptr_t>(sum_codes) & 7u))
+    return DITANGO_ERR_INVALID;
+  st = check_select(max_blocks, k, band, sink, 0, max_sel);
+  if (st != DITANGO_OK) return st;
+  if (R > kMaxRequests || H > 65535) return DITANGO_ERR_UNSUPPORTED;
+  int64_t qs[2];
+  if (!row_strides(q_strides, R, H, c->d, 8, qs)) return DITANGO_ERR_INVALID;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  // the queries' codes are formed by the selection itself where it takes all
+  // heads of a key head at once, else by a launch of their own
+  const bool fused = select_by_heads(1, H / c->Hkv, max_blocks);
+  if (!fused) {
+    const int64_t s3[3] = {qs[0], qs[1], c->d};
+    const cudaError_t e = launch_block_summary(R, H, 1, c->d, DITANGO_PAGE, Q, s3, nullptr,
+                                               reinterpret_cast<signed char *>(q_codes), q_scale, nullptr, on);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return cuda_status(launch_block_select(R, H, c->Hkv, 1, max_blocks, c->d, k, band, sink, max_sel, 0,
+                                         reinterpret_cast<const signed char *>(q_codes), q_scale,
+                                         reinterpret_cast<const signed char *>(sum_codes), sum_scale, block_table,
+                                         c->n_pages, kv_len, sel, sel_count, dev_status, fused ? Q : nullptr, qs, on));
+}
+
 size_t ditango_kv4_attn_workspace_size(int32_t d) { return dim_ok(d) ? kv4_attn_workspace_bytes(d) : 0; }
 
 ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int32_t T, int32_t max_q,
@@ -826,13 +888,30 @@ ditango_status ditango_block_summary(int32_t B, int32_t H, int32_t N, int32_t d,
     return DITANGO_ERR_INVALID;
   if (block != DITANGO_PAGE && block != DITANGO_QBLOCK) return DITANGO_ERR_INVALID;
   if (!dim_ok(d) || B > 65535 || H > 65535) return DITANGO_ERR_UNSUPPORTED;
-  int64_t s[3] = {strides[0], strides[1], strides[2]};
-  if (N == 1) s[2] = d;
-  if (H == 1) s[1] = s[2] * N;
-  if (B == 1) s[0] = s[1] * H;
-  if (!strides_ok(s)) return DITANGO_ERR_INVALID;
+  int64_t s[3];
+  if (!block_strides(strides, B, H, N, d, s)) return DITANGO_ERR_INVALID;
   return cuda_status(launch_block_summary(B, H, N, d, block, x, s, len, reinterpret_cast<signed char *>(codes),
                                           scale, mean, static_cast<cudaStream_t>(stream)));
+}
+
+ditango_status ditango_block_summaries(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk, int32_t d,
+                                       const uint16_t *Q, const int64_t q_strides[3], const uint16_t *K,
+                                       const int64_t k_strides[3], const int32_t *k_len, int8_t *q_codes,
+                                       float *q_scale, int8_t *k_codes, float *k_scale, float *k_mean,
+                                       ditango_stream stream) {
+  NvtxRange nvtx_range("ditango_block_summaries");
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || Nq < 1 || Nk < 1 || d < 1) return DITANGO_ERR_INVALID;
+  if (!Q || !K || !q_strides || !k_strides || !q_codes || !q_scale || !k_codes || !k_scale ||
+      !aligned16(Q) || !aligned16(K))
+    return DITANGO_ERR_INVALID;
+  if (!dim_ok(d) || B > 65535 || (long long)H + Hkv > 65535) return DITANGO_ERR_UNSUPPORTED;
+  int64_t qs[3], ks[3];
+  if (!block_strides(q_strides, B, H, Nq, d, qs) || !block_strides(k_strides, B, Hkv, Nk, d, ks))
+    return DITANGO_ERR_INVALID;
+  return cuda_status(launch_block_summaries(B, H, Hkv, Nq, Nk, d, Q, qs, K, ks, k_len,
+                                            reinterpret_cast<signed char *>(q_codes), q_scale,
+                                            reinterpret_cast<signed char *>(k_codes), k_scale, k_mean,
+                                            static_cast<cudaStream_t>(stream)));
 }
 
 ditango_status ditango_block_select(int32_t B, int32_t H, int32_t Hkv, int32_t n_q, int32_t n_k, int32_t d,
@@ -843,24 +922,18 @@ ditango_status ditango_block_select(int32_t B, int32_t H, int32_t Hkv, int32_t n
                                     int32_t *sel_count, int32_t *dev_status, ditango_stream stream) {
   NvtxRange nvtx_range("ditango_block_select");
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || n_q < 1 || n_k < 1 || d < 1) return DITANGO_ERR_INVALID;
-  if (k < 0 || sink < 0 || band < -1 || own_blocks < 0 || max_sel < 1) return DITANGO_ERR_INVALID;
   if (!q_codes || !q_scale || !k_codes || !k_scale || !sel || !sel_count) return DITANGO_ERR_INVALID;
   if ((reinterpret_cast<uintptr_t>(q_codes) & 7u) || (reinterpret_cast<uintptr_t>(k_codes) & 7u))
     return DITANGO_ERR_INVALID;
   if (block_table && n_pages < 1) return DITANGO_ERR_INVALID;
-  const long long near = band < 0 ? 0 : (own_blocks > 0 ? own_blocks : 1) + 2LL * band;
-  long long must = sink + near;
-  if (must < k) must = k;
-  if (must > n_k) must = n_k;
-  if (max_sel < must) return DITANGO_ERR_INVALID;
-  if (!dim_ok(d) || B > 65535 || Hkv > 65535 || n_k > select_max_blocks()) return DITANGO_ERR_UNSUPPORTED;
-  // indices of the forced band fit 31 bits
-  if (band > (1 << 24) || own_blocks > 1024 || (long long)n_q * own_blocks > (1 << 30))
+  const ditango_status st = check_select(n_k, k, band, sink, own_blocks, max_sel);
+  if (st != DITANGO_OK) return st;
+  if (!dim_ok(d) || B > 65535 || Hkv > 65535 || (long long)n_q * own_blocks > (1 << 30))
     return DITANGO_ERR_UNSUPPORTED;
   return cuda_status(launch_block_select(B, H, Hkv, n_q, n_k, d, k, band, sink, max_sel, own_blocks,
                                          reinterpret_cast<const signed char *>(q_codes), q_scale,
                                          reinterpret_cast<const signed char *>(k_codes), k_scale, block_table,
-                                         n_pages, k_len, sel, sel_count, dev_status,
+                                         n_pages, k_len, sel, sel_count, dev_status, nullptr, nullptr,
                                          static_cast<cudaStream_t>(stream)));
 }
 

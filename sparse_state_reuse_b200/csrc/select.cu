@@ -33,7 +33,7 @@ struct SummaryParams {
 };
 
 template <int D, int BLOCK>
-__global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const SummaryParams p) {
+__device__ __forceinline__ void summarise(const SummaryParams &p, int h) {
   constexpr int kGroup = (D == 64) ? 8 : 16;             // lanes of a row (12 of 16 busy at 96)
   constexpr int kPass = kSumThreads / kGroup;            // rows of one pass
   constexpr int NB = 128 / BLOCK;                        // blocks of this block of threads
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   __shared__ double s_top[NB][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = tid % kGroup, row = tid / kGroup;
-  const int blk0 = blockIdx.x * NB, h = blockIdx.y, b = blockIdx.z;
+  const int blk0 = blockIdx.x * NB, b = blockIdx.z;
   int len = p.N;
   if (p.len) len = max(0, min(p.N, __ldg(p.len + b)));
   const int left = len - blk0 * BLOCK;                   // valid rows from here on
@@ -114,6 +114,22 @@ __global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const Summar
   if (ch == 0) p.scale[at] = good ? (float)(top / (127.0 * n)) : 0.f;
 }
 
+template <int D, int BLOCK>
+__global__ void __launch_bounds__(kSumThreads) block_summary_kernel(const SummaryParams p) {
+  summarise<D, BLOCK>(p, blockIdx.y);
+}
+
+// Query blocks and key blocks in one launch: the first heads are Q's.
+template <int D>
+__global__ void __launch_bounds__(kSumThreads) block_summaries_kernel(const SummaryParams q, const SummaryParams k) {
+  const int h = blockIdx.y;
+  if (h < q.H) {
+    if (blockIdx.x < q.nb) summarise<D, kQBlock>(q, h);
+  } else if (blockIdx.x * (kQBlock / kPage) < k.nb) {
+    summarise<D, kPage>(k, h - q.H);
+  }
+}
+
 // ---------------------------------------------------------------- selection
 template <bool HEADS>
 constexpr int kSelThreads = HEADS ? 512 : 256;
@@ -124,6 +140,8 @@ struct SelectParams {
   int own;                      // key blocks of a query block; 0: the query stands at the end
   const signed char *qc, *kc;
   const float *qs, *ks;
+  const uint16_t *q;            // HEADS: the queries themselves, (b, head) strides qb and qh, or null
+  long long qb, qh;
   const int *block_table;       // [B, n_k] or null
   const int *k_len;             // [B] tokens, or null
   int *sel, *count, *dev_status;
@@ -284,8 +302,36 @@ __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const 
     const int page = page_of(j);
     return page < 0 ? 0.f : __ldg(p.ks + (size_t)page * p.Hkv + h);
   };
-  // HEADS: the scale of each key block and its page, read at once and not by
-  // the chain of each product
+  // HEADS: the codes of single queries, formed here; the scale of each key block
+  // and its page, read at once and not by the chain of each product
+  __shared__ __align__(16) signed char q_code[HEADS ? 16 : 1][D];
+  __shared__ float q_scale[16];
+  if constexpr (HEADS) {
+    for (int g = warp; p.q && g < rows; g += kWarps) {
+      float f[8], top = 0.f;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (lane < D / 8) u = __ldg(reinterpret_cast<const uint4 *>(p.q + b * p.qb + (h * p.G + g) * p.qh) + lane);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = bf_lo(w[e]);
+        f[2 * e + 1] = bf_hi(w[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, isfinite(f[e]) ? fabsf(f[e]) : INFINITY);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool good = top > 0.f && top < INFINITY;
+      uint32_t c[2] = {0u, 0u};
+      if (good) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          c[e / 4] |= (uint32_t)((int)rint((double)f[e] * 127.0 / (double)top) & 0xff) << (8 * (e % 4));
+      }
+      if (lane < D / 8) *reinterpret_cast<uint2 *>(&q_code[g][lane * 8]) = make_uint2(c[0], c[1]);
+      if (lane == 0) q_scale[g] = good ? (float)((double)top / 127.0) : 0.f;
+    }
+  }
   float *scale = reinterpret_cast<float *>(score + rows * p.stride);
   int *pages = reinterpret_cast<int *>(scale + p.stride);
   if constexpr (HEADS) {
@@ -330,11 +376,13 @@ __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const 
       const bool live = row < rows;
       const size_t at = HEADS ? ((size_t)b * p.Hkv + h) * p.G + (live ? row : 0)
                               : (((size_t)b * p.Hkv + h) * p.G + g) * p.n_q + i0 + (live ? row : 0);
-      qs[x] = live ? __ldg(p.qs + at) : 0.f;
-      const uint2 *src = reinterpret_cast<const uint2 *>(p.qc + at * D + t * (D / 4));
+      const bool here = HEADS && p.q != nullptr;
+      qs[x] = !live ? 0.f : (here ? q_scale[row & 15] : __ldg(p.qs + at));
+      const uint2 *src = reinterpret_cast<const uint2 *>(here ? &q_code[HEADS && live ? row : 0][t * (D / 4)]
+                                                              : p.qc + at * D + t * (D / 4));
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const uint2 u = live ? __ldg(src + s) : make_uint2(0, 0);
+        const uint2 u = live ? src[s] : make_uint2(0, 0);
         a[s][x] = u.x;
         a[s][2 + x] = u.y;
       }
@@ -480,11 +528,36 @@ cudaError_t launch_block_summary(int B, int H, int N, int d, int block, const ui
   return cudaGetLastError();
 }
 
+cudaError_t launch_block_summaries(int B, int H, int Hkv, int Nq, int Nk, int d, const uint16_t *Q,
+                                   const int64_t *qst, const uint16_t *K, const int64_t *kst, const int *k_len,
+                                   signed char *q_codes, float *q_scale, signed char *k_codes, float *k_scale,
+                                   float *k_mean, cudaStream_t stream) {
+  const sel::SummaryParams q{H, Nq, (Nq + kQBlock - 1) / kQBlock, Q, qst[0], qst[1], qst[2], nullptr,
+                             q_codes, q_scale, nullptr};
+  const sel::SummaryParams k{Hkv, Nk, (Nk + kPage - 1) / kPage, K, kst[0], kst[1], kst[2], k_len,
+                             k_codes, k_scale, k_mean};
+  const int rows = Nq > Nk ? Nq : Nk;
+  const dim3 grid((unsigned)((rows + kQBlock - 1) / kQBlock), (unsigned)(H + Hkv), (unsigned)B);
+  switch (d) {
+    case 64: sel::block_summaries_kernel<64><<<grid, sel::kSumThreads, 0, stream>>>(q, k); break;
+    case 96: sel::block_summaries_kernel<96><<<grid, sel::kSumThreads, 0, stream>>>(q, k); break;
+    case 128: sel::block_summaries_kernel<128><<<grid, sel::kSumThreads, 0, stream>>>(q, k); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+// One query block a head group, with the scores of all its heads beside one
+// another in shared memory.
+bool select_by_heads(int n_q, int G, int n_k) {
+  return n_q == 1 && G <= 16 && (G + 2LL) * sel::row_stride(n_k) * 4 <= sel::kMaxScoreBytes;
+}
+
 cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, int k, int band, int sink,
                                 int room, int own, const signed char *qc, const float *qs,
                                 const signed char *kc, const float *ks, const int *block_table,
                                 int n_pages, const int *k_len, int *sel_out, int *count, int *dev_status,
-                                cudaStream_t stream) {
+                                const uint16_t *q, const int64_t *q_strides, cudaStream_t stream) {
   sel::SelectParams p;
   p.Hkv = Hkv;
   p.G = H / Hkv;
@@ -502,6 +575,9 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
   p.ks = ks;
   p.block_table = block_table;
   p.k_len = k_len;
+  p.q = q;
+  p.qb = q ? q_strides[0] : 0;
+  p.qh = q ? q_strides[1] : 0;
   p.sel = sel_out;
   p.count = count;
   p.dev_status = dev_status;
@@ -509,7 +585,7 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
   p.stride = sel::row_stride(n_k);
   int rows = 16;
   while (rows > 1 && (rows / 2 >= n_q || (long long)rows * p.stride * 4 > 100 * 1024)) rows /= 2;
-  const bool heads = n_q == 1 && p.G <= 16 && (p.G + 2LL) * p.stride * 4 <= sel::kMaxScoreBytes;
+  const bool heads = select_by_heads(n_q, p.G, n_k);
   p.rows = rows;
   const int bytes = (heads ? p.G + 2 : rows) * p.stride * 4;
   switch (d) {

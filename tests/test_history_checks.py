@@ -78,6 +78,20 @@ def test_summary_select_and_attention_refuse():
                    (dict(q_codes=A + 4), 1), (dict(block_table=A, n_pages=0), 1), (dict(sel_count=None), 1),
                    (dict(own_blocks=-1), 1)):
         refused(dt.ditango_block_select, status=st, **{**ok, **kw})
+    ok = dict(B=1, H=4, Hkv=2, Nq=10, Nk=10, d=64, Q=A, q_strides=s, K=2 * A, k_strides=s, q_codes=A, q_scale=A,
+              k_codes=A, k_scale=A)
+    for kw, st in ((dict(H=3), 1), (dict(d=72), 2), (dict(Nk=0), 1), (dict(Q=A + 2), 1), (dict(K=None), 1),
+                   (dict(k_strides=(1280, 640, 60)), 1), (dict(k_scale=None), 1), (dict(H=65534), 2),
+                   (dict(H=2 ** 31 - 2), 2), (dict(B=70000), 2)):
+        refused(dt.ditango_block_summaries, status=st, **{**ok, **kw})
+    ok = dict(R=2, H=4, max_blocks=7, k=3, band=1, sink=1, max_sel=4, Q=A, q_strides=(256, 64), sum_codes=A,
+              sum_scale=A, block_table=A, kv_len=A, q_codes=A, q_scale=A, sel=A, sel_count=A)
+    for kw, st in ((dict(R=0), 1), (dict(R=5000), 2), (dict(H=3), 1), (dict(max_blocks=0), 1), (dict(k=-1), 1),
+                   (dict(max_sel=3), 1), (dict(band=-2), 1), (dict(max_blocks=60000), 2), (dict(Q=A + 8), 1),
+                   (dict(q_strides=(256, 60)), 1), (dict(q_strides=None), 1), (dict(kv_len=None), 1),
+                   (dict(sum_codes=A + 4), 1), (dict(q_codes=None), 1), (dict(band=2 ** 25, max_sel=8), 2)):
+        refused(dt.ditango_kv4_select, dt.kv4(4, 2, 64, A), status=st, **{**ok, **kw})
+    refused(dt.ditango_kv4_select, dt.kv4(4, 2, 80, A), status=2, **ok)
     ok = dict(B=1, H=2, Hkv=1, Nq=10, Nk=10, d=64, Q=A, K=2 * A, V=3 * A, q_strides=s, k_strides=s, v_strides=s,
               sel=A, sel_count=A, max_sel=2, out=8 * A, out_is_fp32=0)
     for kw, st in ((dict(H=3, Hkv=2), 1), (dict(d=80), 2), (dict(Nq=0), 1), (dict(max_sel=0), 1),
