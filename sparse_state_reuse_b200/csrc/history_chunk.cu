@@ -19,7 +19,7 @@
 // K and V apart and both twice buffered: a V buffer is in use from one row
 // tile's product to the other's, half a step later, so that a single one leaves
 // no time to write it (with it, and with the codes staged in shared memory by
-// bulk copies, history_frame of perf/operators.py took 2.06 ms).  The codes are
+// bulk copies, the call below took 2.06 ms).  The codes are
 // read 16 bytes at a time into the registers that the tile before just left.
 // Channels keep the unpacked order (0 4 1 5 2 6 3 7 of each 8), and of the
 // second 64 the groups of 16 are exchanged in pairs of groups, which spreads the
@@ -35,6 +35,15 @@
 // TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 384), O1 [384, 512); the fp16 P
 // overwrites the first 64 columns of its S.  Each block takes an equal share of
 // the line of work.
+//
+// 3600 queries over 25200 tokens, 24 heads of 96: 1.19 ms, 703 TFLOP/s (43% of the
+// measured bf16 rate); the tensor pipe is busy 39% of the time, the exponentials'
+// unit 48%, the issue slots 51%.  The step of a row tile is a chain, Q K^T (1/5 of
+// it), softmax (3/5) and P V (1/5), of which the two row tiles hide only each
+// other's products.  Scores in halves of 64 keys, so that one half's product runs
+// under the other's softmax, took away most of the wait for S but make Q K^T twice
+// as dear (64 columns do not fill the tensor pipe) and crowd the exponentials:
+// 1.32 ms.
 #include <mutex>
 #include <set>
 
