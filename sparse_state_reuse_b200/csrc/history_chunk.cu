@@ -37,8 +37,8 @@
 // the line of work.
 //
 // 3600 queries over 25200 tokens, 24 heads of 96: 1.19 ms, 703 TFLOP/s (43% of the
-// measured bf16 rate); the tensor pipe is busy 39% of the time, the exponentials'
-// unit 48%, the issue slots 51%.  The step of a row tile is a chain, Q K^T (1/5 of
+// measured bf16 rate); the tensor pipe is busy 37% of the time, the exponentials'
+// unit 46%, the issue slots 47%.  The step of a row tile is a chain, Q K^T (1/5 of
 // it), softmax (3/5) and P V (1/5), of which the two row tiles hide only each
 // other's products.  Scores in halves of 64 keys, so that one half's product runs
 // under the other's softmax, took away most of the wait for S but make Q K^T twice
