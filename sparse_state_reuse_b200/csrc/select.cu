@@ -168,6 +168,15 @@ __device__ __forceinline__ float score_of(uint32_t u) {
 }
 constexpr uint32_t kForced = 0xffffffffu;
 
+// Where the search looks next between lo and hi.
+__device__ __forceinline__ uint32_t next_mid(uint32_t lo, uint32_t hi, int step) {
+  if ((step & 3) != 3) {
+    const uint32_t x = order_of(0.5f * score_of(lo) + 0.5f * score_of(hi - 1));
+    if (x > lo && x < hi) return x;
+  }
+  return lo + (hi - lo) / 2;
+}
+
 // Warp-wide choice of one row: the threshold between what is taken and what is
 // not, then the list in ascending order.  The search starts from the least and
 // greatest score and ends as soon as the count is met.  A step halves the
@@ -218,11 +227,7 @@ __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, i
     int at_hi = n_forced;
     bool met = false;
     for (int step = 0; hi - lo > 1; ++step) {
-      uint32_t mid = lo + (hi - lo) / 2;
-      if ((step & 3) != 3) {
-        const uint32_t x = order_of(0.5f * score_of(lo) + 0.5f * score_of(hi - 1));
-        if (x > lo && x < hi) mid = x;
-      }
+      const uint32_t mid = next_mid(lo, hi, step);
       int c = 0;
       if constexpr (REG > 0) {
 #pragma unroll
@@ -270,6 +275,110 @@ __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, i
   }
   for (int j = out + lane; j < room; j += 32) dst[j] = -1;
   if (lane == 0) *count = min(out, room);
+}
+
+// The same choice by all threads of a block, each with a run of neighbouring
+// entries in shared memory (an odd number of them: no bank conflicts), for a row
+// that has the block to itself.  Loops instead of the unrolled registers above:
+// a kernel that runs once a step finds its code in no cache, and that was most of
+// the 7 us that one warp took for 1200 entries.
+template <int THREADS>
+__device__ __forceinline__ void choose_block(const uint32_t *key, int nk, int k, int room, int *dst, int *count) {
+  constexpr int WARPS = THREADS / 32;
+  static_assert(WARPS <= 32, "one value a warp is summed by one warp");
+  __shared__ uint32_t part[4][WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = ((nk + THREADS - 1) / THREADS) | 1, j0 = min(nk, tid * per), j1 = min(nk, j0 + per);
+  uint32_t least = kForced, most = 0, forced = 0;
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t x = key[j];
+    if (x == kForced) {
+      ++forced;
+    } else {
+      least = min(least, x);
+      most = max(most, x);
+    }
+  }
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    part[0][warp] = forced;
+    part[1][warp] = least;
+    part[2][warp] = most;
+  }
+  __syncthreads();
+  const int from = min(lane, WARPS - 1);
+  const int n_forced = (int)__reduce_add_sync(0xffffffffu, lane < WARPS ? part[0][from] : 0u);
+  least = __reduce_min_sync(0xffffffffu, part[1][from]);
+  most = __reduce_max_sync(0xffffffffu, part[2][from]);
+  const int need = min(nk, max(n_forced, k));
+  uint32_t above = 0;
+  int ties = 0;
+  __syncthreads();
+  if (need == n_forced) {
+    above = kForced - 1;
+  } else if (need < nk) {
+    uint32_t lo = least, hi = most + 1;
+    int at_hi = n_forced;
+    bool met = false;
+    for (int step = 0; hi - lo > 1; ++step) {
+      const uint32_t mid = next_mid(lo, hi, step);
+      uint32_t c = 0;
+      for (int j = j0; j < j1; ++j) c += key[j] >= mid;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) part[step & 1][warp] = c;      // two places in turn: one barrier a step
+      __syncthreads();
+      const int all = (int)__reduce_add_sync(0xffffffffu, lane < WARPS ? part[step & 1][from] : 0u);
+      if (all == need) {
+        above = mid - 1;
+        met = true;
+        break;
+      }
+      if (all > need) {
+        lo = mid;
+      } else {
+        hi = mid;
+        at_hi = all;
+      }
+    }
+    if (!met) {
+      above = lo;
+      ties = need - at_hi;
+    }
+  }
+  // entries above in the low half, equal ones in the high half (at most 51200 each)
+  uint32_t mine = 0;
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t x = key[j];
+    mine += (x > above ? 1u : 0u) + (ties > 0 && x == above ? 0x10000u : 0u);
+  }
+  uint32_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) part[3][warp] = upto;
+  __syncthreads();
+  uint32_t before = upto - mine, total = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += part[3][w];
+    total += part[3][w];
+  }
+  int equal = (int)(before >> 16), at = (int)(before & 0xffffu) + min(equal, ties);
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t x = key[j];
+    bool take = x > above;
+    if (ties > 0 && x == above) take = equal++ < ties;
+    if (take) {
+      if (at < room) dst[at] = j;
+      ++at;
+    }
+  }
+  const int out = (int)(total & 0xffffu) + min((int)(total >> 16), ties);
+  for (int j = out + tid; j < room; j += THREADS) dst[j] = -1;
+  if (tid == 0) *count = min(out, room);
 }
 
 // One block of threads: up to 16 query blocks of one key head, whose scores of
@@ -325,45 +434,46 @@ __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const 
   __shared__ float q_scale[16];
   if constexpr (HEADS) {
     for (int g = warp; p.q && g < rows; g += kWarps) {
-      float f[8], top = 0.f;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (lane < D / 8) u = __ldg(reinterpret_cast<const uint4 *>(p.q + b * p.qb + (h * p.G + g) * p.qh) + lane);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      // a row by itself: 127 x has 15 bits and x / top 8 by 8, so that fp32's
+      // quotient is exact in a tie and no other comes near one; 2^-16 keeps 127 x
+      // of the largest values finite, and what it could round is far below a code
+      constexpr int kOwn = D / 32;
+      const uint16_t *src = p.q + b * p.qb + (h * p.G + g) * p.qh + lane * kOwn;
+      float f[kOwn], top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] = bf_lo(w[e]);
-        f[2 * e + 1] = bf_hi(w[e]);
+      for (int e = 0; e < kOwn; ++e) {
+        f[e] = __uint_as_float((uint32_t)__ldg(src + e) << 16);
+        top = fmaxf(top, isfinite(f[e]) ? fabsf(f[e]) : INFINITY);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, isfinite(f[e]) ? fabsf(f[e]) : INFINITY);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool good = top > 0.f && top < INFINITY;
-      uint32_t c[2] = {0u, 0u};
-      if (good) {
+      const float down = top > 1e30f ? 0x1p-16f : 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          c[e / 4] |= (uint32_t)((int)rint((double)f[e] * 127.0 / (double)top) & 0xff) << (8 * (e % 4));
-      }
-      if (lane < D / 8) *reinterpret_cast<uint2 *>(&q_code[g][lane * 8]) = make_uint2(c[0], c[1]);
-      if (lane == 0) q_scale[g] = good ? (float)((double)top / 127.0) : 0.f;
+      for (int e = 0; e < kOwn; ++e)
+        q_code[g][lane * kOwn + e] =
+            good ? (signed char)(int)rintf(__fdiv_rn(f[e] * down * 127.f, top * down)) : (signed char)0;
+      if (lane == 0) q_scale[g] = good ? __fdiv_rn(top, 127.f) : 0.f;
     }
   }
   float *scale = reinterpret_cast<float *>(score + rows * p.stride);
   int *pages = reinterpret_cast<int *>(scale + p.stride);
   if constexpr (HEADS) {
+    // the warps without a query head, if there are any, are done with it at once
+    const int from = p.q && rows < kWarps ? rows * 32 : 0;
     constexpr int kOnce = 4;
-    for (int j0 = tid; j0 < nk; j0 += kThreads * kOnce) {
+    const int step = kThreads - from;
+    for (int j0 = tid - from; j0 >= 0 && j0 < nk; j0 += step * kOnce) {
       int page[kOnce];
       float s[kOnce];
 #pragma unroll
       for (int e = 0; e < kOnce; ++e) {
-        const int j = j0 + e * kThreads;
+        const int j = j0 + e * step;
         page[e] = j < nk && p.block_table ? __ldg(p.block_table + (size_t)b * p.n_k + j) : j;
       }
 #pragma unroll
       for (int e = 0; e < kOnce; ++e) {
-        const int j = j0 + e * kThreads;
+        const int j = j0 + e * step;
         const bool good = !p.block_table || (page[e] >= 0 && page[e] < p.n_pages);
         if (j < nk && !good) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
         if (!good) page[e] = -1;
@@ -372,7 +482,7 @@ __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const 
       }
 #pragma unroll
       for (int e = 0; e < kOnce; ++e) {
-        const int j = j0 + e * kThreads;
+        const int j = j0 + e * step;
         if (j >= nk) break;
         scale[j] = s[e];
         pages[j] = page[e];
@@ -475,10 +585,13 @@ __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const 
       score[j] = j < p.sink || (j >= first && j <= last) ? kForced : order_of(__fmul_rn(x, scale[j]));
     }
     __syncthreads();
-  }
-  for (int row = warp; row < (HEADS ? 1 : rows); row += kWarps) {
-    const size_t at = ((size_t)b * p.Hkv + h) * p.n_q + i0 + row;
-    choose_row<REG>(score + row * p.stride, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
+    const size_t at = (size_t)b * p.Hkv + h;
+    choose_block<kThreads>(score, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
+  } else {
+    for (int row = warp; row < rows; row += kWarps) {
+      const size_t at = ((size_t)b * p.Hkv + h) * p.n_q + i0 + row;
+      choose_row<REG>(score + row * p.stride, nk, p.k, p.room, p.sel + at * p.room, p.count + at);
+    }
   }
 }
 
@@ -513,8 +626,10 @@ cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t 
 // lane; a longer one is read from shared memory.
 template <int D, bool HEADS>
 cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t stream) {
-  if (p.n_k <= 32 * 16) return launch_select<D, 16, HEADS>(p, B, bytes, stream);
-  if (p.n_k <= 32 * 48) return launch_select<D, 48, HEADS>(p, B, bytes, stream);
+  if constexpr (!HEADS) {
+    if (p.n_k <= 32 * 16) return launch_select<D, 16, HEADS>(p, B, bytes, stream);
+    if (p.n_k <= 32 * 48) return launch_select<D, 48, HEADS>(p, B, bytes, stream);
+  }
   return launch_select<D, 0, HEADS>(p, B, bytes, stream);
 }
 

@@ -496,6 +496,46 @@ def test_selection_over_a_long_table_and_with_fewer_requests():
     assert got[0][1].tolist() == [[7], [1], [7]]
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_single_queries_of_any_size_and_equal_scores(d):
+    """Both ways to a single query's list (its codes formed by the selection, or
+    before it) and the oracle agree on rows of huge, tiny, zero and not finite
+    values, and on pages that are all alike (ties)."""
+    rng = np.random.default_rng(d)
+    kv, Hkv, H = [1500] * 6, 2, 4
+    c, host, table = filled(rng, kv, Hkv, d, H, 6)
+    q = HC.bf16_round(rng.standard_normal((6, H, d)))
+    q[0] *= 2.0 ** 126 / 2
+    q[1] = HC.bf16_round(q[1] * 2.0 ** -128)
+    q[2] = 0
+    q[3, 1, 5] = np.inf
+    q[4] = HC.bf16_round(np.sign(q[4]) * 2.0 ** 127 * 1.9)
+    Q = HC.up(q)
+    q = Q.float().cpu().numpy().astype(np.float64)
+    long_ = dt.KV4Cache(c.n_pages, Hkv, d, 6, 14000, 6, H=H, data=c.data)
+    long_.block_table[:, :table.shape[1]] = c.block_table
+    long_.kv_len.copy_(c.kv_len)
+    for alike in (False, True):
+        for x in (c, long_):
+            x.summarize(ints([0] * 6))
+            if alike:
+                x.sum_codes.fill_(3)
+                x.sum_scale.fill_(0.25)
+        codes, scale = c.sum_codes.cpu().numpy(), c.sum_scale.cpu().numpy()
+        for k, band, sink in ((5, 0, 1), (24, -1, 0), (1, -1, 0)):
+            got = [[t.cpu() for t in x.select(Q, k, band, sink)] for x in (c, long_)]
+            assert all(torch.equal(a, b) for a, b in zip(*got))
+            for r in range(6):
+                for h in range(Hkv):
+                    qs = [OH.summary(q[r, g:g + 1]) for g in range(2 * h, 2 * h + 2)]
+                    with np.errstate(all="ignore"):
+                        sc = OH.scores([x[0] for x in qs], [x[1] for x in qs], codes[table[r, :24], h],
+                                       scale[table[r, :24], h])
+                    forced = set(range(sink)) | ({23} if band == 0 else set())
+                    want = OH.choose(sc, forced, k)
+                    assert got[0][0][r, h, :len(want)].tolist() == want and got[0][1][r, h] == len(want)
+
+
 def test_pages_past_four_gib():
     """The same tokens on the first pages of a small cache and on the last ones of
     a cache of more than 2^32 bytes: every result is the same."""
