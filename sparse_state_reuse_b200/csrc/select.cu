@@ -280,8 +280,8 @@ __device__ __forceinline__ void choose_row(const uint32_t *key, int nk, int k, i
 // The same choice by all threads of a block, each with a run of neighbouring
 // entries in shared memory (an odd number of them: no bank conflicts), for a row
 // that has the block to itself.  Loops instead of the unrolled registers above:
-// a kernel that runs once a step finds its code in no cache, and that was most of
-// the 7 us that one warp took for 1200 entries.
+// a kernel that runs once a step finds its code in no cache (one warp with the
+// row in registers took 7 us for 1200 entries, this 4.5).
 template <int THREADS>
 __device__ __forceinline__ void choose_block(const uint32_t *key, int nk, int k, int room, int *dst, int *count) {
   constexpr int WARPS = THREADS / 32;
@@ -389,8 +389,9 @@ __device__ __forceinline__ void choose_block(const uint32_t *key, int nk, int k,
 // and shared memory anyway and the products are 3% of the time.  600 x 1200 blocks
 // of 40 heads of 128: 232 us, a fifth of it the threshold search; bound by the
 // chains of latencies of 16 warps an SM (the scores' 78 KB leave room for two
-// blocks).  HEADS, 16 requests of up to 1200 pages, 8 key heads: 22 us, of which
-// the codes' 15 MB are 2; the rest is one block's chain of reads, search and list.
+// blocks).  HEADS, 16 requests of up to 1200 pages, 8 key heads: 18 us cold, of which
+// the codes' 15 MB are 2; the rest is one block's chain: queries' codes 2, scores 6,
+// search and list 4.5.
 template <int D, int REG, bool HEADS>
 __global__ void __launch_bounds__(kSelThreads<HEADS>) block_select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int KS = D / 32, kThreads = kSelThreads<HEADS>, kWarps = kThreads / 32;
