@@ -416,7 +416,9 @@ typedef struct {
  *   pages_used   dev int32 [1] out: entries of free_pages taken.
  * A request that does not fit (a negative length, more than max_blocks pages,
  * the free list or max_tokens exhausted) takes nothing: its kv_len stays
- * ctx_len, its tokens' slots are -1, and DITANGO_ERR_BOUNDS is recorded. */
+ * ctx_len, its tokens' slots are -1, and DITANGO_ERR_BOUNDS is recorded.  What it
+ * lacked counts against the requests behind it that need pages or token places
+ * themselves, not against those that need none. */
 ditango_status ditango_block_tables(int32_t R, int32_t max_blocks, int32_t max_tokens,
                                     int32_t n_pages, const int32_t *ctx_len,
                                     const int32_t *new_len, const int32_t *free_pages,

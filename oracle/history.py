@@ -70,7 +70,7 @@ def tables(ctx, new, free, table, max_tokens):
         ok = ctx[r] >= 0 and new[r] >= 0 and -(-(c + n) // PAGE) <= width
         have, need = -(-c // PAGE), -(-(c + n) // PAGE)
         extra = need - have if ok else 0
-        fits = ok and at + n <= max_tokens and taken + extra <= len(free)
+        fits = ok and (n == 0 or at + n <= max_tokens) and (extra == 0 or taken + extra <= len(free))
         if fits:
             for k in range(extra):
                 table[r, have + k] = free[taken + k]

@@ -79,10 +79,11 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   for (int r = r0; r < r1; ++r) {
     int c, n, e;
     bool ok = lens(r, c, n, e);
-    const bool fits = ok && it + n <= cap && ip + e <= p.n_free;
+    // what a request does not need cannot be short
+    const bool fits = ok && (n == 0 || it + n <= cap) && (e == 0 || ip + e <= p.n_free);
     off[r] = (int)min(it, cap);
     // a request that does not fit takes no page: its entry says so
-    first[r] = fits ? (int)ip : -1;
+    first[r] = fits ? (e > 0 ? (int)ip : 0) : -1;
     if (fits) {
       if (e > 0) atomicMax(&s_used, (int)ip + e);
     } else {

@@ -85,6 +85,17 @@ def test_requests_that_do_not_fit_take_nothing(what):
     check_tables(run_tables(ctx, new, n_pages, width, T, free, table), want)
 
 
+def test_a_request_that_needs_nothing_fits_behind_one_that_does_not():
+    """No free page left for the first request, too many tokens for the second:
+    the third (room on its last page, if there are token places) and the fourth
+    (idle) go on."""
+    ctx, new, table = [64, 10, 70, 20], [1, 500, 3, 0], np.arange(12).reshape(4, 3)
+    for T, fits in ((64, [False, False, False, True]), (1000, [False, False, True, True])):
+        want = OH.tables(ctx, new, [], table, T)
+        assert [k == c + n for k, c, n in zip(want[1], ctx, new)] == fits and want[-1]
+        check_tables(run_tables(ctx, new, 12, 3, T, [], table), want)
+
+
 def test_a_page_number_out_of_range_gives_no_slot():
     table = np.array([[3, 99, 0]])
     c = run_tables([100], [60], 8, 3, 64, [5], table)
