@@ -696,10 +696,17 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
   // Up to 16 rows of a key head go to the kernel of few rows, more to the one
-  // of tcgen05 tiles of 128 rows.
-  const long long most = (long long)max_q * p.G;
+  // of tcgen05 tiles of 128 rows; which of a batch's requests are which only the
+  // device knows, so that both look.  A single request that may have more goes to
+  // the latter whatever it has: the other's look is 3 us.
+  const long long most = (long long)(max_q < T ? max_q : T) * p.G;
   p.min_rows = 0;
-  p.max_rows = most > hattn::kRows ? hattn::kRows : 0x7fffffffffffLL;
+  p.max_rows = 0x7fffffffffffLL;
+  if (most > hattn::kRows && R == 1) {
+    p.counters += hattn::kMaxBlocks;
+    return launch_kv4_chunk(p, d, num_sms, stream);
+  }
+  if (most > hattn::kRows) p.max_rows = hattn::kRows;
   cudaError_t e = cudaErrorInvalidValue;
   switch (d) {
 #define DITANGO_KV4(D)                                                                  \
