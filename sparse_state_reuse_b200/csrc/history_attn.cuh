@@ -96,22 +96,35 @@ struct Range {
   int r;
 };
 
-// All THREADS threads take part; sm: WARPS + 1 long longs and an int.
-template <int TR, int UNIT, int SETUP, int THREADS>
+// All THREADS threads take part; sm: WARPS + 1 long longs and an int.  WHOLE: a
+// number of blocks that is a multiple of the items' is preferred where it costs
+// less than one block in 16: items of one length are then cut into equal parts
+// and no block begins two (500 queries over 5000 tokens, 10 and 2 heads: 57 us
+// without it, 50 us with it.  Few rows: the same, less the time to count the items).
+template <int TR, int UNIT, int SETUP, int THREADS, bool WHOLE = false>
 __device__ __forceinline__ bool find_range(const Params &p, long long min_units, Range &g, long long *sm, int *sm_r) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x;
   g.total = 0;
+  long long items = 0;
   long long v = 0, at = 0;           // of request tid: its work and place; all there is up to THREADS requests
   for (int base = 0; base < p.R; base += THREADS) {
     const int r = base + tid;
     long long sum;
-    v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
+    Request q;
+    q.tiles = q.units = 0;
+    if (r < p.R) q = request_of<TR, UNIT>(p, r);
+    v = work_of<SETUP>(p, q);
     at = block_scan<WARPS>(v, sum, sm);
     g.total += sum;
+    if constexpr (WHOLE) {
+      block_scan<WARPS>((long long)q.tiles * p.Hkv, sum, sm);
+      items += sum;
+    }
   }
   const long long most = (g.total + min_units - 1) / min_units;
   g.n_blk = most < (long long)gridDim.x ? most : (long long)gridDim.x;
+  if (items > 0 && items < g.n_blk && (g.n_blk % items) * 16 <= g.n_blk) g.n_blk -= g.n_blk % items;
   if ((long long)blockIdx.x >= g.n_blk) return false;
   g.w0 = g.total * blockIdx.x / g.n_blk;
   g.w1 = g.total * (blockIdx.x + 1) / g.n_blk;

@@ -70,7 +70,7 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxBlocks = 160;      // most blocks of a launch (the workspace has room for them)
 // A block's share is at least this many tiles: below, joining the parts of an
 // item costs more than the shorter share saves.
-constexpr int kMinUnits = 6;
+constexpr int kMinUnits = 4;
 constexpr int kSetup = 2;            // tiles that beginning and finishing an item counts for
 
 // What is known of a tile before its codes are unpacked.
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 
   {
     hattn::Range g;
-    if (!hattn::find_range<TR, 2, kSetup, kThreads>(p, kMinUnits, g, s_scan, &s_request)) return;
+    if (!hattn::find_range<TR, 2, kSetup, kThreads, true>(p, kMinUnits, g, s_scan, &s_request)) return;
     if (lane == 0) s_walk[warp].start(p, g);
     if (threadIdx.x == 0) s_range = g;
   }
