@@ -44,7 +44,6 @@ namespace hattn {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;            // rows of a tile, at most
 constexpr int kMaxBlocks = 768;      // most blocks of a launch (the workspace has room for them)
 constexpr int kSetup = 8;            // pages that beginning and finishing an item counts for
 // p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
@@ -695,18 +694,20 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   p.counters = reinterpret_cast<int *>(p.partial + partial_floats(d));
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
-  // Up to 16 rows of a key head go to the kernel of few rows, more to the one
-  // of tcgen05 tiles of 128 rows; which of a batch's requests are which only the
-  // device knows, so that both look.  A single request that may have more goes to
-  // the latter whatever it has: the other's look is 3 us.
-  const long long most = (long long)(max_q < T ? max_q : T) * p.G;
-  p.min_rows = 0;
-  p.max_rows = 0x7fffffffffffLL;
-  if (most > hattn::kRows && R == 1) {
+  // Which requests of a batch have few rows, and how long they are, only the
+  // device knows: both kernels are launched and each takes its own, unless the
+  // bounds say enough.  (A launch that takes nothing costs 3 us.)
+  const long long rows = (long long)T * p.G, most = (long long)(max_q < T ? max_q : T) * p.G;
+  const long long tiles = (rows + hattn::kRows - 1) / hattn::kRows;
+  const bool few =
+      most <= hattn::kRows || ((double)tiles + R) * Hkv * ((sel ? max_sel : max_blocks) + 8.0) <= (double)hattn::kFewWork;
+  const bool many = !few && R == 1 && (double)tiles * Hkv * 9 > (double)hattn::kFewWork;
+  if (many) {
+    p.side = hattn::kAllRequests;
     p.counters += hattn::kMaxBlocks;
     return launch_kv4_chunk(p, d, num_sms, stream);
   }
-  if (most > hattn::kRows) p.max_rows = hattn::kRows;
+  p.side = few ? hattn::kAllRequests : hattn::kFewSide;
   cudaError_t e = cudaErrorInvalidValue;
   switch (d) {
 #define DITANGO_KV4(D)                                                                  \
@@ -721,9 +722,8 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
 #undef DITANGO_KV4
     default: break;
   }
-  if (e != cudaSuccess || most <= hattn::kRows) return e;
-  p.min_rows = hattn::kRows + 1;
-  p.max_rows = 0x7fffffffffffLL;
+  if (e != cudaSuccess || few) return e;
+  p.side = hattn::kManySide;
   p.counters += hattn::kMaxBlocks;
   return launch_kv4_chunk(p, d, num_sms, stream);
 }

@@ -31,10 +31,19 @@ struct Params {
   long long lt, lh;
   float *partial;                    // two parts of items a block
   int *counters;                     // one a block, all zero between launches
-  long long min_rows, max_rows;      // requests of fewer or more rows are left to the other kernel
+  int side;                          // which requests are this launch's, see Side
   int *dev_status;
   long long wait_limit_ns;
 };
+
+// A launch takes all requests, or the ones that are the few-row kernel's or the
+// many-row kernel's of a batch that is launched on both.
+enum Side : int { kAllRequests = 0, kFewSide = 1, kManySide = 2 };
+
+// The requests that a launch takes, once the device has looked: the others are
+// left to the other kernel.
+enum Rows : int { kAllRows, kFewRows, kManyRows, kNoRows };
+constexpr int kRows = 16;            // rows of a key head that the kernel of few rows takes in one tile
 
 struct Request {
   int n_q, kv, q0, tiles, units;   // units: work of one item, at least 1
@@ -43,7 +52,7 @@ struct Request {
 // Request r in row tiles of TR rows and units of UNIT pages.  Offsets and lengths
 // that cannot be are recorded and clipped.
 template <int TR, int UNIT>
-__device__ __forceinline__ Request request_of(const Params &p, int r) {
+__device__ __forceinline__ Request request_of(const Params &p, int r, Rows mine) {
   Request q;
   q.q0 = __ldg(p.q_off + r);
   const int q1 = __ldg(p.q_off + r + 1);
@@ -56,7 +65,8 @@ __device__ __forceinline__ Request request_of(const Params &p, int r) {
     if (q.q0 < 0 || q1 < q.q0 || q1 > p.T) q.n_q = 0;
   }
   const long long rows = (long long)q.n_q * p.G;
-  q.tiles = rows < p.min_rows || rows > p.max_rows ? 0 : (int)((rows + TR - 1) / TR);
+  const bool take = mine == kAllRows || (mine == kFewRows ? rows <= kRows : mine == kManyRows && rows > kRows);
+  q.tiles = take ? (int)((rows + TR - 1) / TR) : 0;
   q.units = p.sel ? p.max_sel : (q.kv + kPage - 1) / kPage;
   q.units = q.units < 1 ? 1 : (q.units + UNIT - 1) / UNIT;
   return q;
@@ -90,8 +100,33 @@ __device__ __forceinline__ long long block_scan(long long v, long long &total, l
   return before + x - v;
 }
 
+// The requests with more than 16 rows of a key head go to the kernel of tiles of
+// 128 rows where their work, in tiles of 16 rows by a page and 8 pages an item, is
+// more than this: the kernel of few rows does 500 a us after 13 us, the other 3 to
+// 8 times as many after 27 to 40 us.  (8 key heads of 128, 5 query heads each: 9088,
+// 256 rows over 4000 tokens, 38 against 53 us; 18176, 512 rows, 60 against 55 us.)
+constexpr long long kFewWork = 10000;
+
+// All THREADS threads take part; both kernels come to the same answer.
+template <int THREADS>
+__device__ __forceinline__ Rows rows_of_launch(const Params &p, long long *sm) {
+  if (p.side == kAllRequests) return kAllRows;
+  long long work = 0;
+  for (int base = 0; base < p.R; base += THREADS) {
+    const int r = base + (int)threadIdx.x;
+    long long v = 0, sum;
+    if (r < p.R) v = work_of<8>(p, request_of<kRows, 1>(p, r, kManyRows));
+    block_scan<THREADS / 32>(v, sum, sm);
+    work += sum;
+  }
+  const bool many = work > kFewWork;
+  if (p.side == kFewSide) return many ? kFewRows : kAllRows;
+  return many ? kManyRows : kNoRows;
+}
+
 // This block's range [w0, w1) of the line and the request in which it begins.
 struct Range {
+  Rows rows;
   long long total, n_blk, w0, w1, r_start;
   int r;
 };
@@ -105,6 +140,7 @@ template <int TR, int UNIT, int SETUP, int THREADS, bool WHOLE = false>
 __device__ __forceinline__ bool find_range(const Params &p, long long min_units, Range &g, long long *sm, int *sm_r) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x;
+  g.rows = rows_of_launch<THREADS>(p, sm);
   g.total = 0;
   long long items = 0;
   long long v = 0, at = 0;           // of request tid: its work and place; all there is up to THREADS requests
@@ -113,7 +149,7 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
     long long sum;
     Request q;
     q.tiles = q.units = 0;
-    if (r < p.R) q = request_of<TR, UNIT>(p, r);
+    if (r < p.R) q = request_of<TR, UNIT>(p, r, g.rows);
     v = work_of<SETUP>(p, q);
     at = block_scan<WARPS>(v, sum, sm);
     g.total += sum;
@@ -133,7 +169,7 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
     const int r = base + tid;
     long long sum = g.total;
     if (p.R > THREADS) {
-      v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r)) : 0;
+      v = r < p.R ? work_of<SETUP>(p, request_of<TR, UNIT>(p, r, g.rows)) : 0;
       at = before + block_scan<WARPS>(v, sum, sm);
     }
     if (v > 0 && at <= g.w0 && g.w0 < at + v) {
@@ -159,22 +195,24 @@ struct Segment {
 
 template <int TR, int UNIT, int SETUP>
 struct Walk {
+  Rows rows;
   long long pos, w1, r_start;
   int r;
   Request rq;
   __device__ __forceinline__ void start(const Params &p, const Range &g) {
+    rows = g.rows;
     pos = g.w0;
     w1 = g.w1;
     r_start = g.r_start;
     r = g.r;
-    rq = request_of<TR, UNIT>(p, r);
+    rq = request_of<TR, UNIT>(p, r, rows);
   }
   __device__ __forceinline__ bool next(const Params &p, Segment &s) {
     if (pos >= w1) return false;
     while (pos >= r_start + work_of<SETUP>(p, rq)) {
       r_start += work_of<SETUP>(p, rq);
       ++r;
-      rq = request_of<TR, UNIT>(p, r);
+      rq = request_of<TR, UNIT>(p, r, rows);
     }
     const int cost = rq.units + SETUP;
     const long long item = (pos - r_start) / cost;

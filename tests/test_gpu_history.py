@@ -277,6 +277,63 @@ def test_attend_matches_the_oracle(d, H, Hkv, kv, q_lens, causal):
         check_attend(c, host, table, kv, q_lens, Q, out, lse, causal, what=str(dtype))
 
 
+def with_ballast(rng, kv, Hkv, d, H, q_lens):
+    """filled(), and one more request of so much work (600 queries over 20000
+    tokens, all on one page) that the batch's many rows go to their own kernel."""
+    n, pages = 600, -(-20000 // PAGE)
+    c, host, table = filled(rng, list(kv) + [0], Hkv, d, H, sum(q_lens) + n, fill=0x11, width=pages)
+    c.block_table[-1] = c.n_pages - 1
+    c.kv_len[-1] = 20000
+    return c, host, table, list(q_lens) + [n]
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("H,Hkv,kv,q_lens,causal", [
+    (5, 1, [129, 0, 700], [1, 2, 0], True),
+    (8, 2, [300, 5], [4, 9], True),          # 9 new tokens on 5 places: rows that see nothing
+    (6, 2, [257], [37], True),
+    (3, 3, [130, 64], [20, 1], False),
+    (4, 2, [333, 90], [70, 90], True),
+    (2, 1, [700, 0, 65], [129, 20, 1], True),     # many rows, none of them and few in one batch
+    (3, 1, [1000], [300], False),
+])
+def test_attend_in_a_batch_of_much_work_matches_the_oracle(d, H, Hkv, kv, q_lens, causal):
+    rng = np.random.default_rng(d + H * 5 + sum(kv))
+    T = sum(q_lens)
+    c, host, table, all_q = with_ballast(rng, kv, Hkv, d, H, q_lens)
+    Q = HC.up(HC.bf16_round(1.5 * rng.standard_normal((T + all_q[-1], H, d))))
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full(Q.shape, 5.0, dtype=dtype, device="cuda")
+        lse = torch.full(Q.shape[:2], 5.0, device="cuda")
+        attend(c, all_q, Q, out, lse, max_q=max(all_q), causal=causal)
+        assert c.status.item() == 0
+        check_attend(c, host, table, kv, q_lens, Q[:T], out[:T], lse[:T], causal, what=str(dtype))
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_values_of_any_kind_in_a_batch_of_much_work(d):
+    """What test_values_that_are_not_finite_stay_in_their_rows and
+    test_scales_of_any_size do, in the kernel of many rows."""
+    rng = np.random.default_rng(d)
+    Hkv, H, n, q = 1, 2, 200, 30
+    c, host, table, all_q = with_ballast(rng, [n, n], Hkv, d, H, [q, q])
+    K, V = HC.keys_values(rng, n, Hkv, d)
+    V[190] = 3e38                    # the last tokens: seen by the later rows only
+    V[195, :, 3] = np.inf
+    c.kv_len[:2] = n
+    slots = ints([int(table[1, t // PAGE]) * PAGE + t % PAGE for t in range(n)], torch.int64)
+    c.write(HC.up(K), HC.up(V), slots)
+    Q = HC.up(HC.bf16_round(rng.standard_normal((2 * q + all_q[-1], H, d))))
+    out, lse = torch.zeros(Q.shape, device="cuda"), torch.zeros(Q.shape[:2], device="cuda")
+    attend(c, all_q, Q, out, lse, max_q=max(all_q), causal=True)
+    assert c.status.item() == 0
+    check_attend(c, host, table, [n, n], [q], Q[:q], out[:q], lse[:q], True)    # the request before: untouched
+    got = out[q:2 * q].cpu().numpy()
+    sees = np.arange(q) + n - (q - 1)                 # keys that row t sees
+    assert np.isfinite(got[sees <= 195]).all() and np.isnan(got[sees > 195]).all()
+    assert torch.isfinite(lse[q:2 * q]).all()
+
+
 def test_attend_takes_strided_rows_and_leaves_the_others():
     rng = np.random.default_rng(5)
     d, H, Hkv, kv, q_lens, T = 96, 4, 2, [150, 70], [3, 2], 9     # four rows behind the last token
