@@ -102,10 +102,12 @@ __device__ __forceinline__ long long block_scan(long long v, long long &total, l
 
 // The requests with more than 16 rows of a key head go to the kernel of tiles of
 // 128 rows where their work, in tiles of 16 rows by a page and 8 pages an item, is
-// more than this: the kernel of few rows does 500 a us after 13 us, the other 3 to
-// 8 times as many after 27 to 40 us.  (8 key heads of 128, 5 query heads each: 9088,
-// 256 rows over 4000 tokens, 38 against 53 us; 18176, 512 rows, 60 against 55 us.)
-constexpr long long kFewWork = 10000;
+// more than this: the kernel of few rows does 500 a us after 13 us, the other 2 to
+// 4 times as many after 30 to 45 us.  (Few against many rows' kernel, 25000 tokens,
+// 8 key heads of 128: 12768, 64 rows, 49 against 67 us, 51072, 256 rows, 134 against
+// 94 us.  24 key heads of 96, 4000 tokens: 13632, 128 rows, 43 against 45 us, 27264,
+// 256 rows, 69 against 53 us.)
+constexpr long long kFewWork = 14000;
 
 // All THREADS threads take part; both kernels come to the same answer.
 template <int THREADS>
@@ -134,7 +136,8 @@ struct Range {
 // All THREADS threads take part; sm: WARPS + 1 long longs and an int.  WHOLE: a
 // number of blocks that is a multiple of the items' is preferred where it costs
 // less than one block in 16: items of one length are then cut into equal parts
-// and no block begins two (500 queries over 5000 tokens, 10 and 2 heads: 57 us
+// and no block begins two, and an item of n units is cut into sqrt(2 n) parts at
+// most, since one block joins them all, 1.3 us a part (500 queries over 5000 tokens, 10 and 2 heads: 57 us
 // without it, 50 us with it.  Few rows: the same, less the time to count the items).
 template <int TR, int UNIT, int SETUP, int THREADS, bool WHOLE = false>
 __device__ __forceinline__ bool find_range(const Params &p, long long min_units, Range &g, long long *sm, int *sm_r) {
@@ -160,6 +163,10 @@ __device__ __forceinline__ bool find_range(const Params &p, long long min_units,
   }
   const long long most = (g.total + min_units - 1) / min_units;
   g.n_blk = most < (long long)gridDim.x ? most : (long long)gridDim.x;
+  if (WHOLE && items > 0) {
+    const long long parts = (long long)ceilf(sqrtf(2.f * ((float)g.total / (float)items)));
+    if (items * parts < g.n_blk) g.n_blk = items * parts;
+  }
   if (items > 0 && items < g.n_blk && (g.n_blk % items) * 16 <= g.n_blk) g.n_blk -= g.n_blk % items;
   if ((long long)blockIdx.x >= g.n_blk) return false;
   g.w0 = g.total * blockIdx.x / g.n_blk;
