@@ -66,6 +66,7 @@ struct Params {
   float *out_lse;                    // [B, H, Nq] or null
   int *dev_status;
   long long wait_limit_ns;
+  int split;                         // blocks of threads of a query block (a cluster)
 };
 
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
@@ -104,7 +105,36 @@ struct List {
   }
 };
 
-template <int D>
+// Clusters: where there are few query blocks, up to eight blocks of threads take
+// the parts of one list, each its own online softmax, and join them through one
+// another's shared memory.
+constexpr int kMaxSplit = 8;
+
+// Every thread of the cluster comes to both, whatever happened before.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
 block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -121,7 +151,8 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_BAR + 68);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, hk = h / p.G;
+  const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)blockIdx.x % split : 0;
+  const int i = (int)blockIdx.x / split, h = blockIdx.y, b = blockIdx.z, hk = h / p.G;
 
   List list;
   {
@@ -133,6 +164,13 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     list.keys = p.Nk;
     if (p.k_len) list.keys = max(0, min(p.Nk, __ldg(p.k_len + b)));
     if (threadIdx.x == 0 && n != list.n) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+  }
+  if constexpr (SPLIT) {
+    // this block's part: whole tiles
+    const int tiles = (list.n + 1) / 2;
+    const int t0 = (int)((long long)tiles * rank / split), t1 = (int)((long long)tiles * (rank + 1) / split);
+    list.sel += 2 * t0;
+    list.n = min(list.n, 2 * t1) - 2 * t0;
   }
   const int T = (list.n + 1) / 2;
 
@@ -262,6 +300,10 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       tc_fence_before();
       named_bar_arrive(1, kThreads);
     }
+    if constexpr (SPLIT) {
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -372,6 +414,79 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (lane == 0) mbar_arrive(p_full);
   }
   if (ok && T > 0) ok = wait_bounded(o_full, 0, ctl);
+  if constexpr (SPLIT) {
+    // every product is done (or this block gave up and adds nothing): Q, K and V
+    // make room for its O, m and l
+    constexpr int kRow = D + 4;                 // floats: rows of neighbouring lanes lie in other banks
+    static_assert(BM * kRow * 4 + BM * 8 <= 3 * C::TILE, "O, m and l in the place of Q, K and V");
+    float *stage = reinterpret_cast<float *>(smem + C::OFF_Q);
+    const bool any = ok && T > 0 && !(!(l > 0.f) && l == l);
+    __syncwarp();
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t ov[32];
+      if (T > 0) {
+        tmem_ld32(tO + c * 32, ov);
+        tc_wait_ld();
+      }
+      float4 *dst = reinterpret_cast<float4 *>(stage + r * kRow + c * 32);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        dst[q] = any ? make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                   __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    reinterpret_cast<float2 *>(stage + BM * kRow)[r] = any ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
+    tc_fence_before();
+    named_bar_arrive(1, kThreads);
+    cluster_sync();
+    // the rows are shared out; the parts are joined in the order of the list
+    const int mine = BM / split;
+    constexpr int kVec = D / 4;
+    const uint32_t from = smem_u32(stage);
+    for (int x = r; x < mine * kVec; x += BM) {
+      const int row = rank * mine + x / kVec, ch = (x % kVec) * 4;
+      float2 ml[kMaxSplit];
+      float4 o[kMaxSplit];
+#pragma unroll
+      for (int e = 0; e < kMaxSplit; ++e) {
+        ml[e] = make_float2(-INFINITY, 0.f);
+        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e < split) {
+          const uint32_t peer = cluster_map(from, e);
+          ml[e] = cluster_ld2(peer + BM * kRow * 4 + row * 8);
+          o[e] = cluster_ld4(peer + (row * kRow + ch) * 4);
+        }
+      }
+      float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int e = 0; e < kMaxSplit; ++e) mt = fmaxf(mt, ml[e].x);
+      const float less = mt > -INFINITY ? mt : 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < kMaxSplit; ++e) {
+        const float f = fast_ex2(ml[e].x - less);
+        lt = fmaf(ml[e].y, f, lt);
+        v = make_float4(fmaf(o[e].x, f, v.x), fmaf(o[e].y, f, v.y), fmaf(o[e].z, f, v.z), fmaf(o[e].w, f, v.w));
+      }
+      const int at = i * BM + row;
+      if (at >= p.Nq) continue;
+      const float inv = lt > 0.f ? 1.f / lt : (lt == lt ? 0.f : lt);
+      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      const long long to = b * p.osb + h * p.osh + at * p.osn + ch;
+      if (p.out_fp32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = v;
+      else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + to) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (ch == 0 && p.out_lse)
+        p.out_lse[((size_t)b * p.H + h) * p.Nq + at] =
+            lt > 0.f ? (mt + __log2f(lt)) * 0.69314718055994531f : (lt == lt ? -INFINITY : lt);
+    }
+    cluster_sync();               // the others may still read this block's rows
+    return;
+  }
   if (ok) {
     tc_fence_after();
     // every product is done: the Q tile is free to stage rows, 4 KB a warp
@@ -441,10 +556,10 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   named_bar_arrive(1, kThreads);
 }
 
-template <int D>
+template <int D, bool SPLIT>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int B,
                    cudaStream_t stream) {
-  auto kfn = block_attn_kernel<D>;
+  auto kfn = block_attn_kernel<D, SPLIT>;
   static std::mutex mu;
   static std::set<int> ready;
   int dev = 0;
@@ -463,9 +578,24 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
       ready.insert(dev);
     }
   }
-  const dim3 grid((unsigned)p.n_q, (unsigned)p.H, (unsigned)B);
-  kfn<<<grid, kThreads, Cfg<D>::SMEM, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.n_q * p.split), (unsigned)p.H, (unsigned)B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)p.split;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kfn, tq, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int B,
+                   cudaStream_t stream) {
+  return p.split > 1 ? launch<D, true>(tq, tk, tv, p, B, stream) : launch<D, false>(tq, tk, tv, p, B, stream);
 }
 
 }  // namespace battn
@@ -473,7 +603,8 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B, int H,
                               int Hkv, int Nq, int Nk, int d, const int *sel, const int *count, int room,
                               const int *k_len, float scale, void *out, int out_fp32, const long long *os,
-                              float *out_lse, int *dev_status, long long wait_limit_ns, cudaStream_t stream) {
+                              float *out_lse, int *dev_status, long long wait_limit_ns, int num_sms,
+                              cudaStream_t stream) {
   battn::Params p;
   p.H = H;
   p.G = H / Hkv;
@@ -495,6 +626,11 @@ cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, cons
   p.out_lse = out_lse;
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
+  // Few query blocks leave SMs (two blocks each) without work: their lists are cut,
+  // in parts of at least two tiles where the lists are as long as they may be.
+  const long long blocks = (long long)p.n_q * H * B;
+  p.split = 1;
+  while (p.split < battn::kMaxSplit && blocks * p.split * 2 <= 2LL * num_sms && p.split * 2 * 4 <= room) p.split *= 2;
   switch (d) {
     case 64: return battn::launch<64>(tq, tk, tv, p, B, stream);
     case 96: return battn::launch<96>(tq, tk, tv, p, B, stream);

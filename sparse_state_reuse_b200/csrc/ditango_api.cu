@@ -78,7 +78,7 @@ cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, cons
                               int H, int Hkv, int Nq, int Nk, int d, const int *sel, const int *count,
                               int room, const int *k_len, float scale, void *out, int out_fp32,
                               const long long *os, float *out_lse, int *dev_status,
-                              long long wait_limit_ns, cudaStream_t stream);
+                              long long wait_limit_ns, int num_sms, cudaStream_t stream);
 cudaError_t attn_check_status(int *out, bool reset);
 cudaError_t merge_check_status(int *out, bool reset);
 }  // namespace ditango
@@ -990,7 +990,8 @@ ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq,
     return DITANGO_ERR_CUDA;
   return cuda_status(launch_block_attn(tq, tk, tv, B, H, Hkv, Nq, Nk, d, sel, sel_count, max_sel, k_len,
                                        scale, out, out_is_fp32 ? 1 : 0, os, out_lse, dev_status,
-                                       g_wait_limit_ns.load(), static_cast<cudaStream_t>(stream)));
+                                       g_wait_limit_ns.load(), num_sms_current(),
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
