@@ -445,44 +445,60 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const int mine = BM / split;
     constexpr int kVec = D / 4;
     const uint32_t from = smem_u32(stage);
-    for (int x = r; x < mine * kVec; x += BM) {
-      const int row = rank * mine + x / kVec, ch = (x % kVec) * 4;
-      float2 ml[kMaxSplit];
-      float4 o[kMaxSplit];
+    constexpr int U = 4, EB = 4;                // groups of a thread and parts in flight together
+    for (int x0 = r; x0 < mine * kVec; x0 += BM * U) {
+      float mt[U], lt[U];
+      float4 v[U];
 #pragma unroll
-      for (int e = 0; e < kMaxSplit; ++e) {
-        ml[e] = make_float2(-INFINITY, 0.f);
-        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e < split) {
-          const uint32_t peer = cluster_map(from, e);
-          ml[e] = cluster_ld2(peer + BM * kRow * 4 + row * 8);
-          o[e] = cluster_ld4(peer + (row * kRow + ch) * 4);
-        }
+      for (int w = 0; w < U; ++w) {
+        mt[w] = -INFINITY;
+        lt[w] = 0.f;
+        v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float mt = -INFINITY, lt = 0.f;
+      for (int e0 = 0; e0 < split; e0 += EB) {
+        float2 ml[U][EB];
+        float4 o[U][EB];
 #pragma unroll
-      for (int e = 0; e < kMaxSplit; ++e) mt = fmaxf(mt, ml[e].x);
-      const float less = mt > -INFINITY ? mt : 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < U; ++w)
 #pragma unroll
-      for (int e = 0; e < kMaxSplit; ++e) {
-        const float f = fast_ex2(ml[e].x - less);
-        lt = fmaf(ml[e].y, f, lt);
-        v = make_float4(fmaf(o[e].x, f, v.x), fmaf(o[e].y, f, v.y), fmaf(o[e].z, f, v.z), fmaf(o[e].w, f, v.w));
+          for (int e = 0; e < EB; ++e) {
+            const int x = x0 + w * BM, row = rank * mine + x / kVec, ch = (x % kVec) * 4;
+            ml[w][e] = make_float2(-INFINITY, 0.f);
+            o[w][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < mine * kVec && e0 + e < split) {
+              const uint32_t peer = cluster_map(from, e0 + e);
+              ml[w][e] = cluster_ld2(peer + BM * kRow * 4 + row * 8);
+              o[w][e] = cluster_ld4(peer + (row * kRow + ch) * 4);
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < U; ++w)
+#pragma unroll
+          for (int e = 0; e < EB; ++e) {
+            const float mn = fmaxf(mt[w], ml[w][e].x), less = mn > -INFINITY ? mn : 0.f;
+            const float f0 = fast_ex2(mt[w] - less), f1 = fast_ex2(ml[w][e].x - less);
+            const float4 y = o[w][e];
+            lt[w] = lt[w] * f0 + ml[w][e].y * f1;
+            v[w] = make_float4(v[w].x * f0 + y.x * f1, v[w].y * f0 + y.y * f1, v[w].z * f0 + y.z * f1, v[w].w * f0 + y.w * f1);
+            mt[w] = mn;
+          }
       }
-      const int at = i * BM + row;
-      if (at >= p.Nq) continue;
-      const float inv = lt > 0.f ? 1.f / lt : (lt == lt ? 0.f : lt);
-      v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-      const long long to = b * p.osb + h * p.osh + at * p.osn + ch;
-      if (p.out_fp32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = v;
-      else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + to) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      if (ch == 0 && p.out_lse)
-        p.out_lse[((size_t)b * p.H + h) * p.Nq + at] =
-            lt > 0.f ? (mt + __log2f(lt)) * 0.69314718055994531f : (lt == lt ? -INFINITY : lt);
+#pragma unroll
+      for (int w = 0; w < U; ++w) {
+        const int x = x0 + w * BM, ch = (x % kVec) * 4, at = i * BM + rank * mine + x / kVec;
+        if (x >= mine * kVec || at >= p.Nq) continue;
+        const float inv = lt[w] > 0.f ? 1.f / lt[w] : (lt[w] == lt[w] ? 0.f : lt[w]);
+        const float4 z = make_float4(v[w].x * inv, v[w].y * inv, v[w].z * inv, v[w].w * inv);
+        const long long to = b * p.osb + h * p.osh + at * p.osn + ch;
+        if (p.out_fp32)
+          *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = z;
+        else
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + to) =
+              make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+        if (ch == 0 && p.out_lse)
+          p.out_lse[((size_t)b * p.H + h) * p.Nq + at] =
+              lt[w] > 0.f ? (mt[w] + __log2f(lt[w])) * 0.69314718055994531f : (lt[w] == lt[w] ? -INFINITY : lt[w]);
+      }
     }
     cluster_sync();               // the others may still read this block's rows
     return;
@@ -626,11 +642,15 @@ cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, cons
   p.out_lse = out_lse;
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
-  // Few query blocks leave SMs (two blocks each) without work: their lists are cut,
-  // in parts of at least two tiles where the lists are as long as they may be.
+  // Few query blocks leave SMs (two blocks each) without work: their lists are cut
+  // into parts of at least one tile, if they may have four (4 query blocks, d = 64
+  // and 128: 80 listed blocks 64 and 76 us whole, 16 and 20 us in eight parts; 16
+  // listed 16.4 and 20.5, 11 and 14; 8 listed 12.1 and 13.3, 10.3 and 12.3 in four
+  // parts; 4 listed 8.3 and 10.3, 10.3 and 12.8 in two).
   const long long blocks = (long long)p.n_q * H * B;
   p.split = 1;
-  while (p.split < battn::kMaxSplit && blocks * p.split * 2 <= 2LL * num_sms && p.split * 2 * 4 <= room) p.split *= 2;
+  while (room >= 8 && p.split < battn::kMaxSplit && blocks * p.split * 2 <= 2LL * num_sms && p.split * 4 <= room)
+    p.split *= 2;
   switch (d) {
     case 64: return battn::launch<64>(tq, tk, tv, p, B, stream);
     case 96: return battn::launch<96>(tq, tk, tv, p, B, stream);

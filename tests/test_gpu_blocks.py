@@ -178,6 +178,38 @@ def test_attention_over_listed_blocks_matches_the_oracle(d, B, H, Hkv, Nq, Nk, m
     assert (wide[:, 0] == 5).all() and (wide[:, -1] == 5).all() and (wide[..., d:] == 5).all()
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("B,H,Hkv,Nq,Nk,most,k_len,how,dtype", [
+    (1, 100, 50, 60, 900, 14, None, "packed", torch.bfloat16),            # two parts
+    (1, 60, 30, 60, 700, 10, None, "packed", torch.float32),              # four
+    (2, 2, 1, 200, 3000, 40, [3000, 70], "view", torch.bfloat16),         # eight, most of them empty in one entry
+    (1, 1, 1, 129, 1500, 23, None, "packed", torch.float32),
+])
+def test_lists_cut_into_parts(d, B, H, Hkv, Nq, Nk, most, k_len, how, dtype):
+    """Few query blocks: their lists are shared out over blocks of threads; lists of
+    any length, some without a tile for every part."""
+    test_attention_over_listed_blocks_matches_the_oracle(d, B, H, Hkv, Nq, Nk, most, k_len, how, dtype)
+
+
+def test_parts_of_a_list_give_the_same_bits_and_replay():
+    op = dt.BlockSparseAttention(1, 2, 200, 5000, 64, 40)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    Q, K, V = (torch.randn((1, 2, n, 64), generator=g, device="cuda").bfloat16() for n in (200, 5000, 5000))
+    out, lse = torch.empty((1, 2, 200, 64), device="cuda"), torch.empty((1, 2, 200), device="cuda")
+    op.step(Q, K, V, out, lse)
+    torch.cuda.synchronize()
+    ref = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.step(Q, K, V, out, lse)
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    assert op.status.item() == 0
+
+
 def test_entries_and_counts_out_of_range_are_empty_and_recorded():
     rng = np.random.default_rng(2)
     d, Nq, Nk = 128, 200, 320
