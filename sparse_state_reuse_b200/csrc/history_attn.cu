@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       // columns 2t and 2t + 1 belong to lanes 8t and 8t + 4
-      const float mul = p.scale_log2 * __uint_as_float(ex << 23);
+      const float mul = score_factor(p.scale_log2 * __uint_as_float(ex << 23));
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int y = 2 * x + e;

@@ -323,6 +323,12 @@ struct Unpack {
   }
 };
 
+// The factor of a row's scores.  A row of zeros (or a tiny scale) takes it below
+// the least fp32 number, and 0 times the -inf of a masked score would be NaN: it
+// stays positive.  What it multiplies is then below 2^136, so that a score that
+// should be 0 comes out below 2^-12.
+__device__ __forceinline__ float score_factor(float x) { return fmaxf(x, __uint_as_float(1u)); }
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

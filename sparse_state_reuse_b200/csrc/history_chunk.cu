@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c) tmem_ld16p(tS + c * 16, &sv[c * 16]);
       tc_wait_ld();
-      const float v_now = tile.vref, mulk = mul * tile.kref;
+      const float v_now = tile.vref, mulk = hattn::score_factor(mul * tile.kref);
       // rows of a warp may see different keys: the branch is the warp's, so that it
       // stays together for the tensor memory instructions
       if (__any_sync(0xffffffffu, n0 + n1 < BN)) {
