@@ -73,6 +73,19 @@ constexpr int kMaxBlocks = 160;      // most blocks of a launch (the workspace h
 constexpr int kMinUnits = 4;
 constexpr int kSetup = 2;            // tiles that beginning and finishing an item counts for
 
+// P in fp16: a row exponentiates against its maximum less 7, so that p is 2^7
+// where it was 1, and 2^15 where a maximum grew by the 2^8 that it may before
+// the row is rescaled (fp16 ends at 65504).  Smaller ones are then kept to 2^-32
+// of the largest, half a step of fp16's least numbers: 300000 keys of 2^-27 each
+// beside one of 1 are a thousandth of the sum, and were lost whole with p at 1.
+// Sums, maximum and lse go by the same shift.  Past kHuge neither the shift nor the
+// growth is small against the rounding of the maximum, and both are left out.
+constexpr float kSpareLog2 = 7.0f;
+__device__ __forceinline__ float reference_of(float mx) { return fabsf(mx) > kHuge ? mx : mx - kSpareLog2; }
+__device__ __forceinline__ bool outgrown(float mx, float m) {
+  return mx > (fabsf(m) > kHuge ? m : m + (kSpareLog2 + kRescaleLog2));
+}
+
 // What is known of a tile before its codes are unpacked.
 constexpr int kRing = 4;
 struct Tile {
@@ -610,13 +623,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       const float mx2 =
           max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * mulk;
       if (u == 0) {
-        m_used = mx2;
+        m_used = reference_of(mx2);
       } else {
         // S of this tile is complete, and with it every product issued before:
         // O may be rescaled, when a maximum grew by more than 2^8 or V's reference did
-        const bool need = mx2 > m_used + kRescaleLog2;
+        const bool need = outgrown(mx2, m_used);
         if (__any_sync(0xffffffffu, need || v_now != vref)) {
-          const float m_new = need ? mx2 : m_used;
+          const float m_new = need ? reference_of(mx2) : m_used;
           const float alpha = need ? fast_ex2(m_used - m_new) : 1.f;
           l *= alpha;
           m_used = m_new;

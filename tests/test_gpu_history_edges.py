@@ -149,3 +149,87 @@ def test_zero_rows_and_lists_shorter_than_their_room(many):
     o, lse = b.attend(Q, False)
     assert b.c.status.item() == 5
     b.check(Q, o, lse, False, lists=[[list(range(11))], [[0, 1, 2, 3, 8, 9, 10]]])
+
+
+# ---------------------------------------------------------------- probabilities far apart
+def one_page_many_times(d, Hkv, pages, first, rest):
+    """A cache of two pages, `first` and `rest` ((K, V) of 64 tokens each, for every
+    head alike), and a request whose table holds the first and then `pages` times
+    the other."""
+    host = HC.HostPages(2, 1, d)
+    for p, (K, V) in enumerate((first, rest)):
+        for t in range(PAGE):
+            host.put(p, t, 0, 0, K[t])
+            host.put(p, t, 0, 1, V[t])
+    data = torch.from_numpy(host.data.repeat(Hkv, 1)).cuda()
+    c = dt.KV4Cache(2, Hkv, d, 1, pages + 1, 256, data=data)
+    c.block_table.fill_(1)
+    c.block_table[0, 0] = 0
+    c.kv_len.fill_((pages + 1) * PAGE)
+    return c, host
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("q", [1, 64])
+def test_a_long_tail_far_below_one_key_keeps_its_mass(d, q):
+    """One key with a value of zero, and 300000 keys 2^-27 below it: the output is
+    the tail's mass.  As many heads as blocks of threads, so that each has all keys
+    of its own.  A probability is rounded by half a step of fp16's least numbers
+    at most, 2^-25, of which the largest is 2^7 in the kernel of many rows and at
+    least 2^5 (times the scale of V) in the other: 2^-30 of it."""
+    rng = np.random.default_rng(d)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pages, Hkv = 4700, sms * (4 if q == 1 else 1)
+    K, V = np.zeros((2, PAGE, d), np.float32), HC.bf16_round(1 + rng.random((2, PAGE, d)))
+    K[:, :, 0] = HC.bf16_round(rng.uniform(-0.5, 0.5, (2, PAGE)))
+    Q = np.zeros((q, d), np.float32)
+    Q[:, 0] = HC.bf16_round(8 + rng.random(q))
+    K[0, 0, 0] = HC.bf16_round([27 * np.log(2) / (8.5 * d ** -0.5)])[0]
+    V[0, 0] = 0
+    c, host = one_page_many_times(d, Hkv, pages, (K[0], V[0]), (K[1], V[1]))
+    c.q_off.copy_(ints([0, q]))
+    out, lse = torch.zeros((q, Hkv, d), device="cuda"), torch.zeros((q, Hkv), device="cuda")
+    c.attend(HC.up(Q)[:, None].repeat(1, Hkv, 1), out, lse, max_q=q)
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    (k0, v0, y0, x0), (k1, v1, y1, x1) = host.get(0, 0), host.get(1, 0)
+    qs = Q.astype(np.float64)
+    s0, s1 = qs @ k0.T * d ** -0.5, qs @ k1.T * d ** -0.5
+    m = s0.max(1, keepdims=True)
+    p0, p1 = np.exp(s0 - m), np.exp(s1 - m) * pages
+    l = (p0.sum(1) + p1.sum(1))[:, None]
+    o = (p0 @ v0 + p1 @ v1) / l
+    mass = (p0 @ np.abs(v0) + p1 @ np.abs(v1)) / l
+    dS = max(HC.logit_bound(qs, y, d ** -0.5, d) for y in (y0, y1))
+    step = 2.0 ** -30 * PAGE * (pages + 1) * max(x0.max(), x1.max())
+    tol = step + (HC.EPS + 2 * dS + 2.0 ** -19) * mass
+    assert (mass > 2 * step).all()
+    e = (m + np.log(l))[:, 0]
+    for h in range(0, Hkv, 7):
+        err = np.abs(out[:, h].cpu().numpy() - o)
+        assert (err <= tol).all(), (h, float((err / tol).max()))
+        assert (np.abs(lse[:, h].cpu().numpy() - e) <= dS + 2.0 ** -19 * (1 + np.abs(e))).all()
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_logits_of_any_size(many):
+    """Logits up to 2^30, where fp32 knows them to many units only: the largest key
+    takes all, and nothing overflows."""
+    rng = np.random.default_rng(3)
+    d, H, q, n = 64, 1, 40, 500
+    K, V = np.zeros((n, 1, d), np.float32), normal(rng, n, 1, d)
+    K[:, 0, 0] = HC.bf16_round(np.exp2(rng.uniform(0, 29, n)) * rng.choice([-1, 1], n))
+    K[:, 0, 1:] = K[:, :, :1].reshape(n, 1)             # rows of one value: held exactly
+    b = Batch(rng, [(K, V)], H, [q], many, d)
+    Q = np.zeros((q, H, d), np.float32)
+    Q[..., 0] = 2.0
+    o, lse = b.attend(Q, True, scale=1.0)
+    assert np.isfinite(o).all() and np.isfinite(lse).all() and b.c.status.item() == 0
+    for t in range(q):
+        seen = n - (q - 1 - t)
+        s = 2.0 * K[:seen, 0, 0].astype(np.float64)
+        best = np.flatnonzero(s >= s.max() * (1 - 2.0 ** -20))
+        if len(best) == 1 and np.partition(s, -2)[-2] < s.max() * 0.99:
+            v = b.rows_of(0, 0)[1][best[0]]
+            assert (np.abs(o[t, 0] - v) <= HC.EPS * (np.abs(v) + np.abs(v).max())).all()
+            assert abs(lse[t, 0] - s.max()) <= 2.0 ** -19 * s.max()
