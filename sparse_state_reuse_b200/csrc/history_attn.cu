@@ -9,8 +9,12 @@
 // exactly; scales and h are applied to scores and probabilities in fp32.  fp16 and not
 // bf16: its longer significand takes two codes in place, and it rounds p s' to
 // 2^-11.  Q is scaled by a power of two a row to lie below 2 (an exact step for
-// all but values 2^-24 of the row's largest), p s' by one that follows the
-// largest V scale met so far.
+// all but values 2^-24 of the row's largest), p s' by one of the row's own: 2^6
+// over the largest V scale met so far, as long as the scales that the warp meets
+// are of one size.  Where they are not (a page's largest is above what the row
+// is held to, or 2^6 below it), the row is held to the weights that it has
+// itself, so that neither a key that it does not see nor one whose probability is
+// nothing pushes the others out of fp16.
 //
 // Keys and channels are the rows of the products (m16n8k16, S^T = K Q^T and
 // O^T = V^T P^T) and query rows their 8 columns: 8 rows at a time, of which a
@@ -49,6 +53,7 @@ constexpr int kSetup = 8;            // pages that beginning and finishing an it
 // p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
 // 2^6 more uses the range that is left.
 constexpr float kWeightScale = 64.f;
+constexpr float kFirstScale = 0x1p69f;   // before the first weight: 2^6 over 2^-63
 
 // Key of row n of an 8-key tile.  The order within a tile is free (scores and
 // values use the same); this one spreads the rows that a warp reads at once
@@ -69,6 +74,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+
+// The least power of two above x >= 0, from 2^-63 to 2^127.
+__device__ __forceinline__ float power_above(float x) {
+  return __uint_as_float(min(max((__float_as_uint(x) >> 23) + 1u, 64u), 254u) << 23);
 }
 
 template <int D>
@@ -96,7 +106,7 @@ struct WarpTile {
   float qsum[2 * NR], mul[2 * NR];   // sum of the scaled q; log2(e) scale 2^exponent
   float m[2 * NR], l[2 * NR], z[2 * NR];   // running maximum (log2), lane's sums of p and of p h'
   int vis[2 * NR];                   // keys that the row sees
-  float vref;                        // power of two that no V scale so far exceeds
+  float vs[2 * NR];                  // power of two by which the row's weights p s' are multiplied
 };
 
 // Scores of the 64 keys of a page (at st) for the lane's columns, before
@@ -162,7 +172,7 @@ __device__ __forceinline__ void page_scores(const WarpTile<D, NR> &w, const Unpa
 
 // The softmax step and the second product of a page (at st).
 template <int D, int NR, int E, bool MASKED>
-__device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base, int kv,
+__device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &unpack8, const uint8_t *st, int k_base, int kv, int vis_all,
                                             float (&sc)[4][NR][4]) {
   using T = WarpTile<D, NR>;
   const int lane = threadIdx.x & 31, t = lane & 3, n8 = lane >> 2;
@@ -185,26 +195,55 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
       need = need || mx[y] > w.m[y] + kRescaleLog2;
     }
   // the largest V scale of the page (rows that stand for NaN have none)
-  uint32_t top;
-  {
-    const uint32_t *vm = reinterpret_cast<const uint32_t *>(st + Smem<D>::kVMeta);
-    uint32_t a = vm[lane] & 0xffffu, b = vm[lane + 32] & 0xffffu;
-    if constexpr (MASKED) {
-      if (k_base + lane >= kv) a = 0u;
-      if (k_base + lane + 32 >= kv) b = 0u;
+  const uint32_t *vm = reinterpret_cast<const uint32_t *>(st + Smem<D>::kVMeta);
+  uint32_t sa16 = vm[lane] & 0xffffu, sb16 = vm[lane + 32] & 0xffffu;
+  if constexpr (MASKED) {
+    if (k_base + lane >= kv) sa16 = 0u;
+    if (k_base + lane + 32 >= kv) sb16 = 0u;
+  }
+  if (sa16 >= 0x7f80u) sa16 = 0u;
+  if (sb16 >= 0x7f80u) sb16 = 0u;
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max(sa16, sb16));
+  const float top_s = __uint_as_float(top << 16);
+  bool misfit = false, refit = false;
+#pragma unroll
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float fit = top_s * w.vs[2 * x + e];
+      misfit = misfit || fit > kWeightScale || (fit < 1.f && top != 0u);
     }
-    if (a >= 0x7f80u) a = 0u;
-    if (b >= 0x7f80u) b = 0u;
-    top = __reduce_max_sync(0xffffffffu, max(a, b));
-  }
-  float vmul = 1.f;
-  if (__uint_as_float(top << 16) > w.vref) {
-    const float v = __uint_as_float(min(max(((top >> 7) + 1u), 64u), 254u) << 23);
-    vmul = w.vref / v;
-    w.vref = v;
-    need = true;
-  }
-  if (__any_sync(0xffffffffu, need)) {
+  if (__any_sync(0xffffffffu, need || misfit)) {
+    float vmul[2 * NR];
+#pragma unroll
+    for (int y = 0; y < 2 * NR; ++y) vmul[y] = 1.f;
+    if (__any_sync(0xffffffffu, misfit)) {
+      // scales within 2^6 of one another, and of those before, that every row sees:
+      // the largest holds for all rows
+      const float vnew = kWeightScale / power_above(top_s);
+      const uint32_t low = __reduce_min_sync(0xffffffffu, min(sa16 ? sa16 : 0xffffu, sb16 ? sb16 : 0xffffu));
+      bool alike = top <= low + (6u << 7) && (!MASKED || vis_all >= kv);
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float vs = w.vs[2 * x + e], fit = top_s * vs;
+          alike = alike && fit >= 1.f && (fit <= 64.f * kWeightScale || vs == kFirstScale);
+        }
+      refit = __any_sync(0xffffffffu, !alike);
+      if (!refit) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int y = 2 * x + e;
+            if (top_s * w.vs[y] > kWeightScale) {
+              vmul[y] = vnew / w.vs[y];
+              w.vs[y] = vnew;
+            }
+          }
+      }
+    }
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -215,7 +254,7 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
         w.m[y] = mn;
         w.l[y] *= al;
         w.z[y] *= al;
-        const float ao = al * vmul;
+        const float ao = al * vmul[y];
 #pragma unroll
         for (int j = 0; j < T::MT; ++j) {
           w.o[x][j][e] *= ao;
@@ -248,7 +287,50 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
         mul[y] = 1.f;
       }
   }
-  const float vs = kWeightScale / w.vref;
+  if (refit) {
+    // each row by itself: the largest weight p s' that it has in this page.  2^-8
+    // keeps that product finite.
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int y = 2 * x + e;
+        float most = 0.f, big = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int key = 16 * u + kn + 8 * half;
+            const float sv = bf_lo(vm[key]) * 0x1p-8f;
+            const float ex = fast_ex2(fmaf(sc[u][x][2 * half + e], mul[y], neg[y]));
+            if ((!MASKED || k_base + key < w.vis[y]) && sv < INFINITY) most = fmaxf(most, ex * sv);
+          }
+#pragma unroll
+        for (int j = 0; j < T::MT; ++j) big = fmaxf(big, fmaxf(fabsf(w.o[x][j][e]), fabsf(w.o[x][j][2 + e])));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        }
+        if (most > 0.f) {
+          // that weight becomes 1/2 to 2^13, where the page's largest scale asks for
+          // neither more nor less; what there is of O stays finite
+          const float unit = 0x1p-8f / power_above(most), old = w.vs[y];
+          float vs = top_s > 0.f ? kWeightScale / power_above(top_s) : unit, ao = 1.f;
+          vs = fminf(fminf(fmaxf(vs, unit), unit * 0x1p13f), kFirstScale);
+          if (big > 0.f) {
+            vs = fminf(vs, old * fminf(0x1p100f / power_above(big), 0x1p90f));
+            ao = vs / old;
+          }
+          w.vs[y] = vs;
+#pragma unroll
+          for (int j = 0; j < T::MT; ++j) {
+            w.o[x][j][e] *= ao;
+            w.o[x][j][2 + e] *= ao;
+          }
+        }
+      }
+  }
   // 16 keys at a time: p, the weights p s', and the product
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -256,7 +338,6 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
     const uint32_t ma = *reinterpret_cast<const uint32_t *>(meta), mb = *reinterpret_cast<const uint32_t *>(meta + 32);
     const float sa = bf_lo(ma), sb = bf_lo(mb);
     const float ha = fmaf(8.f, sa, bf_hi(ma)), hb = fmaf(8.f, sb, bf_hi(mb));
-    const float wa = sa * vs, wb = sb * vs;
     uint32_t pb[NR][2];
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
@@ -267,7 +348,7 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
         for (int e = 0; e < E; ++e) {
           const int y = 2 * x + e, q = 2 * half + e;
           const float ex = fast_ex2(fmaf(sc[u][x][q], mul[y], neg[y]));
-          g[q] = ex * (half ? wb : wa);
+          g[q] = ex * ((half ? sb : sa) * w.vs[y]);
           w.l[y] += ex;
           if constexpr (MASKED) {       // a masked token's scale may be anything
             if (k_base + 16 * u + kn + 8 * half >= w.vis[y]) g[q] = 0.f;
@@ -436,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
 #pragma unroll
         for (int e = 0; e < 4; ++e) w.o[x][j][e] = 0.f;
     }
-    w.vref = __uint_as_float(64u << 23);
+#pragma unroll
+    for (int y = 0; y < 2 * NR; ++y) w.vs[y] = kFirstScale;
     // keys that every row of the tile sees
     const int vis_all = p.causal ? rq.kv - (rq.n_q - 1 - row0 / p.G) : rq.kv;
 
@@ -450,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
       if (!(ok = wait_warp(full(it), (it >> 1) & 1, ctl))) break;
       if (k_base + kPage > vis_all) {
         page_scores<D, NR, E, true>(w, unpack8, st, k_base, sc);
-        page_values<D, NR, E, true>(w, unpack8, st, k_base, rq.kv, sc);
+        page_values<D, NR, E, true>(w, unpack8, st, k_base, rq.kv, vis_all, sc);
       } else {
         page_scores<D, NR, E, false>(w, unpack8, st, k_base, sc);
-        page_values<D, NR, E, false>(w, unpack8, st, k_base, rq.kv, sc);
+        page_values<D, NR, E, false>(w, unpack8, st, k_base, rq.kv, vis_all, sc);
       }
       __syncwarp();                 // every lane has read the page
       if (npage >= 0) issue(sent++, npage);
@@ -471,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
     __syncthreads();
     if (s_abort) return;            // uniform after the barrier: a wait gave up
     float *mg = reinterpret_cast<float *>(place);
-    const float vout = w.vref / kWeightScale;
 #pragma unroll
     for (int ye = 0; ye < NR * E; ++ye) {
       const int x = ye / E, e = ye % E, y = 2 * x + e;
@@ -481,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
         w.z[y] += __shfl_xor_sync(0xffffffffu, w.z[y], o);
       }
       float *row = mg + (E == 2 ? 8 * x + 2 * t + e : 4 * x + t) * S::kMergeStride;
-      const float z = w.z[y];
+      const float z = w.z[y], vout = 1.f / w.vs[y];
       auto val = [&](int j, int up) { return fmaf(w.o[x][j][2 * up + e], vout, z); };
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)

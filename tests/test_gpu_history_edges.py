@@ -233,3 +233,54 @@ def test_logits_of_any_size(many):
             v = b.rows_of(0, 0)[1][best[0]]
             assert (np.abs(o[t, 0] - v) <= HC.EPS * (np.abs(v) + np.abs(v).max())).all()
             assert abs(lse[t, 0] - s.max()) <= 2.0 ** -19 * s.max()
+
+
+# ---------------------------------------------------------------- values far apart
+def outliers(rng, n, Hkv, d, key, unseen=True):
+    """n tokens; before the last 20, two that every row sees and whose logits
+    (with rows of Q that are `key` and noise) are hundreds below the others: values
+    2^40 and 2^90 times the usual; with `unseen`, among the last, that only the later
+    rows of a causal chunk see: the largest values there are, and 2^-40 of the usual."""
+    K, V = HC.keys_values(rng, n, Hkv, d)
+    K = HC.bf16_round(K * 0.25 + key)
+    far = HC.bf16_round(-40.0 * key)
+    for at, size in ((n // 3, 2.0 ** 40), (n - 40, 2.0 ** 90)):
+        K[at] = far
+        V[at] = HC.bf16_round(V[at] * size)
+    if not unseen:
+        return K, V
+    V[n - 17] = HC.bf16_round(V[n - 17] * 2.0 ** -40)
+    V[n - 10] = 3e38 * np.sign(V[n - 10])
+    V[n - 4] = HC.bf16_round(V[n - 4] * 2.0 ** 30)
+    return K, V
+
+
+def check_outliers(b, Q, o, lse, wide):
+    """As Batch.check: P s' (or P, and V with it: `wide`, both bf16) rounded once."""
+    scale, G, at = b.d ** -0.5, b.H // b.Hkv, 0
+    for r, n in enumerate(b.q_lens):
+        for h in range(b.Hkv):
+            k, v, y, x, pos = b.rows_of(r, h)
+            for t in range(n):
+                seen = pos < b.kv[r] - (n - 1 - t)
+                g = slice(h * G, (h + 1) * G)
+                qr = Q[at + t, g].astype(np.float64)
+                oo, e, P = OH.attend_rows(qr, k[seen], v[seen], scale)
+                dS = HC.logit_bound(qr, y[seen], scale, b.d)
+                HC.check(o[at + t, g], lse[at + t, g], oo, e, P, (np.abs(v) * (1 + HC.EPS) if wide else x)[seen],
+                         v[seen], dS, False, (r, h, t))
+        at += n
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("q", [1, 6, 30])
+def test_outlying_and_unseen_values_few_rows(d, q):
+    rng = np.random.default_rng(d + q)
+    Hkv, H = 2, 2
+    key = HC.bf16_round(4.0 * rng.choice([-1, 1], d))
+    kvs = [outliers(rng, n, Hkv, d, key, q > 6) for n in (70, 200, 900)]
+    b = Batch(rng, kvs, H, [q] * 3, False, d)
+    Q = HC.bf16_round(key * 0.25 + normal(rng, 3 * q, H, d))
+    o, lse = b.attend(Q, True)
+    assert b.c.status.item() == 0
+    check_outliers(b, Q, o, lse, False)
