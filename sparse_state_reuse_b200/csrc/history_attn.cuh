@@ -326,8 +326,10 @@ struct Unpack {
 // The factor of a row's scores.  A row of zeros (or a tiny scale) takes it below
 // the least fp32 number, and 0 times the -inf of a masked score would be NaN: it
 // stays positive.  What it multiplies is then below 2^136, so that a score that
-// should be 0 comes out below 2^-12.
-__device__ __forceinline__ float score_factor(float x) { return fmaxf(x, __uint_as_float(1u)); }
+// should be 0 comes out below 2^-12.  A factor past fp32 stays finite likewise.
+__device__ __forceinline__ float score_factor(float x) {
+  return fminf(fmaxf(x, __uint_as_float(1u)), __uint_as_float(0x7f7fffffu));
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;

@@ -5,7 +5,8 @@
 // keys), but with the scales inside the products, so that the softmax has
 // nothing to do for them:
 //   K  s (c - 8) over a power of two of the tile: a significand of 8 bits times
-//      a number of -8 ... 7 has 11 bits, so it is exact in fp16.  What is left,
+//      a number of -8 ... 7 has 11 bits, so it is exact in fp16 (but for what lies
+//      2^-25 below the tile's largest key).  What is left,
 //      h sum(q), is one more step of the product: h and sum(q) are split into
 //      three fp16 parts each, and six of the 16 columns of that step hold the
 //      pairs that matter (the rest is below 2^-32 of it).
@@ -87,14 +88,36 @@ __device__ __forceinline__ bool outgrown(float mx, float m) {
 }
 
 // What is known of a tile before its codes are unpacked.
+//
+// A causal item's last tiles hold keys that not all of its rows see, and those may
+// be of any size beside the others.  Where the sizes of such a tile's keys differ by
+// more than 2^4, K is held key by key: each over a power of two of its own, which
+// the softmax puts back into the scores.  (Keys that a row sees need no such care:
+// what the largest takes from the others is below the rounding of its own score.)
 constexpr int kRing = 4;
-struct Tile {
+constexpr uint32_t kEven = 4;
+constexpr uint32_t kOwnK = 1;
+struct alignas(16) Tile {
   uint2 v[BN];                  // V's s and h over vref, as fp16 pairs
   uint32_t ks[BN];              // K's s over kref, as an fp16 pair
   float kh[BN];                 // K's h over kref
+  float kf[BN];                 // kOwnK: the keys' own powers of two, over kref
   float kref, vref;             // the powers of two over which K and V are held
+  uint32_t flags;               // kOwnK
   int pos[2];                   // first token of each page, past every length where there is none
   uint32_t bad[4];              // keys whose V is not finite (written as 0: the softmax marks who sees it)
+};
+
+// Tiles of a segment with keys that some rows of a causal item see and others do
+// not: [first, last).  (Lists hold blocks in any order.)
+struct Edge {
+  int first, last;
+  __device__ __forceinline__ Edge(const Params &p, const hattn::Segment &sg) {
+    const int row0 = sg.tile * TR, row1 = (int)min((long long)row0 + TR, (long long)sg.rq.n_q * p.G) - 1;
+    const int seen = sg.rq.kv - (sg.rq.n_q - 1);       // of the request's first token, which sees this many
+    first = p.sel ? 0 : max(0, seen + row0 / p.G) / BN - sg.u0;
+    last = p.sel ? 0x7fffffff : (max(0, seen + row1 / p.G) + BN - 1) / BN - sg.u0;
+  }
 };
 
 template <int D>
@@ -107,6 +130,7 @@ struct Cfg {
   // 16 bytes are 128 bytes together, the two column halves next to each other)
   static constexpr int AUG = 128 * 32, OFF_QA = 6 * TILE, OFF_KA = OFF_QA + 2 * AUG;
   static constexpr int OFF_TILE = OFF_KA + 2 * AUG;
+  static_assert(OFF_TILE % 16 == 0, "records are aligned");
   static constexpr int OFF_BAR = OFF_TILE + kRing * (int)sizeof(Tile);
   static constexpr int USED = OFF_BAR + 240;
   // more than half of the SM's, since a block allocates all TMEM columns
@@ -149,6 +173,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 32 lanes x 8 consecutive columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // 16-byte piece of row r of the additional step's operands, columns 0 to 7
 // (columns 8 to 15 are 8 pieces on).
 __device__ __forceinline__ int aug_at(int r) { return (r >> 3) * 16 + (r & 7); }
@@ -176,7 +207,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-template <int D>
+template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -275,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         const hattn::Pages pages(p, sg);
         const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
         uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
+        const Edge edge(p, sg);
         // page numbers are read two tiles ahead, scales one
-        int page[2], ppos[2], pos[2];
+        int page[2], ppos[2], pos[2], at[2];   // the next tile's pages and places, this one's
         uint32_t mk[4], mv[4];
         auto look = [&](int j) {
 #pragma unroll
@@ -300,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           }
           pos[0] = ppos[0];
           pos[1] = ppos[1];
+          at[0] = max(page[0], 0);             // (no page: pos is past every length)
+          at[1] = max(page[1], 0);
         };
         look(0);
         fetch();
@@ -333,8 +367,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           if (lane == 0) {
             tile.kref = __uint_as_float(kref_bits);
             tile.vref = __uint_as_float(vref_bits);
+            if (CAUSAL) tile.flags = 0u;
             tile.pos[0] = pos[0];
             tile.pos[1] = pos[1];
+          }
+          if (CAUSAL && j >= edge.first && j < edge.last) {
+            // K once more, key by key, if the sizes are far apart (the scales are read
+            // again: this is rare, and the code around it stays as fast as it is)
+            auto meta = [&](int k) {
+              const uint8_t *src = p.data + ((size_t)(k < 2 ? at[0] : at[1]) * p.Hkv + head) * page_bytes(D) + kPage * D;
+              const int key = (k & 1) * 32 + lane, from = k < 2 ? pos[0] : pos[1];
+              return key < pages.kv - from ? __ldg(reinterpret_cast<const uint32_t *>(src) + key) : 0u;
+            };
+            uint32_t low = ~0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float kb = bound(mk[k]);
+              if (kb > 0.f && kb < INFINITY) low = min(low, __float_as_uint(kb));
+            }
+            low = __reduce_min_sync(0xffffffffu, low);
+            if ((kref_bits >> 23) > (low >> 23) + 1u + kEven) {
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t m = meta(k);
+                const float kb = bound(m), s = bf_lo(m);
+                const uint32_t own = kb < INFINITY ? reference(__float_as_uint(kb)) : 127u << 23;
+                const float down = __uint_as_float((254u << 23) - own);
+                const int key = k * 32 + lane;
+                tile.ks[key] = hattn::pack_f16x2(s * down, s * down);
+                tile.kh[key] = fmaf(8.f, s, bf_hi(m)) * down;
+                tile.kf[key] = __uint_as_float(own - (20u << 23));
+              }
+              if (lane == 0) {
+                // a power of two in the middle, so that no score with its key's own
+                // factor leaves fp32
+                tile.kref = 0x1p20f;
+                tile.flags = kOwnK;
+              }
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(tile_full(n));
@@ -552,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     {
       const bool live = r < rows;
       const int tok = live ? (row0 + r) / p.G : 0, head = live ? (row0 + r) % p.G : 0;
-      if (p.causal && live) vis -= sg.rq.n_q - 1 - tok;
+      if (CAUSAL && live) vis -= sg.rq.n_q - 1 - tok;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + (sg.rq.q0 + tok) * p.qt + (sg.h * p.G + head) * p.qh);
       uint4 u[D / 8];
       float big = 0.f;
@@ -592,6 +662,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       const int n0 = max(0, min(kPage, vis - tile.pos[0])), n1 = max(0, min(kPage, vis - tile.pos[1]));
       __syncwarp();
       tc_fence_after();
+      if constexpr (CAUSAL) {
+        if (__any_sync(0xffffffffu, (tile.flags & kOwnK) != 0u)) {
+          // the keys' own factors, in place, before the scores take the registers
+          // (this test alone costs the loop 3%: calls that are not causal have none)
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 8) {
+            uint32_t v[8];
+            tmem_ld8(tS + c, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * tile.kf[c + e]);
+            tmem_st8(tS + c, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+          }
+          tc_wait_st();
+        }
+      }
       uint32_t sv[BN];
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c) tmem_ld16p(tS + c * 16, &sv[c * 16]);
@@ -852,9 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
   named_bar_arrive(1, kThreads);
 }
 
-template <int D>
+template <int D, bool CAUSAL>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
-  auto kfn = kv4_chunk_kernel<D>;
+  auto kfn = kv4_chunk_kernel<D, CAUSAL>;
   static std::mutex mu;
   static std::set<int> ready;
   int dev = 0;
@@ -876,6 +962,11 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
   const int blocks = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
   kfn<<<blocks, kThreads, Cfg<D>::SMEM, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
+  return p.causal ? launch<D, true>(p, num_sms, stream) : launch<D, false>(p, num_sms, stream);
 }
 
 }  // namespace hchunk

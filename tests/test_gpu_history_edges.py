@@ -284,3 +284,43 @@ def test_outlying_and_unseen_values_few_rows(d, q):
     o, lse = b.attend(Q, True)
     assert b.c.status.item() == 0
     check_outliers(b, Q, o, lse, False)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("many", [False, True])
+def test_unseen_and_uneven_keys(d, many):
+    """Keys from 2^-100 to 2^100 of the usual beside ordinary ones in every page, and
+    keys of 1e38 that only the last rows of a causal chunk see.  Rows whose logits
+    fp32 knows to a unit are within the bounds; nothing overflows in the others
+    that see no more than 2^40."""
+    rng = np.random.default_rng(d)
+    Hkv, H, q = 1, 2, 30
+    kvs = []
+    for n in (150, 700):
+        K, V = HC.keys_values(rng, n, Hkv, d)
+        tiny = rng.choice(n - 40, 30, replace=False)
+        K[tiny] = HC.bf16_round(K[tiny] * 2.0 ** rng.integers(-100, -3, 30)[:, None, None])
+        K[n - 12] = HC.bf16_round(K[n - 12] * 2.0 ** 40)     # seen by 13 rows of 30
+        K[n - 5] = 1e38 * np.sign(K[n - 5])
+        kvs.append((K, V))
+    b = Batch(rng, kvs, H, [q, q], many, d)
+    Q = normal(rng, 2 * q, H, d)
+    Q[3] = HC.bf16_round(Q[3] * 2.0 ** -60)
+    o, lse = b.attend(Q, True)
+    assert b.c.status.item() == 0
+    at, exact = 0, 0
+    for r in range(2):
+        k, v, y, x, pos = b.rows_of(r, 0)
+        for t in range(q):
+            seen = pos < b.kv[r] - (q - 1 - t)
+            qr = Q[at + t].astype(np.float64)
+            dS = HC.logit_bound(qr, y[seen], d ** -0.5, d)
+            if dS < 0.1:
+                exact += 1
+                oo, e, P = OH.attend_rows(qr, k[seen], v[seen], d ** -0.5)
+                HC.check(o[at + t], lse[at + t], oo, e, P, x[seen], v[seen], dS, False, (r, t))
+            elif np.abs(k[seen]).max() < 2.0 ** 50:
+                assert np.isfinite(o[at + t]).all() and np.isfinite(lse[at + t]).all()
+                assert (np.abs(o[at + t]) <= np.abs(v[seen]).max(0) * (1 + HC.EPS)).all()
+        at += q
+    assert exact >= 36
