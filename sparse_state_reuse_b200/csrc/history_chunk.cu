@@ -299,8 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     uint32_t n0 = 0;             // tiles of the segments before
     if (warp == 9) {
       // ---------------------------------------------------------- records
-      // bound of |x|: 8 s + |least + 8 s|; not finite: the row stands for NaN
-      auto bound = [](uint32_t m) { return fmaf(8.f, bf_lo(m), fabsf(fmaf(8.f, bf_lo(m), bf_hi(m)))); };
+      // bound of |x|: |least| or |least + 15 s|; not finite: the row stands for NaN
+      auto bound = [](uint32_t m) {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(bf_hi(m))), "f"(fabsf(fmaf(15.f, bf_lo(m), bf_hi(m)))));
+        return r;
+      };
       auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
       while (ok && next_segment()) {
         const hattn::Pages pages(p, sg);

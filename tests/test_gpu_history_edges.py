@@ -17,7 +17,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 PAGE = dt.PAGE
-BALLAST = 600        # queries of the request that makes a batch's work large, over 20000 tokens
+BALLAST = 1200        # queries of the request that makes a batch's work large, over 20000 tokens
 
 
 def ints(x, dtype=torch.int32):
@@ -324,3 +324,33 @@ def test_unseen_and_uneven_keys(d, many):
                 assert (np.abs(o[at + t]) <= np.abs(v[seen]).max(0) * (1 + HC.EPS)).all()
         at += q
     assert exact >= 36
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("many", [False, True])
+def test_the_largest_values_and_keys(d, many):
+    """Rows of 3.3e38 of both signs: their 15 steps end within fp32, 8 steps from 0 would
+    not.  One such value a row of Q takes all; a key of that size is seen only by
+    rows of Q that are nothing to it."""
+    rng = np.random.default_rng(d)
+    H, q, n = 1, 40, 300
+    K, V = normal(rng, n, 1, d) * 0.25, normal(rng, n, 1, d)
+    K = HC.bf16_round(K)
+    K[:, :, 0] = 0
+    K[7] = 0
+    K[7, :, 0] = 64.0                                      # takes all of the rows that have channel 0
+    V[7] = HC.bf16_round(3.3e38 * np.sign(V[7]))
+    K[200] = HC.bf16_round(3.3e38 * np.sign(K[200]))
+    K[200, :, 0] = -3.3e38
+    b = Batch(rng, [(K, V)], H, [q], many, d)
+    v = b.rows_of(0, 0)[1][:n]
+    assert np.isfinite(v).all()
+    Q = np.zeros((q, H, d), np.float32)
+    Q[..., 0] = 8.0
+    o, lse = b.attend(Q, False)
+    assert b.c.status.item() == 0
+    k = b.rows_of(0, 0)[0][:n, 0]
+    s = 8.0 * k * d ** -0.5
+    assert np.argmax(s) == 7 and np.partition(s, -2)[-2] < s[7] - 30
+    assert (np.abs(o[:, 0] - v[7]) <= 3 * HC.EPS * np.abs(v[7]).max()).all()
+    assert (np.abs(lse - s[7]) <= 2.0 ** -19 * (1 + s[7])).all()
