@@ -726,7 +726,8 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
 
 }  // namespace hattn
 
-// Parts of items (either kernel's) and then both kernels' counters.
+// Parts of items (either kernel's), then both kernels' counters, then the words of
+// the many rows' kernel.
 static size_t partial_floats(int d) {
   const size_t few = (size_t)hattn::kMaxBlocks * 2 * hattn::kRows * (d + 2);
   const size_t many = kv4_chunk_partial_floats(d);
@@ -734,7 +735,7 @@ static size_t partial_floats(int d) {
 }
 
 size_t kv4_attn_workspace_bytes(int d) {
-  return partial_floats(d) * sizeof(float) + (hattn::kMaxBlocks + kv4_chunk_counters()) * sizeof(int);
+  return partial_floats(d) * sizeof(float) + (hattn::kMaxBlocks + kv4_chunk_counters() + kv4_chunk_words()) * sizeof(int);
 }
 
 cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int max_blocks, int n_pages,
@@ -773,6 +774,7 @@ cudaError_t launch_kv4_attn(int R, int H, int Hkv, int d, int T, int max_q, int 
   p.lh = lse_strides[1];
   p.partial = static_cast<float *>(workspace);
   p.counters = reinterpret_cast<int *>(p.partial + partial_floats(d));
+  p.words = p.counters + hattn::kMaxBlocks + kv4_chunk_counters();
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
   // Which requests of a batch have few rows, and how long they are, only the

@@ -31,6 +31,7 @@ struct Params {
   long long lt, lh;
   float *partial;                    // two parts of items a block
   int *counters;                     // one a block, all zero between launches
+  int *words;                        // many rows, causal: one a block, see Sizes
   int side;                          // which requests are this launch's, see Side
   int *dev_status;
   long long wait_limit_ns;
@@ -361,5 +362,6 @@ __device__ __forceinline__ float max_abs8(const uint4 &u) {
 cudaError_t launch_kv4_chunk(const hattn::Params &p, int d, int num_sms, cudaStream_t stream);
 size_t kv4_chunk_partial_floats(int d);
 int kv4_chunk_counters();
+int kv4_chunk_words();
 
 }  // namespace ditango

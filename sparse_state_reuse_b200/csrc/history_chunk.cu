@@ -10,8 +10,12 @@
 //      h sum(q), is one more step of the product: h and sum(q) are split into
 //      three fp16 parts each, and six of the 16 columns of that step hold the
 //      pairs that matter (the rest is below 2^-32 of it).
-//   V  s' (c' - 8) + h' in fp16 (2^-11, four times finer than the bf16 it was
+//   V  s' (c' - 8) + h' in fp16 (2^-12, eight times finer than the bf16 it was
 //      made from) over a power of two that no value of the item so far exceeds.
+//      Where a causal item's last tiles hold values that some rows do not see and
+//      that are far from the others, V and P are bf16 from there on, over a power of
+//      two that leaves room for every bf16 value: 2^-9 and 2^-9, but no row's values
+//      depend on another's keys.
 // P is fp16.
 //
 // One block of threads an SM takes two row tiles (256 rows) against the same
@@ -37,7 +41,7 @@
 // overwrites the first 64 columns of its S.  Each block takes an equal share of
 // the line of work.
 //
-// 3600 queries over 25200 tokens, 24 heads of 96: 1.19 ms, 703 TFLOP/s (43% of the
+// 3600 queries over 25200 tokens, 24 heads of 96: 1.20 ms, 697 TFLOP/s (43% of the
 // measured bf16 rate); the tensor pipe is busy 37% of the time, the exponentials'
 // unit 46%, the issue slots 47%.  The step of a row tile is a chain, Q K^T (1/5 of
 // it), softmax (3/5) and P V (1/5), of which the two row tiles hide only each
@@ -87,23 +91,37 @@ __device__ __forceinline__ bool outgrown(float mx, float m) {
   return mx > (fabsf(m) > kHuge ? m : m + (kSpareLog2 + kRescaleLog2));
 }
 
+// A causal item's last tiles hold keys that not all of its rows see, and those may
+// be of any size beside the others.  (Keys that a row sees need no such care: what
+// the largest takes from the others is below the rounding of its own score, and
+// 2^-25 of the largest value.)  A call that is causal is launched twice: kAsIs looks,
+// before it begins, whether any of these keys are 2^7, or their values 2^10, from
+// one another, and kFarApart, which does nothing else, does the work once more where
+// they are.  A test for it in the loops below costs them 3 to 25% (the registers are
+// full), the look 1% and the empty launch 3 us.
+enum Sizes { kAsIs, kFarApart };
+
 // What is known of a tile before its codes are unpacked.
 //
-// A causal item's last tiles hold keys that not all of its rows see, and those may
-// be of any size beside the others.  Where the sizes of such a tile's keys differ by
+// kFarApart: where the sizes of such a tile's keys differ by
 // more than 2^4, K is held key by key: each over a power of two of its own, which
-// the softmax puts back into the scores.  (Keys that a row sees need no such care:
-// what the largest takes from the others is below the rounding of its own score.)
+// the softmax puts back into the scores.  Where the values differ by more than 2^10, from one another or from those before,
+// this tile and those after it hold V in bf16, and the softmax P.
 constexpr int kRing = 4;
-constexpr uint32_t kEven = 4;
-constexpr uint32_t kOwnK = 1;
+constexpr uint32_t kEven = 4, kEvenV = 10;
+constexpr uint32_t kOwnK = 1, kWideV = 2;
+// V and O in bf16's range: values of 2^128 give sums of 2^(15 + 128 - 40) a key,
+// and those below 2^-86 are lost.
+constexpr uint32_t kWideRef = (127u + 40u) << 23;
+constexpr float kWideDown = 0x1p-40f;
 struct alignas(16) Tile {
   uint2 v[BN];                  // V's s and h over vref, as fp16 pairs
   uint32_t ks[BN];              // K's s over kref, as an fp16 pair
   float kh[BN];                 // K's h over kref
+  float2 vw[BN];                // kWideV: V's s and h over vref, and v is (1, 0)
   float kf[BN];                 // kOwnK: the keys' own powers of two, over kref
   float kref, vref;             // the powers of two over which K and V are held
-  uint32_t flags;               // kOwnK
+  uint32_t flags;               // kOwnK, kWideV
   int pos[2];                   // first token of each page, past every length where there is none
   uint32_t bad[4];              // keys whose V is not finite (written as 0: the softmax marks who sees it)
 };
@@ -207,9 +225,68 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-template <int D, bool CAUSAL>
+constexpr uint32_t kBothBf16 = (1u << 7) | (1u << 10);
+
+// The sizes of a causal item's keys and values that not all of its rows see, and of
+// its first row's own, are near enough to one another for kAsIs.  All threads.
+// near[4]: largest and least K, V.
+constexpr uint32_t kNearK = 7, kNearV = 10;
+__device__ __forceinline__ float bound_of(uint32_t meta) {     // of |x| of a row: |least| or |least + 15 s|, or not finite
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(bf_hi(meta))), "f"(fabsf(fmaf(15.f, bf_lo(meta), bf_hi(meta)))));
+  return r;
+}
+template <int D>
+__device__ __forceinline__ bool far_apart(const Params &p, const hattn::Segment &sg, uint32_t *near) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int from = max(0, sg.rq.kv - (sg.rq.n_q - 1) + sg.tile * TR / p.G - 1);
+  __syncthreads();
+  if (threadIdx.x < 4) near[threadIdx.x] = (threadIdx.x & 1) ? ~0u : 0u;
+  __syncthreads();
+  const int *table = p.block_table + (size_t)sg.r * p.max_blocks;
+  uint32_t lim[4] = {0u, ~0u, 0u, ~0u};
+  const int last = (sg.rq.kv + kPage - 1) / kPage;
+  constexpr int U = 4, WARPS = kThreads / 32;
+  for (int b0 = from / kPage + warp; b0 < last; b0 += WARPS * U) {
+    int page[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) page[e] = b0 + e * WARPS < last ? __ldg(table + b0 + e * WARPS) : -1;
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (page[e] < 0 || page[e] >= p.n_pages) continue;
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(
+          p.data + ((size_t)page[e] * p.Hkv + sg.h) * page_bytes(D) + kPage * D);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int pos = (b0 + e * WARPS) * kPage + (k & 1) * 32 + lane;
+        const float x = bound_of(__ldg(src + k * 32 + lane));
+        if (pos >= from && pos < sg.rq.kv && x > 0.f && x < INFINITY) {
+          lim[(k >> 1) * 2] = max(lim[(k >> 1) * 2], __float_as_uint(x));
+          lim[(k >> 1) * 2 + 1] = min(lim[(k >> 1) * 2 + 1], __float_as_uint(x));
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lim[k] = (k & 1) ? __reduce_min_sync(0xffffffffu, lim[k]) : __reduce_max_sync(0xffffffffu, lim[k]);
+    if (lane == 0) {
+      if (k & 1) atomicMin(near + k, lim[k]);
+      else atomicMax(near + k, lim[k]);
+    }
+  }
+  __syncthreads();
+  return (near[0] >> 23) > (near[1] >> 23) + kNearK || (near[2] >> 23) > (near[3] >> 23) + kNearV;
+}
+
+template <int D, Sizes SIZES>
 __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
+  constexpr bool FAR = SIZES == kFarApart;
+  if constexpr (FAR) {
+    // the words of every block of the launch before
+    if (!__syncthreads_or(threadIdx.x < gridDim.x && p.words[threadIdx.x] != 0)) return;
+  }
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -246,7 +323,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 
   {
     hattn::Range g;
-    if (!hattn::find_range<TR, 2, kSetup, kThreads, true>(p, kMinUnits, g, s_scan, &s_request)) return;
+    if (!hattn::find_range<TR, 2, kSetup, kThreads, true>(p, kMinUnits, g, s_scan, &s_request)) {
+      if (!FAR && p.causal && threadIdx.x == 0) p.words[blockIdx.x] = 0;
+      return;
+    }
+    if (!FAR && p.causal) {
+      __shared__ uint32_t s_near[4];
+      WalkT look;
+      hattn::Segment part;
+      look.start(p, g);
+      bool far = false;
+      while (look.next(p, part)) far = far_apart<D>(p, part, s_near) || far;
+      if (threadIdx.x == 0) p.words[blockIdx.x] = far;
+    }
     if (lane == 0) s_walk[warp].start(p, g);
     if (threadIdx.x == 0) s_range = g;
   }
@@ -300,16 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     if (warp == 9) {
       // ---------------------------------------------------------- records
       // bound of |x|: |least| or |least + 15 s|; not finite: the row stands for NaN
-      auto bound = [](uint32_t m) {
-        float r;
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(bf_hi(m))), "f"(fabsf(fmaf(15.f, bf_lo(m), bf_hi(m)))));
-        return r;
-      };
+      auto bound = [](uint32_t m) { return bound_of(m); };
       auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
       while (ok && next_segment()) {
         const hattn::Pages pages(p, sg);
         const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
         uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
+        bool wide = false;
         const Edge edge(p, sg);
         // page numbers are read two tiles ahead, scales one
         int page[2], ppos[2], pos[2], at[2];   // the next tile's pages and places, this one's
@@ -347,6 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           if (!(ok = wait_warp(tile_empty(n), ((n / kRing) & 1) ^ 1, ctl))) break;
           Tile &tile = tiles[n % kRing];
           uint32_t ktop = 0, vtop = 0;
+          if (FAR && j >= edge.last) {      // seen by no row
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mv[k] = 0u;
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float kb = bound(mk[k]), vb = bound(mv[k]);
@@ -357,7 +447,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             if (lane == 0) tile.bad[k] = word;
           }
           const uint32_t kref_bits = reference(__reduce_max_sync(0xffffffffu, ktop));
-          vref_bits = max(vref_bits, reference(__reduce_max_sync(0xffffffffu, vtop)));
+          const uint32_t vnew = reference(__reduce_max_sync(0xffffffffu, vtop));
+          if (FAR && j >= edge.first && j < edge.last && !wide) {
+            uint32_t low = ~0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float vb = bound(mv[k]);
+              if (vb > 0.f) low = min(low, __float_as_uint(vb));
+            }
+            low = __reduce_min_sync(0xffffffffu, low);
+            wide = (vnew >> 23) > (low >> 23) + 1u + kEvenV ||
+                   (vref_bits > 64u << 23 && vnew > vref_bits + (kEvenV << 23));
+          }
+          vref_bits = FAR && wide ? kWideRef : max(vref_bits, vnew);
           const float kdown = __uint_as_float((254u << 23) - kref_bits), vdown = __uint_as_float((254u << 23) - vref_bits);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -367,15 +469,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             tile.kh[key] = fmaf(8.f, ks, bf_hi(mk[k])) * kdown;
             const float vh = fmaf(8.f, vs, bf_hi(mv[k])) * vdown;
             tile.v[key] = make_uint2(hattn::pack_f16x2(vs * vdown, vs * vdown), hattn::pack_f16x2(vh, vh));
+            if (FAR && wide) {
+              tile.v[key] = make_uint2(0x3c003c00u, 0u);
+              tile.vw[key] = make_float2(vs * vdown, vh);
+            }
           }
           if (lane == 0) {
             tile.kref = __uint_as_float(kref_bits);
             tile.vref = __uint_as_float(vref_bits);
-            if (CAUSAL) tile.flags = 0u;
+            if (FAR) tile.flags = wide ? kWideV : 0u;
             tile.pos[0] = pos[0];
             tile.pos[1] = pos[1];
           }
-          if (CAUSAL && j >= edge.first && j < edge.last) {
+          if (FAR && j >= edge.first && j < edge.last) {
             // K once more, key by key, if the sizes are far apart (the scales are read
             // again: this is rare, and the code around it stays as fast as it is)
             auto meta = [&](int k) {
@@ -406,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
                 // a power of two in the middle, so that no score with its key's own
                 // factor leaves fp32
                 tile.kref = 0x1p20f;
-                tile.flags = kOwnK;
+                tile.flags = kOwnK | (wide ? kWideV : 0u);
               }
             }
           }
@@ -486,6 +592,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
               reinterpret_cast<uint4 *>(smem + C::OFF_KA + (n & 1) * C::AUG)[aug_at(row)] = make_uint4(h12, h13, h12, 0);
             }
           }
+          if (FAR && is_v && (tile.flags & kWideV)) {
+            // c - 8 stands there: s (c - 8) + h as bf16 in its place
+#pragma unroll 1
+            for (int row = row0; row < BN; row += C::STEP) {
+              const float2 sh = tile.vw[row];
+              auto wide = [&](uint32_t x) {
+                return pack_bf16x2(fmaf(__half2float(__ushort_as_half((unsigned short)(x & 0xffffu))), sh.x, sh.y),
+                                   fmaf(__half2float(__ushort_as_half((unsigned short)(x >> 16))), sh.x, sh.y));
+              };
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                uint4 *to = reinterpret_cast<uint4 *>(dst + place(q) + (row - row0) * 128);
+                const uint4 x = *to;
+                *to = make_uint4(wide(x.x), wide(x.y), wide(x.z), wide(x.w));
+              }
+            }
+          }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(is_v ? v_full(n) : k_full(n));
@@ -532,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           tc_commit(full);
         }
       };
-      auto pv = [&](int k, uint32_t n, bool acc) {
+      auto pv = [&](int k, uint32_t n, bool acc, uint32_t idesc) {
         const uint64_t b = fix64(smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024));
         const uint32_t accumulate = fix32(acc ? 1u : 0u);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + 256 + 128 * k, tmem + 128 * k + kk * 8, b + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+            mma_ts(tmem + 256 + 128 * k, tmem + 128 * k + kk * 8, b + (uint64_t)((kk * 2048) >> 4), idesc,
                    kk > 0 ? 1u : accumulate);
         }
       };
@@ -561,9 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           const uint32_t n = n0 + t;
           const bool more = t + 1 < T;
           if (!(ok = wait_warp(v_full(n), (n >> 1) & 1, ctl))) break;
+          uint32_t kind = idesc_pv;
+          if (FAR && (tiles[n % kRing].flags & kWideV)) kind |= kBothBf16;
+          kind = fix32(kind);
           if (!(ok = wait_warp(p_full(0), n & 1, ctl))) break;
           tc_fence_after();
-          pv(0, n, t > 0);
+          pv(0, n, t > 0, kind);
           if (more) {
             if (!(ok = wait_warp(k_full(n + 1), ((n + 1) >> 1) & 1, ctl))) break;
             tc_fence_after();
@@ -575,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
             if (!(ok = wait_warp(p_full(1), pc1 & 1, ctl))) break;
             ++pc1;
             tc_fence_after();
-            pv(1, n, t > 0);
+            pv(1, n, t > 0, kind);
             if (more) qk(1, n + 1);
             else commit(o_full(1));
           }
@@ -626,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     {
       const bool live = r < rows;
       const int tok = live ? (row0 + r) / p.G : 0, head = live ? (row0 + r) % p.G : 0;
-      if (CAUSAL && live) vis -= sg.rq.n_q - 1 - tok;
+      if (p.causal && live) vis -= sg.rq.n_q - 1 - tok;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + (sg.rq.q0 + tok) * p.qt + (sg.h * p.G + head) * p.qh);
       uint4 u[D / 8];
       float big = 0.f;
@@ -666,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       const int n0 = max(0, min(kPage, vis - tile.pos[0])), n1 = max(0, min(kPage, vis - tile.pos[1]));
       __syncwarp();
       tc_fence_after();
-      if constexpr (CAUSAL) {
+      if constexpr (FAR) {
         if (__any_sync(0xffffffffu, (tile.flags & kOwnK) != 0u)) {
           // the keys' own factors, in place, before the scores take the registers
           // (this test alone costs the loop 3%: calls that are not causal have none)
@@ -767,6 +893,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         unf2(add2(lsum[1], lsum[3]), s2, s3);
         l += (s0 + s1) + (s2 + s3);
       }
+      if constexpr (FAR) {
+        if (__any_sync(0xffffffffu, (tile.flags & kWideV) != 0u)) {     // P in bf16, as V
+          tc_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < BN / 2; c += 8) {
+            uint32_t v[8];
+            tmem_ld8(tS + c, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = pack_bf16x2(__half2float(__ushort_as_half((unsigned short)(v[e] & 0xffffu))),
+                                 __half2float(__ushort_as_half((unsigned short)(v[e] >> 16))));
+            tmem_st8(tS + c, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+          }
+        }
+      }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -781,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
     const bool whole = sg.whole();
     float *part = p.partial + ((size_t)blockIdx.x * 2 + (sg.u0 == 0 ? 1 : 0)) * C::SLOT + kt * BM * (D + 2);
     const bool none = !(l > 0.f) && l == l;
-    float fac = whole ? (l > 0.f ? vref / l : 0.f) : vref;
+    // (parts are over 2^40: a sum of the largest values that is not yet divided stays finite)
+    float fac = whole ? (l > 0.f ? vref / l : 0.f) : vref * kWideDown;
     if (!(l == l) || poison) fac = __uint_as_float(0x7fc00000u);
     float4 *epi = reinterpret_cast<float4 *>(smem + C::OFF_Q + kt * C::TILE + (warp & 3) * 4096);
     auto out_row = [&](int row) -> long long {      // element offset of a row of the tile in out
@@ -923,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       for (int w = 0; w < UR; ++w) {
         const int row = base + 16 * w + row_in;
         if (row >= rows) continue;
-        const float inv = lt[w] > 0.f ? 1.f / lt[w] : (lt[w] == lt[w] ? 0.f : lt[w]);
+        const float inv = lt[w] > 0.f ? 1.f / kWideDown / lt[w] : (lt[w] == lt[w] ? 0.f : lt[w]);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
           const float4 z = make_float4(v[w][q].x * inv, v[w][q].y * inv, v[w][q].z * inv, v[w][q].w * inv);
@@ -942,9 +1085,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
   named_bar_arrive(1, kThreads);
 }
 
-template <int D, bool CAUSAL>
+template <int D, Sizes SIZES>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
-  auto kfn = kv4_chunk_kernel<D, CAUSAL>;
+  auto kfn = kv4_chunk_kernel<D, SIZES>;
   static std::mutex mu;
   static std::set<int> ready;
   int dev = 0;
@@ -970,11 +1113,13 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
-  return p.causal ? launch<D, true>(p, num_sms, stream) : launch<D, false>(p, num_sms, stream);
+  const cudaError_t e = launch<D, kAsIs>(p, num_sms, stream);
+  return e != cudaSuccess || !p.causal ? e : launch<D, kFarApart>(p, num_sms, stream);
 }
 
 }  // namespace hchunk
 
+int kv4_chunk_words() { return hchunk::kMaxBlocks; }
 size_t kv4_chunk_partial_floats(int d) { return (size_t)hchunk::kMaxBlocks * 2 * hchunk::TR * (d + 2); }
 int kv4_chunk_counters() { return 2 * hchunk::kMaxBlocks; }
 

@@ -256,7 +256,8 @@ def outliers(rng, n, Hkv, d, key, unseen=True):
 
 
 def check_outliers(b, Q, o, lse, wide):
-    """As Batch.check: P s' (or P, and V with it: `wide`, both bf16) rounded once."""
+    """As Batch.check, P s' rounded once; `wide`: P is rounded to fp16 and then with V
+    to bf16, 2^-12 + 2 2^-9 of P |v| and their products."""
     scale, G, at = b.d ** -0.5, b.H // b.Hkv, 0
     for r, n in enumerate(b.q_lens):
         for h in range(b.Hkv):
@@ -267,7 +268,7 @@ def check_outliers(b, Q, o, lse, wide):
                 qr = Q[at + t, g].astype(np.float64)
                 oo, e, P = OH.attend_rows(qr, k[seen], v[seen], scale)
                 dS = HC.logit_bound(qr, y[seen], scale, b.d)
-                HC.check(o[at + t, g], lse[at + t, g], oo, e, P, (np.abs(v) * (1 + HC.EPS) if wide else x)[seen],
+                HC.check(o[at + t, g], lse[at + t, g], oo, e, P, (np.abs(v) * (1 + 2.0 ** -4 + 2.0 ** -7) if wide else x)[seen],
                          v[seen], dS, False, (r, h, t))
         at += n
 
@@ -324,6 +325,34 @@ def test_unseen_and_uneven_keys(d, many):
                 assert (np.abs(o[at + t]) <= np.abs(v[seen]).max(0) * (1 + HC.EPS)).all()
         at += q
     assert exact >= 36
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("q,kvs", [(30, (70, 200, 900)), (100, (130, 2000)), (300, (300, 1100))])
+def test_outlying_and_unseen_values_many_rows(d, q, kvs):
+    """What not all rows of a causal chunk see is of any size.  (Values that all rows
+    see stay within 2^20 of one another here: below 2^-25 of the largest they are
+    lost, as the header says.)"""
+    rng = np.random.default_rng(d + q)
+    Hkv, H = 1, 2
+    key = HC.bf16_round(4.0 * rng.choice([-1, 1], d))
+    made = []
+    for n in kvs:
+        K, V = outliers(rng, n, Hkv, d, key)
+        for at in (n // 3, n - 40):
+            V[at] = normal(rng, Hkv, d)
+        if n > 3 * q // 2:
+            V[n - q - 5] = HC.bf16_round(V[n - q - 5] * 2.0 ** 12)
+        made.append((K, V))
+    b = Batch(rng, made, H, [q] * len(kvs), True, d)
+    Q = HC.bf16_round(key * 0.25 + normal(rng, q * len(kvs), H, d))
+    o, lse = b.attend(Q, True)
+    assert b.c.status.item() == 0
+    check_outliers(b, Q, o, lse, True)
+    # the blocks listed in any order: those that no row sees among the first
+    lists = [[rng.permutation(-(-n // PAGE)).tolist()] for n in kvs]
+    got = b.attend(Q, True, lists=lists, room=max(len(x[0]) for x in lists) + 2)
+    check_outliers(b, Q, *got, True)
 
 
 @pytest.mark.parametrize("d", [64, 96, 128])
