@@ -6,6 +6,8 @@ definitions, one request and one row at a time.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 PAGE = 64
@@ -20,8 +22,8 @@ def bf16_value(bits):
     return (np.asarray(bits, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)
 
 
-def least_bf16_not_below(x: float) -> float:
-    """The smallest bf16 value >= x (x >= 0)."""
+def least_bf16_not_below(x) -> float:
+    """The smallest bf16 value >= x (x >= 0; a float or a Fraction)."""
     f = np.float32(x)
     if float(f) < x:
         f = np.nextafter(f, np.float32(np.inf))
@@ -36,8 +38,14 @@ def quantize_row(x):
     if not np.isfinite(x).all():
         return np.zeros(len(x), np.uint8), np.nan, np.nan
     lo, hi = x.min(), x.max()
-    s = least_bf16_not_below((hi - lo) / 15)
-    c = np.rint((x - lo) / s) if s > 0 else np.zeros(len(x))
+    s = least_bf16_not_below((Fraction(float(hi)) - Fraction(float(lo))) / 15)
+    if s == 0:
+        return np.zeros(len(x), np.uint8), s, lo
+    q = (x - lo) / s
+    c = np.rint(q)
+    # near the middle between two codes fp64 may not know the side
+    for i in np.flatnonzero(np.abs(np.abs(q - c) - 0.5) < 1e-9):
+        c[i] = round((Fraction(float(x[i])) - Fraction(float(lo))) / Fraction(float(s)))    # ties to even
     return c.astype(np.uint8), s, lo
 
 

@@ -182,17 +182,23 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // A quotient that is k + 1/2 then comes out as that (it is a fp32 number), and
 // one that is not stays on its side: t and s being multiples of powers of two
 // with 24 and 8 bits, it is at least 2^-24 of itself away.  All of this needs t
-// to be exact; `bad` collects t + lo - x, which is 0 exactly then.  The few
-// groups with an inexact t, and scales outside fp32's comfortable range, are
-// formed again in fp64, where the difference of two bf16 values is exact for
-// what can matter to the rounding.
+// to be exact.  Where |x| < |lo|, t + lo - x is what t lacks (the sum of a larger
+// and a smaller number and its remainder), and `bad` collects it.  Where |x| >= |lo|
+// it is not (both roundings can cancel: least 2^-30, x 1.5), but there t is exact as
+// long as |x| is at most 2^14 |lo|: it is a multiple of lo's last bit and 2^23 of
+// those at most.  Rows whose least value is smaller, groups with an inexact t, and
+// scales outside fp32's comfortable range take the difference in fp64, with its
+// remainder: against the middle between two codes (13 bits), and if it is there, by
+// the remainder's sign.
 __device__ __noinline__ uint32_t codes8_wide(uint4 v, float lo, float s) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   uint32_t w = 0;
   for (int k = 0; k < 8; ++k) {
-    const float x = (k & 1) ? bf_hi(u[k >> 1]) : bf_lo(u[k >> 1]);
-    const double q = rint(((double)x - (double)lo) / (double)s);
-    w |= (uint32_t)(int)fmin(fmax(q, 0.0), 15.0) << (4 * k);
+    const double x = (k & 1) ? bf_hi(u[k >> 1]) : bf_lo(u[k >> 1]), y = -(double)lo;
+    const double t = x + y, z = t - x, rest = (x - (t - z)) + (y - z);     // t + rest = x - lo
+    const double c = fmin(fmax(floor(t / (double)s), 0.0), 15.0), middle = (c + 0.5) * (double)s;
+    const bool up = t > middle || (t == middle && (rest > 0.0 || (rest == 0.0 && ((int)c & 1))));
+    w |= (uint32_t)min((int)c + (up ? 1 : 0), 15) << (4 * k);
   }
   return w;
 }
@@ -227,7 +233,7 @@ __device__ __forceinline__ uint32_t scale_bits(float lo, float hi) {
   if (fmaxf(fabsf(lo), fabsf(hi)) < 1e37f) {
     q = __fdiv_ru(__fsub_ru(hi, lo), 15.f);
   } else {
-    q = __double2float_ru(((double)hi - (double)lo) / 15.0);
+    q = __double2float_ru(__ddiv_ru(__dsub_ru((double)hi, (double)lo), 15.0));
   }
   const uint32_t b = __float_as_uint(q);
   return (b + 0xffffu) >> 16;
@@ -305,7 +311,8 @@ __global__ void __launch_bounds__(kRowThreads) write_kernel(const RowsParams p) 
     uint32_t sb = scale_bits(lo, hi);
     const float s = __uint_as_float(sb << 16);
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    const bool fine = (s > 1e-30f && s < 1e30f) || s == 0.f;
+    const bool fine =
+        (s > 1e-30f && s < 1e30f && (lo == 0.f || fabsf(hi) <= 16384.f * fabsf(lo))) || s == 0.f;
     uint32_t w[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {

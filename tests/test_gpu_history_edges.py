@@ -10,6 +10,7 @@ import sparse_state_reuse_b200 as dt
 from oracle import history as OH
 
 import history_common as HC
+from test_history_checks_rows import tie_row
 
 pytestmark = pytest.mark.gpu
 
@@ -383,3 +384,39 @@ def test_the_largest_values_and_keys(d, many):
     assert np.argmax(s) == 7 and np.partition(s, -2)[-2] < s[7] - 30
     assert (np.abs(o[:, 0] - v[7]) <= 3 * HC.EPS * np.abs(v[7]).max()).all()
     assert (np.abs(lse - s[7]) <= 2.0 ** -19 * (1 + s[7])).all()
+
+
+# ---------------------------------------------------------------- the quantiser
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_codes_beside_a_tiny_least_value_are_exact(d):
+    """Quotients that are a least value of 2^-30 (2^-14 ... 2^-133) of the others away
+    from a tie, on either side, and scales that reach the largest value by as little."""
+    rng = np.random.default_rng(d)
+    rows = []
+    for tiny in (2.0 ** -13, 2.0 ** -14, 2.0 ** -15, 2.0 ** -17, 2.0 ** -30, 2.0 ** -60, 2.0 ** -100, 2.0 ** -133, 0.0):
+        for sign in (1, -1):
+            for size in (1.0, 2.0 ** 30, 2.0 ** -20, 2.0 ** 122):
+                x, _ = tie_row(sign * tiny)
+                row = np.resize(x, d) * size
+                row[np.arange(d) % len(x) == 0] = sign * tiny
+                row[d - 1] = x[-1] * size
+                rows.append(row)
+                rows.append(-row)
+    rows.append(np.where(np.arange(d) % 2 == 0, 15 * 2.0 ** 123, -2.0 ** -120))
+    rows += [HC.bf16_round(np.abs(rng.standard_normal(d)) * 2.0 ** rng.integers(-30, 1, d)) for _ in range(60)]
+    x = np.stack(rows).astype(np.float32)
+    assert (HC.bf16_round(x) == x).all()
+    n = len(x)
+    pages = -(-n // PAGE)
+    want = HC.HostPages(pages, 1, d)
+    for t in range(n):
+        want.put(t // PAGE, t % PAGE, 0, 0, x[t])
+        want.put(t // PAGE, t % PAGE, 0, 1, x[n - 1 - t])
+    c = dt.KV4Cache(pages, 1, d, 1, pages, n)
+    c.write(HC.up(x[:, None]), HC.up(x[::-1, None]), torch.arange(n, device="cuda"))
+    torch.cuda.synchronize()
+    got = c.data.cpu().numpy()
+    bad = np.argwhere(got != want.data)
+    for p, h, i in bad:                              # -0 and 0 are the same least value
+        assert i >= PAGE * d and got[p, h, i] % 128 == want.data[p, h, i] % 128 == 0, (p, i)
+    assert c.status.item() == 0
