@@ -530,7 +530,8 @@ ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int3
  * Summaries of the blocks of x dev bf16 [B][H][N][d] ((b, h, n) element
  * strides, multiples of 8; 16-byte aligned): of each block of `block` rows
  * (DITANGO_PAGE or DITANGO_QBLOCK; the last one may be shorter) the sum S over
- * its rows and, with top = max |S|,
+ * its rows (fp64, of sums of up to four rows in fp32, which are exact for values
+ * within 2^14 of one another) and, with top = max |S|,
  *   codes int8 [B][H][nb][d] = rint(127 S / top), scale float32 [B][H][nb] =
  *   top / (127 n), mean float32 [B][H][nb][d] (or NULL) = S / n.
  *   len          dev int32 [B] valid rows, or NULL; blocks without a valid row,

@@ -17,11 +17,14 @@ namespace sel {
 
 // ---------------------------------------------------------------- summaries
 // A block of threads takes 128 rows (one query block or two key blocks), all in
-// flight at once (16 bytes a load): bound by reading x.  Sums are exact: a lane
-// adds up to four bf16 values in fp32 (24 bits hold them but for values 2^13
-// times smaller than their neighbours), and goes on in fp64.  Q and K of 76800
-// tokens, 40 heads of 128: 262 us, 6.0 TB/s (92% of the copy rate).
+// flight at once (16 bytes a load): bound by reading x.  A lane adds up to four bf16
+// values in fp32, which holds their sum exactly unless they differ by 2^14 and
+// more, and goes on in fp64.  (All in fp64: 76 us more, a conversion a value.)  The
+// values go in over 2^7, which is exact for every bf16 value and leaves room for
+// four of the largest.  Q and K of 76800 tokens, 40 heads of 128: 262 us, 6.0 TB/s
+// (92% of the copy rate).
 constexpr int kSumThreads = 256;
+constexpr float kDown = 0x1p-7f;
 
 struct SummaryParams {
   int H, N, nb;
@@ -61,22 +64,22 @@ __device__ __forceinline__ void summarise(const SummaryParams &p, int h) {
   for (int q = 0; q < NB; ++q) {
     double acc[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.0;
-#pragma unroll
     for (int a = 0; a < kLoads; a += 4) {
       float f[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (a + e < kLoads) {
           const uint4 u = v[q * kLoads + a + e];
-          f[0] += bf_lo(u.x); f[1] += bf_hi(u.x); f[2] += bf_lo(u.y); f[3] += bf_hi(u.y);
-          f[4] += bf_lo(u.z); f[5] += bf_hi(u.z); f[6] += bf_lo(u.w); f[7] += bf_hi(u.w);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = e ? fmaf(bf_lo(w[k]), kDown, f[2 * k]) : bf_lo(w[k]) * kDown;
+            f[2 * k + 1] = e ? fmaf(bf_hi(w[k]), kDown, f[2 * k + 1]) : bf_hi(w[k]) * kDown;
+          }
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += (double)f[k];
+      for (int k = 0; k < 8; ++k) acc[k] = a ? acc[k] + (double)f[k] : (double)f[k];
     }
 #pragma unroll
     for (int o = kGroup; o < 32; o <<= 1)
@@ -96,6 +99,7 @@ __device__ __forceinline__ void summarise(const SummaryParams &p, int h) {
   if (ch < D) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s += part[q][w][ch];
+    s *= 1.0 / kDown;
   }
   double top = isfinite(s) ? fabs(s) : (double)INFINITY;
 #pragma unroll

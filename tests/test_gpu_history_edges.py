@@ -420,3 +420,34 @@ def test_codes_beside_a_tiny_least_value_are_exact(d):
     for p, h, i in bad:                              # -0 and 0 are the same least value
         assert i >= PAGE * d and got[p, h, i] % 128 == want.data[p, h, i] % 128 == 0, (p, i)
     assert c.status.item() == 0
+
+
+# ---------------------------------------------------------------- block summaries
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_summaries_of_blocks_whose_sums_pass_fp32(d):
+    """Rows of 1e38: the sum of four passes fp32, the block's sum is finite in fp64,
+    with its codes, scale and mean; a block with an infinity has none."""
+    rng = np.random.default_rng(d)
+    n, H = 5 * PAGE + 17, 2
+    x = HC.bf16_round(rng.choice([-1e38, 1e38, 3e38], (1, H, n, d)) * rng.uniform(0.5, 1.0, (1, H, n, d)))
+    x[0, :, :, 3] = HC.bf16_round(rng.standard_normal((H, n)))
+    x[0, 1, 70, 5] = np.inf
+    op = dt.BlockSparseAttention(1, H, n, n, d, 2)
+    op.select(HC.up(x), HC.up(x))
+    torch.cuda.synchronize()
+    for h in range(H):
+        for size, codes, scale in ((PAGE, op.k_codes, op.k_scale), (dt.QBLOCK, op.q_codes, op.q_scale)):
+            for j in range(-(-n // size)):
+                rows = x[0, h, j * size:(j + 1) * size].astype(np.float64)
+                c, s, mean = OH.summary(rows)
+                got = codes[0, h, j].cpu().numpy().astype(int)
+                if not np.isfinite(rows).all():
+                    assert (got == 0).all() and scale[0, h, j].item() == 0
+                    continue
+                # (channel 3, of another size, is 0 beside the rest whatever its rounding)
+                assert (got == c).all() and scale[0, h, j].item() == s and s > 0, (h, size, j)
+                if size == PAGE:
+                    got = op.k_mean[0, h, j].cpu().numpy()
+                    assert np.isfinite(got).all()
+                    near = np.abs(got - mean) <= 2.0 ** -22 * np.abs(rows).mean(0)
+                    assert near.all(), (h, j, np.flatnonzero(~near))
