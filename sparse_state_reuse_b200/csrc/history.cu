@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   }
   // slots of the tokens
   const int total = off[p.R];
-  for (int t = blockIdx.x * kTabThreads + tid; t < p.max_tokens; t += gridDim.x * kTabThreads) {
+  for (long long at = blockIdx.x * kTabThreads + tid; at < p.max_tokens; at += gridDim.x * kTabThreads) {
+    const int t = (int)at;            // (past max_tokens, a step on, the index may pass 2^31)
     long long slot = -1;
     if (t < total) {
       int lo = 0, hi = p.R - 1;     // the last request that starts at or before t and is not empty
@@ -488,7 +489,7 @@ cudaError_t launch_block_tables(int R, int max_blocks, int max_tokens, int n_pag
                                 int *dev_status, int num_sms, cudaStream_t stream) {
   hist::TablesParams p{R, max_blocks, max_tokens, n_pages, n_free, ctx_len, new_len, free_pages,
                        block_table, kv_len, q_off, slot_map, pages_used, dev_status};
-  long long grid = (max_tokens + hist::kTabThreads - 1) / hist::kTabThreads;
+  long long grid = ((long long)max_tokens + hist::kTabThreads - 1) / hist::kTabThreads;
   if (grid < 1) grid = 1;
   if (grid > num_sms) grid = num_sms;
   hist::tables_kernel<<<(int)grid, hist::kTabThreads, 2 * (R + 1) * sizeof(int), stream>>>(p);

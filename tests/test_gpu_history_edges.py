@@ -451,3 +451,24 @@ def test_summaries_of_blocks_whose_sums_pass_fp32(d):
                     assert np.isfinite(got).all()
                     near = np.abs(got - mean) <= 2.0 ** -22 * np.abs(rows).mean(0)
                     assert near.all(), (h, j, np.flatnonzero(~near))
+
+
+# ---------------------------------------------------------------- large sizes
+def test_a_slot_map_of_two_to_the_31_places():
+    """As many token places as the argument can say: every one is written, and no
+    other word."""
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 * 2 ** 30:
+        pytest.skip("less than 24 GB free")
+    buf = torch.full((T + 2048,), 7, dtype=torch.int64, device="cuda")
+    slots = buf[1024:1024 + T]
+    table, free = ints([[5, 0, 0]]), ints([3, 1])
+    out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, 2, 1, 1)]
+    dt.ditango_block_tables(1, 3, T, 8, ints([10]), ints([100]), free, 2, table, out[0], out[1], slots, out[2], out[3])
+    torch.cuda.synchronize()
+    assert out[0].item() == 110 and out[1].tolist() == [0, 100] and out[2].item() == 1 and out[3].item() == 0
+    want = [5 * PAGE + p if p < PAGE else 3 * PAGE + p - PAGE for p in range(10, 110)]
+    assert slots[:100].tolist() == want
+    assert (buf[:1024] == 7).all() and (buf[1024 + T:] == 7).all()
+    for a in range(100, T, 2 ** 28):
+        assert (slots[a:min(T, a + 2 ** 28)] == -1).all()
