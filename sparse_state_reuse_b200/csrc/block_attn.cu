@@ -232,13 +232,16 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const bool leader = elect_one();
       constexpr uint32_t idesc_qk = idesc_bf16_f32(BM, BN, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
-      const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t dK = smem_desc_sw128(sK, 16, 1024);
-      const uint64_t dV = smem_desc_sw128(sV, C::CHUNK, 1024);   // MN-major: chunks of d are CHUNK apart
+      // V is MN-major: chunks of d are CHUNK apart
+      auto commit = [&](uint32_t at) {
+        at = pinned(at);
+        if (leader) tc_commit(at);
+      };
       bool ok = wait_warp(q_full, 0, ctl);
       for (int t = 0; t < T && ok; ++t) {
         if (!(ok = wait_warp(k_full, t & 1, ctl))) break;
         tc_fence_after();
+        const uint64_t dQ = pinned(smem_desc_sw128(sQ, 16, 1024)), dK = pinned(smem_desc_sw128(sK, 16, 1024));
         if (leader) {
           // S = Q K^T.  P of the tile before lives in S: its product was
           // issued before, and one thread's products run in order.
@@ -247,24 +250,26 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint64_t off = (uint64_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
             mma_ss(tmem, dQ + off, dK + off, idesc_qk, kk > 0);
           }
-          tc_commit(s_full);
-          tc_commit(k_empty);
         }
+        commit(s_full);
+        commit(k_empty);
         if (!(ok = wait_warp(v_full, t & 1, ctl))) break;
         if (!(ok = wait_warp(p_full, t & 1, ctl))) break;
         tc_fence_after();
+        const uint64_t dV = pinned(smem_desc_sw128(sV, C::CHUNK, 1024));
+        const uint32_t more = pinned(t > 0 ? 1u : 0u);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + 128, tmem + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, t > 0 || kk > 0);
-          tc_commit(v_empty);
-          if (t + 1 == T) tc_commit(o_full);
+            mma_ts(tmem + 128, tmem + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, kk > 0 ? 1u : more);
         }
+        commit(v_empty);
+        if (t + 1 == T) commit(o_full);
       }
       // what was issued ends before TMEM is released, on both paths
       volatile int never = 0;
       WaitCtl drain{&never, nullptr, 100000000LL};
-      if (!ok && leader) tc_commit(o_full);
+      if (!ok) commit(o_full);
       wait_bounded(o_full, 0, drain);
       __syncwarp();
     }

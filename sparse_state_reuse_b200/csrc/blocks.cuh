@@ -97,6 +97,19 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// A value that the compiler does not move or form again past this point.  What one
+// elected lane's tcgen05 instructions name (descriptors, barriers) is pinned by the
+// whole warp before that lane's branch: the instructions take it from uniform
+// registers, which a branch of one lane is no place to form.
+__device__ __forceinline__ uint32_t pinned(uint32_t x) {
+  asm volatile("mov.b32 %0, %0;" : "+r"(x));
+  return x;
+}
+__device__ __forceinline__ uint64_t pinned(uint64_t x) {
+  asm volatile("mov.b64 %0, %0;" : "+l"(x));
+  return x;
+}
+
 // Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(

@@ -589,31 +589,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
-      // The whole warp runs the loop; one elected lane issues and commits.  What
-      // a product or commit names (descriptors, barriers) is formed by the whole
-      // warp before that lane's branch, and kept from moving into it: these
-      // operands are uniform registers.
+      // The whole warp runs the loop; one elected lane issues and commits, what it
+      // names being pinned before its branch.
       const bool leader = elect_one();
       constexpr uint32_t idesc_qk = idesc_f16_f32(BM, BN, 0);
       constexpr uint32_t idesc_pv = idesc_f16_f32(BM, D, 1);
-      auto fix32 = [](uint32_t x) {
-        asm volatile("mov.b32 %0, %0;" : "+r"(x));
-        return x;
-      };
-      auto fix64 = [](uint64_t x) {
-        asm volatile("mov.b64 %0, %0;" : "+l"(x));
-        return x;
-      };
       auto commit = [&](uint32_t at) {
-        at = fix32(at);
+        at = pinned(at);
         if (leader) tc_commit(at);
       };
       auto qk = [&](int k, uint32_t n) {
-        const uint64_t a = fix64(smem_desc_sw128(sbase + C::OFF_Q + k * C::TILE, 16, 1024));
-        const uint64_t b = fix64(smem_desc_sw128(sbase + C::OFF_K + (n & 1) * C::TILE, 16, 1024));
-        const uint64_t qa = fix64(smem_desc_plain(sbase + C::OFF_QA + k * C::AUG, 128, 256));
-        const uint64_t ka = fix64(smem_desc_plain(sbase + C::OFF_KA + (n & 1) * C::AUG, 128, 256));
-        const uint32_t full = fix32(s_full(k));
+        const uint64_t a = pinned(smem_desc_sw128(sbase + C::OFF_Q + k * C::TILE, 16, 1024));
+        const uint64_t b = pinned(smem_desc_sw128(sbase + C::OFF_K + (n & 1) * C::TILE, 16, 1024));
+        const uint64_t qa = pinned(smem_desc_plain(sbase + C::OFF_QA + k * C::AUG, 128, 256));
+        const uint64_t ka = pinned(smem_desc_plain(sbase + C::OFF_KA + (n & 1) * C::AUG, 128, 256));
+        const uint32_t full = pinned(s_full(k));
         // S_k = Q_k K^T.  P of the tile before lives in S_k: its product was
         // issued before, and one thread's products run in order.
         if (leader) {
@@ -627,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
         }
       };
       auto pv = [&](int k, uint32_t n, bool acc, uint32_t idesc) {
-        const uint64_t b = fix64(smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024));
-        const uint32_t accumulate = fix32(acc ? 1u : 0u);
+        const uint64_t b = pinned(smem_desc_sw128(sbase + C::OFF_V + (n & 1) * C::TILE, C::CHUNK, 1024));
+        const uint32_t accumulate = pinned(acc ? 1u : 0u);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
@@ -657,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
           if (!(ok = wait_warp(v_full(n), (n >> 1) & 1, ctl))) break;
           uint32_t kind = idesc_pv;
           if (FAR && (tiles[n % kRing].flags & kWideV)) kind |= kBothBf16;
-          kind = fix32(kind);
+          kind = pinned(kind);
           if (!(ok = wait_warp(p_full(0), n & 1, ctl))) break;
           tc_fence_after();
           pv(0, n, t > 0, kind);
