@@ -23,9 +23,6 @@
 // under the power limit, 1180 and 1060 to 1120 TFLOP/s (65 to 73% of the measured
 // bf16 rate; the dense kernel of this library reaches 67%).  Register splits of
 // 192/64 and 208/48 were slower or the same.
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "blocks.cuh"
 
@@ -557,23 +554,19 @@ template <int D, bool SPLIT>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int B,
                    cudaStream_t stream) {
   auto kfn = block_attn_kernel<D, SPLIT>;
-  static std::mutex mu;
-  static std::set<int> ready;
+  static OnDevices ready;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready.count(dev)) {
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kfn);
-      if (e != cudaSuccess) return e;
-      // another count would leave setmaxnreg waiting for registers that do not come
-      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-      if (e != cudaSuccess) return e;
-      ready.insert(dev);
-    }
+  if (!ready.has(dev)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kfn);
+    if (e != cudaSuccess) return e;
+    // another count would leave setmaxnreg waiting for registers that do not come
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.add(dev);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.n_q * p.split), (unsigned)p.H, (unsigned)B);

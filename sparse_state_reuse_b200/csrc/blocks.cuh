@@ -11,6 +11,8 @@
 // contiguous run, so that a kernel fetches it with one bulk copy.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace ditango {
@@ -37,6 +39,20 @@ struct FastDiv {
 #ifdef __CUDACC__
   __device__ __forceinline__ uint32_t div(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
 #endif
+};
+
+// The devices on which a kernel's attributes have been set.  Neither a lock nor an
+// allocation, whose failure would end in an exception at a C entry: two threads may
+// both set them, which does no harm.
+class OnDevices {
+ public:
+  bool has(int dev) const { return dev < 64 && (bits_.load(std::memory_order_acquire) >> dev & 1u); }
+  void add(int dev) {
+    if (dev < 64) bits_.fetch_or(1ull << dev, std::memory_order_release);
+  }
+
+ private:
+  std::atomic<unsigned long long> bits_{0};
 };
 
 #ifdef __CUDACC__

@@ -37,9 +37,6 @@
 // after the start (lengths, page numbers and the copy follow one another), and the
 // join of the parts takes the last 4 us.  Reading Q before the pages, which shortens
 // its own wait, delays the copies as much (59 us).
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "history_attn.cuh"
 
@@ -699,26 +696,21 @@ template <int D, int NR, int E>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
   auto kfn = kv4_attn_kernel<D, NR, E>;
   constexpr int bytes = Smem<D>::kBytes;
-  static std::mutex mu;
-  static std::set<int> ready;
-  static int per_sm = 1;
+  static OnDevices ready;
+  static std::atomic<int> per_sm{1};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int blocks;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready.count(dev)) {
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (e != cudaSuccess) return e;
-      int n = 1;
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kfn, kThreads, bytes);
-      if (e != cudaSuccess) return e;
-      per_sm = n < 1 ? 1 : n;
-      ready.insert(dev);
-    }
-    blocks = per_sm * num_sms;
+  if (!ready.has(dev)) {
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    int n = 1;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kfn, kThreads, bytes);
+    if (e != cudaSuccess) return e;
+    per_sm.store(n < 1 ? 1 : n);
+    ready.add(dev);
   }
+  int blocks = per_sm.load() * num_sms;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   kfn<<<blocks, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();

@@ -49,8 +49,6 @@
 // under the other's softmax, took away most of the wait for S but make Q K^T twice
 // as dear (64 columns do not fill the tensor pipe) and crowd the exponentials:
 // 1.32 ms.
-#include <mutex>
-#include <set>
 
 #include <cuda_fp16.h>
 
@@ -1049,23 +1047,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
 template <int D, Sizes SIZES>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
   auto kfn = kv4_chunk_kernel<D, SIZES>;
-  static std::mutex mu;
-  static std::set<int> ready;
+  static OnDevices ready;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready.count(dev)) {
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kfn);
-      if (e != cudaSuccess) return e;
-      // another count would leave setmaxnreg waiting for registers that do not come
-      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-      if (e != cudaSuccess) return e;
-      ready.insert(dev);
-    }
+  if (!ready.has(dev)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kfn);
+    if (e != cudaSuccess) return e;
+    // another count would leave setmaxnreg waiting for registers that do not come
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.add(dev);
   }
   const int blocks = num_sms < kMaxBlocks ? num_sms : kMaxBlocks;
   kfn<<<blocks, kThreads, Cfg<D>::SMEM, stream>>>(p);

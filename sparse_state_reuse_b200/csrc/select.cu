@@ -7,8 +7,6 @@
 // with q_i . k_j a sum of products of 8-bit codes: a whole number, which every
 // order of summation gives alike.  The fp32 operations around it have one
 // order, so that a selection is a function of its inputs down to the last bit.
-#include <mutex>
-#include <set>
 
 #include "blocks.cuh"
 
@@ -609,18 +607,14 @@ int row_stride(int n_k) { return (n_k + 8 - 1) / 8 * 8 + (40 - (n_k + 7) / 8 * 8
 template <int D, int REG, bool HEADS>
 cudaError_t launch_select(const SelectParams &p, int B, int bytes, cudaStream_t stream) {
   auto kfn = block_select_kernel<D, REG, HEADS>;
-  static std::mutex mu;
-  static std::set<int> ready;
+  static OnDevices ready;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready.count(dev)) {
-      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxScoreBytes);
-      if (e != cudaSuccess) return e;
-      ready.insert(dev);
-    }
+  if (!ready.has(dev)) {
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxScoreBytes);
+    if (e != cudaSuccess) return e;
+    ready.add(dev);
   }
   const dim3 grid((unsigned)(HEADS ? 1 : (p.n_q + p.rows - 1) / p.rows), (unsigned)p.Hkv, (unsigned)B);
   kfn<<<grid, kSelThreads<HEADS>, bytes, stream>>>(p);
