@@ -125,7 +125,7 @@ def status_string(s: int) -> str:
 
 def _ptr(x):
     """Device address of a tensor (or an address given as an int)."""
-    if x is None or x.__class__ is int:
+    if x is None or isinstance(x, int):
         return x
     if getattr(x, "is_cuda", True) is False:
         # a host tensor's address would be dereferenced by a kernel
