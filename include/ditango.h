@@ -489,6 +489,7 @@ size_t ditango_kv4_attn_workspace_size(int32_t d);
  * Query head h reads key head h / (H / Hkv).
  *   T, max_q     rows of Q, and a bound on the new tokens of one request (it
  *                chooses the kernel; a bound that is too small costs time only).
+ *                Nothing is done for T = 0.
  *   Q            dev bf16 [T][H][d], (token, head) element strides, multiples
  *                of 8, 16-byte aligned.
  *   q_off, kv_len, block_table   as ditango_block_tables leaves them.

@@ -854,7 +854,7 @@ ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int3
   NvtxRange nvtx_range("ditango_kv4_attn");
   const ditango_status st = check_kv4(c);
   if (st != DITANGO_OK) return st;
-  if (R < 1 || H < 1 || H % c->Hkv || T < 0 || max_q < 1 || max_blocks < 1) return DITANGO_ERR_INVALID;
+  if (R < 1 || H < 1 || H % c->Hkv || T < 0 || max_q < (T > 0 ? 1 : 0) || max_blocks < 1) return DITANGO_ERR_INVALID;
   if (!q_strides || !q_off || !kv_len || !block_table) return DITANGO_ERR_INVALID;
   if ((sel == nullptr) != (sel_count == nullptr) || (sel && max_sel < 1)) return DITANGO_ERR_INVALID;
   if (!(scale >= 0.f) || !std::isfinite(scale)) return DITANGO_ERR_INVALID;
