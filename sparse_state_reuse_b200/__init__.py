@@ -297,6 +297,12 @@ def _need(t, name, shape, dtypes, device, contiguous=False):
     raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
 
 
+def _width(lists):
+    """The last dimension of lists, whose length the caller chooses (at least 1)."""
+    shape = getattr(lists, "shape", ())
+    return max(shape[-1], 1) if len(shape) else 1
+
+
 class KV4Cache:
     """A paged history of keys and values in 4 bits, and attention over it.
 
@@ -472,7 +478,7 @@ class KV4Cache:
             raise ValueError("sel and sel_count go together")
         room = 0
         if sel is not None:
-            room = sel.shape[-1]
+            room = _width(sel)
             _need(sel, "sel", (self.n_requests, self.Hkv, room), (torch.int32,), dev, contiguous=True)
             _need(sel_count, "sel_count", (self.n_requests, self.Hkv), (torch.int32,), dev, contiguous=True)
         run = self._run
@@ -571,7 +577,7 @@ class BlockSparseAttention:
         if sel is None:
             sel, sel_count = self.sel, self.sel_count
         else:
-            _need(sel, "sel", (B, Hkv, self.n_q, sel.shape[-1]), (torch.int32,), dev, contiguous=True)
+            _need(sel, "sel", (B, Hkv, self.n_q, _width(sel)), (torch.int32,), dev, contiguous=True)
             _need(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), dev, contiguous=True)
         self._check_len(k_len)
         run = self._run

@@ -31,3 +31,32 @@ def test_attention_of_no_rows_does_nothing():
         with pytest.raises(dt.DitangoError) as e:
             dt.ditango_kv4_attn(dt.kv4(4, 2, 64, A), stream=0, **{**a, **kw})
         assert e.value.status == 1
+
+
+def on_the_host(cls, **attrs):
+    """An object whose buffers would be on the CPU: the checks run, and a launch fails the test."""
+    def launch(*a):
+        raise AssertionError("reached the library")
+
+    o = cls.__new__(cls)
+    o.__dict__.update(dict(device=torch.device("cpu"), _run=launch), **attrs)
+    return o
+
+
+BAD_LISTS = [([[1, 2]], TypeError), (torch.tensor(3), TypeError), (torch.zeros((2, 2, 3)), TypeError),
+             (torch.zeros((2, 2, 0), dtype=torch.int32), ValueError),
+             (torch.zeros((2, 3, 3), dtype=torch.int32), ValueError), (5, TypeError)]
+
+
+@pytest.mark.parametrize("sel,error", BAD_LISTS)
+def test_lists_that_are_no_lists_are_refused(sel, error):
+    c = on_the_host(dt.KV4Cache, H=4, Hkv=2, d=64, n_requests=2)
+    Q, count = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 2), dtype=torch.int32)
+    with pytest.raises(error, match="sel"):
+        c.attend(Q, torch.zeros_like(Q), sel=sel, sel_count=count)
+    b = on_the_host(dt.BlockSparseAttention, B=2, H=4, Hkv=2, Nq=100, Nk=70, d=64, n_q=1)
+    Q, K = (torch.zeros((2, h, n, 64), dtype=torch.bfloat16) for h, n in ((4, 100), (2, 70)))
+    if isinstance(sel, torch.Tensor) and sel.dim() == 3:
+        sel = sel[:, :, None]
+    with pytest.raises(error, match="sel"):
+        b.attend(Q, K, K, torch.zeros_like(Q), sel=sel, sel_count=count[..., None])
