@@ -605,6 +605,20 @@ ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq,
                                   int32_t out_is_fp32, const int64_t *out_strides,
                                   float *out_lse, int32_t *dev_status, ditango_stream stream);
 
+/* The same with (b, h, n) element strides of out_lse (NULL: packed), so that O and
+ * lse may be a slot of a state buffer, [B * H][Lmax], and merge with the
+ * partitions' states. */
+ditango_status ditango_block_attn_strided(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk,
+                                          int32_t d, const uint16_t *Q, const uint16_t *K,
+                                          const uint16_t *V, const int64_t q_strides[3],
+                                          const int64_t k_strides[3], const int64_t v_strides[3],
+                                          const int32_t *sel, const int32_t *sel_count,
+                                          int32_t max_sel, const int32_t *k_len, float scale,
+                                          void *out, int32_t out_is_fp32,
+                                          const int64_t *out_strides, float *out_lse,
+                                          const int64_t *lse_strides, int32_t *dev_status,
+                                          ditango_stream stream);
+
 /* Time limit, in nanoseconds, of every wait inside the kernels (default
  * 1e9).  Process-wide; read at each launch. */
 void ditango_set_wait_limit_ns(int64_t ns);

@@ -297,6 +297,15 @@ def _need(t, name, shape, dtypes, device, contiguous=False):
     raise ValueError(f"{name}: on {t.device}, the buffers are on {device}")
 
 
+def _lse(t, shape, device):
+    """A float32 tensor of this shape and any strides."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError("out_lse: a float32 tensor is required")
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"out_lse: a tensor of shape {tuple(shape)} on {device} is required")
+
+
 def _width(lists):
     """The last dimension of lists, whose length the caller chooses (at least 1)."""
     shape = getattr(lists, "shape", ())
@@ -470,10 +479,7 @@ class KV4Cache:
         _need(Q, "Q", shape, (torch.bfloat16,), dev)
         _need(out, "out", shape, (torch.bfloat16, torch.float32), dev)
         if out_lse is not None:
-            if not isinstance(out_lse, torch.Tensor) or out_lse.dtype != torch.float32:
-                raise TypeError("out_lse: a float32 tensor is required")
-            if out_lse.shape != (T, self.H) or out_lse.device != dev:
-                raise ValueError(f"out_lse: a tensor of shape {(T, self.H)} on {dev} is required")
+            _lse(out_lse, (T, self.H), dev)
         if (sel is None) != (sel_count is None):
             raise ValueError("sel and sel_count go together")
         room = 0
@@ -562,7 +568,9 @@ class BlockSparseAttention:
     def attend(self, Q, K, V, out, out_lse=None, sel=None, sel_count=None, k_len=None, scale=0.0,
                stream=None):
         """O (and lse [B, H, Nq]) of every query block over its listed key
-        blocks: the object's lists, or sel [B, Hkv, n_q, any] and sel_count."""
+        blocks: the object's lists, or sel [B, Hkv, n_q, any] and sel_count.
+        out and out_lse may be strided views, such as a slot of a
+        PartitionedAttention's state buffer."""
         import torch
         B, H, Hkv, Nq, d = self.B, self.H, self.Hkv, self.Nq, self.d
         dev, bf16 = self.device, (torch.bfloat16,)
@@ -571,7 +579,7 @@ class BlockSparseAttention:
         _need(V, "V", (B, Hkv, self.Nk, d), bf16, dev)
         _need(out, "out", (B, H, Nq, d), (torch.float32, torch.bfloat16), dev)
         if out_lse is not None:
-            _need(out_lse, "out_lse", (B, H, Nq), (torch.float32,), dev, contiguous=True)
+            _lse(out_lse, (B, H, Nq), dev)
         if (sel is None) != (sel_count is None):
             raise ValueError("sel and sel_count go together")
         if sel is None:
@@ -581,10 +589,11 @@ class BlockSparseAttention:
             _need(sel_count, "sel_count", (B, Hkv, self.n_q), (torch.int32,), dev, contiguous=True)
         self._check_len(k_len)
         run = self._run
-        run("ditango_block_attn", stream, B, H, Hkv, Nq, self.Nk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+        run("ditango_block_attn_strided", stream, B, H, Hkv, Nq, self.Nk, d, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
             run.strides(Q, 3), run.strides(K, 3), run.strides(V, 3), sel.data_ptr(), sel_count.data_ptr(),
             sel.shape[-1], _addr(k_len), scale, out.data_ptr(), 1 if out.dtype == torch.float32 else 0,
-            run.strides(out, 3), _addr(out_lse), self.status.data_ptr())
+            run.strides(out, 3), _addr(out_lse), None if out_lse is None else run.strides(out_lse, 3),
+            self.status.data_ptr())
 
     def step(self, Q, K, V, out, out_lse=None, k_len=None, scale=0.0, stream=None):
         """select, then attend."""

@@ -106,6 +106,8 @@ _SIGS = {
     "ditango_block_select": (C.c_int, [C.c_int32] * 11 + [_P] * 5 + [C.c_int32] + [_P] * 5),
     "ditango_block_attn": (C.c_int, [C.c_int32] * 6 + [_P] * 8 + [C.c_int32, _P, C.c_float, _P,
                                      C.c_int32, _P, _P, _P, _P]),
+    "ditango_block_attn_strided": (C.c_int, [C.c_int32] * 6 + [_P] * 8 + [C.c_int32, _P, C.c_float, _P,
+                                             C.c_int32, _P, _P, _P, _P, _P]),
     "ditango_set_wait_limit_ns": (None, [C.c_int64]),
     "ditango_checked_build": (C.c_int32, []),
     "ditango_check_status": (C.c_int, [_P, C.c_int32]),
@@ -420,9 +422,10 @@ def ditango_block_select(B, H, Hkv, n_q, n_k, d, k, band, sink, own_blocks, max_
 
 def ditango_block_attn(B, H, Hkv, Nq, Nk, d, Q, K, V, q_strides, k_strides, v_strides, sel, sel_count,
                        max_sel, out, out_is_fp32, out_strides=None, out_lse=None, k_len=None, scale=0.0,
-                       dev_status=None, stream=None):
+                       dev_status=None, stream=None, lse_strides=None):
     """Attention of every query block over its listed key blocks."""
-    _check("ditango_block_attn", _lib.ditango_block_attn(
+    _check("ditango_block_attn", _lib.ditango_block_attn_strided(
         B, H, Hkv, Nq, Nk, d, _ptr(Q), _ptr(K), _ptr(V), _i64s(q_strides), _i64s(k_strides),
         _i64s(v_strides), _ptr(sel), _ptr(sel_count), max_sel, _ptr(k_len), scale, _ptr(out),
-        int(bool(out_is_fp32)), _i64s(out_strides), _ptr(out_lse), _ptr(dev_status), _stream(stream)))
+        int(bool(out_is_fp32)), _i64s(out_strides), _ptr(out_lse), _i64s(lse_strides),
+        _ptr(dev_status), _stream(stream)))

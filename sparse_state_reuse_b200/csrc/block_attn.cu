@@ -60,7 +60,8 @@ struct Params {
   void *out;
   int out_fp32;
   long long osb, osh, osn;
-  float *out_lse;                    // [B, H, Nq] or null
+  float *out_lse;                    // (b, h, n) strides below, or null
+  long long lsb, lsh, lsn;
   int *dev_status;
   long long wait_limit_ns;
   int split;                         // blocks of threads of a query block (a cluster)
@@ -474,7 +475,7 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + to) =
               make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
         if (ch == 0 && p.out_lse)
-          p.out_lse[((size_t)b * p.H + h) * p.Nq + at] =
+          p.out_lse[b * p.lsb + h * p.lsh + at * p.lsn] =
               lt[w] > 0.f ? (mt[w] + __log2f(lt[w])) * 0.69314718055994531f : (lt[w] == lt[w] ? -INFINITY : lt[w]);
       }
     }
@@ -543,7 +544,7 @@ block_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       __syncwarp();
     }
     if (p.out_lse && (r & 31) < rows)
-      p.out_lse[((size_t)b * p.H + h) * p.Nq + i * BM + r] =
+      p.out_lse[b * p.lsb + h * p.lsh + (long long)(i * BM + r) * p.lsn] =
           l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994531f : (l == l ? -INFINITY : l);
   }
   tc_fence_before();
@@ -593,8 +594,8 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B, int H,
                               int Hkv, int Nq, int Nk, int d, const int *sel, const int *count, int room,
                               const int *k_len, float scale, void *out, int out_fp32, const long long *os,
-                              float *out_lse, int *dev_status, long long wait_limit_ns, int num_sms,
-                              cudaStream_t stream) {
+                              float *out_lse, const long long *ls, int *dev_status, long long wait_limit_ns,
+                              int num_sms, cudaStream_t stream) {
   battn::Params p;
   p.H = H;
   p.G = H / Hkv;
@@ -614,6 +615,9 @@ cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, cons
   p.osh = os[1];
   p.osn = os[2];
   p.out_lse = out_lse;
+  p.lsb = ls[0];
+  p.lsh = ls[1];
+  p.lsn = ls[2];
   p.dev_status = dev_status;
   p.wait_limit_ns = wait_limit_ns;
   // Few query blocks leave SMs (two blocks each) without work: their lists are cut

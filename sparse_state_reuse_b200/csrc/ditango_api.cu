@@ -77,8 +77,9 @@ cudaError_t launch_block_select(int B, int H, int Hkv, int n_q, int n_k, int d, 
 cudaError_t launch_block_attn(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int B,
                               int H, int Hkv, int Nq, int Nk, int d, const int *sel, const int *count,
                               int room, const int *k_len, float scale, void *out, int out_fp32,
-                              const long long *os, float *out_lse, int *dev_status,
-                              long long wait_limit_ns, int num_sms, cudaStream_t stream);
+                              const long long *os, float *out_lse, const long long *ls,
+                              int *dev_status, long long wait_limit_ns, int num_sms,
+                              cudaStream_t stream);
 cudaError_t attn_check_status(int *out, bool reset);
 cudaError_t merge_check_status(int *out, bool reset);
 }  // namespace ditango
@@ -288,7 +289,7 @@ ditango_status cuda_status(cudaError_t e) {
 
 extern "C" {
 
-int32_t ditango_version(void) { return 10300; }
+int32_t ditango_version(void) { return 10400; }
 
 const char *ditango_status_string(int32_t s) {
   switch (s) {
@@ -944,6 +945,20 @@ ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq,
                                   int32_t max_sel, const int32_t *k_len, float scale, void *out,
                                   int32_t out_is_fp32, const int64_t *out_strides, float *out_lse,
                                   int32_t *dev_status, ditango_stream stream) {
+  return ditango_block_attn_strided(B, H, Hkv, Nq, Nk, d, Q, K, V, q_strides, k_strides, v_strides, sel,
+                                    sel_count, max_sel, k_len, scale, out, out_is_fp32, out_strides, out_lse,
+                                    nullptr, dev_status, stream);
+}
+
+ditango_status ditango_block_attn_strided(int32_t B, int32_t H, int32_t Hkv, int32_t Nq, int32_t Nk, int32_t d,
+                                          const uint16_t *Q, const uint16_t *K, const uint16_t *V,
+                                          const int64_t q_strides[3], const int64_t k_strides[3],
+                                          const int64_t v_strides[3], const int32_t *sel,
+                                          const int32_t *sel_count, int32_t max_sel, const int32_t *k_len,
+                                          float scale, void *out, int32_t out_is_fp32,
+                                          const int64_t *out_strides, float *out_lse,
+                                          const int64_t *lse_strides, int32_t *dev_status,
+                                          ditango_stream stream) {
   NvtxRange nvtx_range("ditango_block_attn");
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || Nq < 1 || Nk < 1 || d < 1 || max_sel < 1)
     return DITANGO_ERR_INVALID;
@@ -983,13 +998,21 @@ ditango_status ditango_block_attn(int32_t B, int32_t H, int32_t Hkv, int32_t Nq,
   const int esz = out_is_fp32 ? 4 : 2;
   for (int a = 0; a < 3; ++a)
     if (os[a] <= 0 || (os[a] * esz) % 16) return DITANGO_ERR_INVALID;
+  long long ls[3] = {(long long)H * Nq, Nq, 1};
+  if (lse_strides) {
+    const int size[3] = {B, H, Nq};
+    for (int a = 0; a < 3; ++a) {
+      ls[a] = lse_strides[a];
+      if (size[a] > 1 && ls[a] <= 0) return DITANGO_ERR_INVALID;
+    }
+  }
   if (scale == 0.f) scale = 1.f / std::sqrt((float)d);
   CUtensorMap tq, tk, tv;
   if (!make_qkv_map(&tq, Q, gq, qs, DITANGO_QBLOCK) || !make_qkv_map(&tk, K, gk, ks, DITANGO_PAGE) ||
       !make_qkv_map(&tv, V, gk, vs, DITANGO_PAGE))
     return DITANGO_ERR_CUDA;
   return cuda_status(launch_block_attn(tq, tk, tv, B, H, Hkv, Nq, Nk, d, sel, sel_count, max_sel, k_len,
-                                       scale, out, out_is_fp32 ? 1 : 0, os, out_lse, dev_status,
+                                       scale, out, out_is_fp32 ? 1 : 0, os, out_lse, ls, dev_status,
                                        g_wait_limit_ns.load(), num_sms_current(),
                                        static_cast<cudaStream_t>(stream)));
 }

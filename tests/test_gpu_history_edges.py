@@ -472,3 +472,46 @@ def test_a_slot_map_of_two_to_the_31_places():
     assert (buf[:1024] == 7).all() and (buf[1024 + T:] == 7).all()
     for a in range(100, T, 2 ** 28):
         assert (slots[a:min(T, a + 2 ** 28)] == -1).all()
+
+
+# ---------------------------------------------------------------- states of block attention
+@pytest.mark.parametrize("n1", [200, 333])
+def test_a_state_over_selected_blocks_merges_with_the_partitions_states(n1):
+    """Partition 1's queries over listed blocks of partition 0's keys, written into
+    their slot of the state buffer (whose rows are more than the queries where
+    n1 < n0), and the partition's own, fresh: the merge joins them."""
+    rng = np.random.default_rng(n1)
+    B, H, d, n0 = 2, 2, 128, 320
+    pa = dt.PartitionedAttention(B, H, n0 + n1, d, [0, n0, n0 + n1])
+    qkv = [normal(rng, B, H, n0 + n1, d) for _ in range(3)]
+    Q, K, V = (HC.up(x) for x in qkv)
+    pa.plan.copy_(torch.tensor([0, 0, 2, 1], dtype=torch.int8))      # (1, 0) reused, (1, 1) fresh
+    pa.fresh_list[0] = 3
+    pa.counts.copy_(ints([1, 1]))
+    slot = dt.ditango_slot_table(pa.geom)[1]
+    pa.partial(Q, K, V)
+    pa.state_O[slot[0]] = 7.0
+    pa.state_lse[slot[0]] = 7.0
+    op = dt.BlockSparseAttention(B, H, n1, n0, d, 4)
+    lists = [[[sorted(rng.choice(5, 3, replace=False).tolist()) for _ in range(op.n_q)] for _ in range(H)]
+             for _ in range(B)]
+    O = pa.state_O[slot[0]].view(B, H, pa.Lmax, d)[:, :, :n1]
+    lse = pa.state_lse[slot[0]].view(B, H, pa.Lmax)[:, :, :n1]
+    op.attend(Q[:, :, n0:], K[:, :, :n0], V[:, :, :n0], O, lse, ints(lists), torch.full_like(op.sel_count, 3))
+    out = torch.empty((B, H, n0 + n1, d), device="cuda")
+    out_lse = torch.empty((B, H, n0 + n1), device="cuda")
+    pa.merge(out, out_lse)
+    torch.cuda.synchronize()
+    assert pa.status.item() == 0 and op.status.item() == 0
+    assert (pa.state_lse[slot[0]][:, n1:] == 7).all() and (pa.state_O[slot[0]][:, n1:] == 7).all()
+    for b in range(B):
+        for h in range(H):
+            for i in range(op.n_q):
+                at = np.concatenate([np.arange(j * PAGE, (j + 1) * PAGE) for j in lists[b][h][i]]
+                                    + [np.arange(n0, n0 + n1)])
+                rows = np.arange(n0 + i * dt.QBLOCK, min(n0 + n1, n0 + (i + 1) * dt.QBLOCK))
+                q, k, v = (x[b, h].astype(np.float64) for x in qkv)
+                o, e, P = OH.attend_rows(q[rows], k[at], v[at], d ** -0.5)
+                HC.check(out[b, h, rows].cpu().numpy().astype(np.float64),
+                         out_lse[b, h, rows].cpu().numpy().astype(np.float64), o, e, P, v[at], v[at],
+                         HC.logit_bound(q[rows], np.abs(k[at]), d ** -0.5, d), False, (b, h, i))

@@ -60,3 +60,19 @@ def test_lists_that_are_no_lists_are_refused(sel, error):
         sel = sel[:, :, None]
     with pytest.raises(error, match="sel"):
         b.attend(Q, K, K, torch.zeros_like(Q), sel=sel, sel_count=count[..., None])
+
+
+def test_block_attention_refuses_strides_of_lse_that_lie_on_one_another():
+    s = (64 * 640, 640, 64)
+    a = dict(B=1, H=2, Hkv=1, Nq=10, Nk=10, d=64, Q=A, K=2 * A, V=3 * A, q_strides=s, k_strides=s, v_strides=s,
+             sel=A, sel_count=A, max_sel=2, out=8 * A, out_is_fp32=0, out_lse=9 * A)
+    for strides in ((20, 0, 1), (20, 10, 0), (20, -10, 1)):
+        with pytest.raises(dt.DitangoError) as e:
+            dt.ditango_block_attn(lse_strides=strides, stream=0, **a)
+        assert e.value.status == 1
+    b = on_the_host(dt.BlockSparseAttention, B=2, H=4, Hkv=2, Nq=100, Nk=70, d=64, n_q=1, status=None)
+    Q, K = (torch.zeros((2, h, n, 64), dtype=torch.bfloat16) for h, n in ((4, 100), (2, 70)))
+    for lse, error in ((torch.zeros((2, 4, 100), dtype=torch.bfloat16), TypeError), (7, TypeError),
+                       (torch.zeros((2, 4, 99)), ValueError)):
+        with pytest.raises(error, match="out_lse"):
+            b.attend(Q, K, K, torch.zeros_like(Q), lse)
