@@ -331,10 +331,21 @@ class KV4Cache:
     request that did not fit or a page number out of range.  The buffers are
     one batch's: calls that may overlap on the GPU need objects of their own.
     data and block_table may be given (a cache that already exists).
+
+    The layers of a model have pages of their own and one batch: `like`, an
+    object of the same sizes, lends its tables, lengths, slots, status, and
+    scratch, so that tables() is called once, on any of them.  Their calls must
+    follow one another (one stream).
+
+    tables() takes pages from free_pages[0] on, in a replayed graph too.  Before
+    the next step the taken ones go to the end, without a look at pages_used:
+
+        n = torch.arange(len(free), device=free.device)     # kept
+        free.copy_(free[(n + cache.pages_used) % len(free)])
     """
 
     def __init__(self, n_pages, Hkv, d, max_requests, max_blocks, max_tokens, H=None, device="cuda",
-                 data=None, block_table=None):
+                 data=None, block_table=None, like=None):
         import torch
         for name, v in (("n_pages", n_pages), ("Hkv", Hkv), ("max_requests", max_requests),
                         ("max_blocks", max_blocks), ("max_tokens", max_tokens)):
@@ -345,7 +356,21 @@ class KV4Cache:
         H = Hkv if H is None else H
         if H < 1 or H % Hkv:
             raise ValueError(f"{H} query heads are not a multiple of {Hkv} key heads")
+        if like is not None:
+            if not isinstance(like, KV4Cache):
+                raise TypeError(f"like: a KV4Cache is required, got {type(like).__name__}")
+            sizes = (Hkv, H, d, max_requests, max_blocks, max_tokens)
+            if sizes != (like.Hkv, like.H, like.d, like.max_requests, like.max_blocks, like.max_tokens):
+                raise ValueError("like: an object of the same heads, dimension, requests, blocks and tokens")
+            if n_pages < like.n_pages:
+                raise ValueError(f"{n_pages} pages, the tables of `like` hold numbers up to {like.n_pages}")
+            if block_table is not None:
+                raise ValueError("like and block_table exclude each other")
+            block_table = like.block_table
+            device = like.device
         dev = torch.device(device if data is None else data.device)
+        if like is not None and dev != like.device:
+            raise ValueError(f"data: on {dev}, the buffers of `like` are on {like.device}")
         if dev.type != "cuda":
             raise ValueError(f"the history lives on a CUDA device, not {dev}")
         if dev.index is None:
@@ -353,7 +378,8 @@ class KV4Cache:
         self.device = dev
         self.n_pages, self.Hkv, self.H, self.d = n_pages, Hkv, H, d
         self.max_requests, self.max_blocks, self.max_tokens = max_requests, max_blocks, max_tokens
-        self.n_requests = max_requests     # requests of the last tables() call
+        # requests of the last tables() call
+        self._batch = {"requests": max_requests} if like is None else like._batch
         shape = (n_pages, Hkv, PAGE * (d + 8))
         if data is None:
             data = torch.zeros(shape, dtype=torch.uint8, device=dev)
@@ -366,24 +392,37 @@ class KV4Cache:
         else:
             _need(block_table, "block_table", shape, (torch.int32,), dev, contiguous=True)
         self.block_table = block_table
-        i32 = dict(dtype=torch.int32, device=dev)
-        self.kv_len = torch.zeros(max_requests, **i32)
-        self.q_off = torch.zeros(max_requests + 1, **i32)
-        self.slot_map = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
-        self.pages_used = torch.zeros(1, **i32)
-        self.status = torch.zeros(1, **i32)
         self.sum_codes = torch.zeros((n_pages, Hkv, d), dtype=torch.int8, device=dev)
         self.sum_scale = torch.zeros((n_pages, Hkv), dtype=torch.float32, device=dev)
-        # the attention's partial states and counters (each launch leaves the counters at zero)
-        self.ws_bytes = ditango_kv4_attn_workspace_size(d)
-        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
-        # room for the single tokens' 8-bit codes, for select()
-        self._q_codes = torch.empty((max_requests, H, d), dtype=torch.int8, device=dev)
-        self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
-        self._lists = {}
+        if like is not None:
+            for name in ("kv_len", "q_off", "slot_map", "pages_used", "status", "ws_bytes", "workspace",
+                         "_q_codes", "_q_scale", "_lists"):
+                setattr(self, name, getattr(like, name))
+        else:
+            i32 = dict(dtype=torch.int32, device=dev)
+            self.kv_len = torch.zeros(max_requests, **i32)
+            self.q_off = torch.zeros(max_requests + 1, **i32)
+            self.slot_map = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
+            self.pages_used = torch.zeros(1, **i32)
+            self.status = torch.zeros(1, **i32)
+            # the attention's partial states and counters (each launch leaves the counters at zero)
+            self.ws_bytes = ditango_kv4_attn_workspace_size(d)
+            self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
+            # room for the single tokens' 8-bit codes, for select()
+            self._q_codes = torch.empty((max_requests, H, d), dtype=torch.int8, device=dev)
+            self._q_scale = torch.empty((max_requests, H), dtype=torch.float32, device=dev)
+            self._lists = {}
         self.kv = kv4(n_pages, Hkv, d, self.data)
         self._run = _Launcher(dev)
         self._kv = _abi.C.byref(self.kv)
+
+    @property
+    def n_requests(self):
+        return self._batch["requests"]
+
+    @n_requests.setter
+    def n_requests(self, n):
+        self._batch["requests"] = n
 
     def _lengths(self, name, t, n=None):
         import torch

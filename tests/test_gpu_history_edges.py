@@ -515,3 +515,70 @@ def test_a_state_over_selected_blocks_merges_with_the_partitions_states(n1):
                 HC.check(out[b, h, rows].cpu().numpy().astype(np.float64),
                          out_lse[b, h, rows].cpu().numpy().astype(np.float64), o, e, P, v[at], v[at],
                          HC.logit_bound(q[rows], np.abs(k[at]), d ** -0.5, d), False, (b, h, i))
+
+
+# ---------------------------------------------------------------- layers, and the free list
+def test_layers_share_one_batch_and_the_free_list_goes_on_in_a_graph():
+    """Two layers' pages over one object's tables, against objects of their own;
+    decode steps as replays of one graph, the free list turned on the device."""
+    rng = np.random.default_rng(12)
+    R, Hkv, H, d, n_pages, width, steps = 3, 2, 4, 64, 24, 6, 70
+    first = dt.KV4Cache(n_pages, Hkv, d, R, width, 64 * R, H=H)
+    layers = [first, dt.KV4Cache(n_pages, Hkv, d, R, width, 64 * R, H=H, like=first)]
+    own = [dt.KV4Cache(n_pages, Hkv, d, R, width, 64 * R, H=H) for _ in range(2)]
+    assert layers[1].workspace is first.workspace and layers[1].kv_len is first.kv_len
+    perm = rng.permutation(n_pages)
+    free = ints(perm)
+    turn = torch.arange(n_pages, device="cuda")
+    ctx, new = torch.zeros(R, dtype=torch.int32, device="cuda"), ints([60, 1, 64])
+    KV = [[HC.up(normal(rng, 125, Hkv, d)) for _ in range(2)] for _ in range(2)]
+
+    def place(cs):
+        cs[0].tables(ctx, new, free)
+        if cs is own:
+            cs[1].tables(ctx, new, free)
+
+    def go_on(c):
+        free.copy_(free[(turn + c.pages_used) % n_pages])
+        ctx.copy_(c.kv_len)
+
+    for cs in (layers, own):
+        place(cs)
+        for c, (K, V) in zip(cs, KV):
+            c.write(K, V)
+    assert layers[1].n_requests == R
+    go_on(first)
+    new.fill_(1)
+    Q = HC.up(normal(rng, R, H, d))
+    K1, V1 = HC.up(normal(rng, R, Hkv, d)), HC.up(normal(rng, R, Hkv, d))
+    outs = [[torch.zeros((R, H, d), device="cuda") for _ in range(2)] for _ in range(2)]
+
+    def step():
+        for cs, out in zip((layers, own), outs):
+            place(cs)
+            for c, o in zip(cs, out):
+                c.write(K1, V1)
+                c.summarize(ctx)
+                sel, count = c.select(Q, 2, band=0, sink=1)
+                c.attend(Q, o, max_q=1, sel=sel, sel_count=count)
+        go_on(first)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lens = np.array([60, 1, 64])
+    used = 3
+    for i in range(steps):
+        K1.copy_(HC.up(normal(rng, R, Hkv, d)))
+        graph.replay()
+        used += int((lens % PAGE == 0).sum())
+        lens += 1
+        torch.cuda.synchronize()
+        assert first.kv_len.tolist() == lens.tolist() and first.status.item() == 0
+        assert free.tolist() == np.roll(perm, -used).tolist()
+        for a, b in zip(*outs):
+            assert torch.equal(a, b) and (a != 0).any()
+    for a, b in zip(layers, own):
+        assert torch.equal(a.block_table, b.block_table) and torch.equal(a.data, b.data)
+        assert torch.equal(a.sum_codes, b.sum_codes)

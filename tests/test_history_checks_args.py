@@ -50,7 +50,7 @@ BAD_LISTS = [([[1, 2]], TypeError), (torch.tensor(3), TypeError), (torch.zeros((
 
 @pytest.mark.parametrize("sel,error", BAD_LISTS)
 def test_lists_that_are_no_lists_are_refused(sel, error):
-    c = on_the_host(dt.KV4Cache, H=4, Hkv=2, d=64, n_requests=2)
+    c = on_the_host(dt.KV4Cache, H=4, Hkv=2, d=64, _batch={"requests": 2})
     Q, count = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 2), dtype=torch.int32)
     with pytest.raises(error, match="sel"):
         c.attend(Q, torch.zeros_like(Q), sel=sel, sel_count=count)
@@ -76,3 +76,16 @@ def test_block_attention_refuses_strides_of_lse_that_lie_on_one_another():
                        (torch.zeros((2, 4, 99)), ValueError)):
         with pytest.raises(error, match="out_lse"):
             b.attend(Q, K, K, torch.zeros_like(Q), lse)
+
+
+def test_a_cache_borrows_from_one_of_its_sizes_only():
+    like = on_the_host(dt.KV4Cache, n_pages=9, H=4, Hkv=2, d=64, max_requests=3, max_blocks=5, max_tokens=7,
+                       block_table=None, _batch={"requests": 2})
+    ok = dict(n_pages=9, Hkv=2, d=64, max_requests=3, max_blocks=5, max_tokens=7, H=4, like=like)
+    for kw, error in ((dict(n_pages=8), ValueError), (dict(H=2), ValueError), (dict(d=96), ValueError),
+                      (dict(max_tokens=8), ValueError), (dict(max_blocks=4), ValueError), (dict(like=3), TypeError),
+                      (dict(block_table=torch.zeros((3, 5), dtype=torch.int32)), ValueError)):
+        with pytest.raises(error):
+            dt.KV4Cache(**{**ok, **kw})
+    like.n_requests = 1
+    assert like.n_requests == 1
