@@ -495,7 +495,9 @@ size_t ditango_kv4_attn_workspace_size(int32_t d);
  *   q_off, kv_len, block_table   as ditango_block_tables leaves them.
  *   sel, sel_count  dev int32 [R][Hkv][max_sel] and [R][Hkv], or NULL: only the
  *                listed blocks (indices into the request's table row, distinct)
- *                are attended, for all new tokens of the request alike.
+ *                are attended, for all new tokens of the request alike.  Indices
+ *                out of range count as empty, counts as 0 or max_sel, and are
+ *                recorded as DITANGO_ERR_BOUNDS.
  *   scale        logit scale; 0 means 1/sqrt(d).
  *   out          dev [T][H][d] bf16 or float32 (out_is_fp32), (token, head)
  *                element strides out_strides, multiples of 4 (NULL: packed);

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
     const Request rq = sg.rq;
     const int h = sg.h, row0 = sg.tile * TR;
     const int rows = min(TR, rq.n_q * p.G - row0);
-    const Pages pages(p, sg);
+    const Pages pages(p, sg, tid == 0);
     const int end = min(sg.u1, pages.n);
 
     auto issue = [&](uint32_t n, int page) {

@@ -254,7 +254,9 @@ struct Pages {
   const int *table, *sel;
   int n, kv, max_blocks, n_pages;
   int *dev_status;
-  __device__ __forceinline__ Pages(const Params &p, const Segment &s) {
+  // record: whether this thread records a count out of range (which counts as the
+  // nearest that is in range)
+  __device__ __forceinline__ Pages(const Params &p, const Segment &s, bool record) {
     table = p.block_table + (size_t)s.r * p.max_blocks;
     kv = s.rq.kv;
     max_blocks = p.max_blocks;
@@ -265,7 +267,9 @@ struct Pages {
     if (p.sel) {
       const size_t at = (size_t)s.r * p.Hkv + s.h;
       sel = p.sel + at * p.max_sel;
-      n = max(0, min(p.max_sel, __ldg(p.sel_count + at)));
+      const int count = __ldg(p.sel_count + at);
+      n = max(0, min(p.max_sel, count));
+      if (record && count != n) set_status(dev_status, DITANGO_ERR_BOUNDS);
     }
   }
   __device__ __forceinline__ int page(int e, int &block, bool record) const {

@@ -305,6 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       while (look.next(p, part)) far = far_apart<D>(p, part, s_near) || far;
       if (threadIdx.x == 0) p.words[blockIdx.x] = far;
     }
+    if (p.sel && blockIdx.x == 0)                 // counts out of range
+      for (int i = threadIdx.x; i < p.R * p.Hkv; i += kThreads) {
+        const int count = __ldg(p.sel_count + i);
+        if (count < 0 || count > p.max_sel) set_status(p.dev_status, DITANGO_ERR_BOUNDS);
+      }
     if (lane == 0) s_walk[warp].start(p, g);
     if (threadIdx.x == 0) s_range = g;
   }
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       auto bound = [](uint32_t m) { return bound_of(m); };
       auto reference = [](uint32_t top) { return min(max((top >> 23) + 1u, 64u), 253u) << 23; };
       while (ok && next_segment()) {
-        const hattn::Pages pages(p, sg);
+        const hattn::Pages pages(p, sg, false);
         const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
         uint32_t vref_bits = 64u << 23;        // 2^-63: a power of two that no V of the segment exceeds
         bool wide = false;
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
       const int at[4] = {place(0), place(1), place(2), place(3)};
       const int from = (is_v ? kPage * D / 2 : 0) + row0 * (D / 2) + part * 16;
       while (ok && next_segment()) {
-        const hattn::Pages pages(p, sg);
+        const hattn::Pages pages(p, sg, false);
         const int T = sg.u1 - sg.u0, first = 2 * sg.u0, head = sg.h;
         // page numbers are read two tiles ahead, codes one
         int page[2];

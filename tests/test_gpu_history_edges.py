@@ -582,3 +582,27 @@ def test_layers_share_one_batch_and_the_free_list_goes_on_in_a_graph():
     for a, b in zip(layers, own):
         assert torch.equal(a.block_table, b.block_table) and torch.equal(a.data, b.data)
         assert torch.equal(a.sum_codes, b.sum_codes)
+
+
+# ---------------------------------------------------------------- bad lists
+@pytest.mark.parametrize("many", [False, True])
+def test_counts_of_a_list_out_of_range_are_clipped_and_recorded(many):
+    rng = np.random.default_rng(5)
+    d, H, q = 64, 2, 30
+    b = Batch(rng, [HC.keys_values(rng, 300, 1, d)] * 2, H, [q, q], many, d)
+    Q = normal(rng, 2 * q, H, d)
+    b.attend(Q, False, lists=[[[0, 1, 2]], [[3]]], room=3)
+    assert b.c.status.item() == 0
+    for counts, lists in (((99, 1), [[[2, 0, 4]], [[3]]]), ((3, -2), [[[2, 0, 4]], [[]]])):
+        b.c.status.zero_()
+        R = len(b.table)
+        sel = ints(np.array([[[2, 0, 4]], [[3, 1, 0]]] + [[[0, 1, 2]]] * (R - 2)))
+        count = ints(np.array([[counts[0]], [counts[1]]] + [[3]] * (R - 2)))
+        Qd = torch.zeros((b.rows, H, d), dtype=torch.bfloat16, device="cuda")
+        Qd[:b.T] = HC.up(Q)
+        out, lse = torch.zeros(Qd.shape, device="cuda"), torch.zeros(Qd.shape[:2], device="cuda")
+        b.c.attend(Qd, out, lse, max_q=b.max_q, sel=sel, sel_count=count)
+        torch.cuda.synchronize()
+        assert b.c.status.item() == 5
+        b.check(Q, out[:b.T].cpu().numpy().astype(np.float64), lse[:b.T].cpu().numpy().astype(np.float64), False,
+                lists=lists)
