@@ -509,9 +509,9 @@ size_t ditango_kv4_attn_workspace_size(int32_t d);
  * as they were.  Keys that a row does not see never touch it, whatever they
  * hold.  For the second product a probability is rounded to fp16, to 2^-30 of the
  * row's largest at worst; lse and the sums are fp32.  Where more than 16 rows of a
- * key head go together, a value is rounded to fp16 too, to 2^-25 of the largest that
- * all of them see at worst (probabilities and values to bf16 where the new tokens'
- * values are 2^10 or more apart).  The result does not depend on the order in which
+ * key head go together, a value is rounded to fp16 too, to 2^-15 of the largest that
+ * the row sees at worst (probabilities and values to bf16 where values that not all
+ * rows see are 2^10 or more apart).  The result does not depend on the order in which
  * blocks run. */
 ditango_status ditango_kv4_attn(const ditango_kv4 *c, int32_t R, int32_t H, int32_t T,
                                 int32_t max_q, int32_t max_blocks, const uint16_t *Q,

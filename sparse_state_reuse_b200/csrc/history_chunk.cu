@@ -95,7 +95,7 @@ __device__ __forceinline__ bool outgrown(float mx, float m) {
 // 2^-25 of the largest value.)  A call that is causal is launched twice: kAsIs looks,
 // before it begins, whether any of these keys are 2^7, or their values 2^10, from
 // one another, and kFarApart, which does nothing else, does the work once more where
-// they are.  A test for it in the loops below costs them 3 to 25% (the registers are
+// they are; with lists it does the work alone.  A test for it in the loops below costs them 3 to 25% (the registers are
 // full), the look 1% and the empty launch 3 us.
 enum Sizes { kAsIs, kFarApart };
 
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
   using C = Cfg<D>;
   constexpr bool FAR = SIZES == kFarApart;
   if constexpr (FAR) {
-    // the words of every block of the launch before
-    if (!__syncthreads_or(threadIdx.x < gridDim.x && p.words[threadIdx.x] != 0)) return;
+    // the words of every block of the launch before, if there was one
+    if (p.words && !__syncthreads_or(threadIdx.x < gridDim.x && p.words[threadIdx.x] != 0)) return;
   }
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_chunk_kernel(const __grid_con
               if (vb > 0.f) low = min(low, __float_as_uint(vb));
             }
             low = __reduce_min_sync(0xffffffffu, low);
-            wide = (vnew >> 23) > (low >> 23) + 1u + kEvenV ||
+            wide = (max(vnew, vref_bits) >> 23) > (low >> 23) + 1u + kEvenV ||
                    (vref_bits > 64u << 23 && vnew > vref_bits + (kEvenV << 23));
           }
           vref_bits = FAR && wide ? kWideRef : max(vref_bits, vnew);
@@ -1073,6 +1073,11 @@ cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch(const Params &p, int num_sms, cudaStream_t stream) {
+  if (p.causal && p.sel) {          // what a row sees of a list may be of any size beside the new tokens
+    Params always = p;
+    always.words = nullptr;
+    return launch<D, kFarApart>(always, num_sms, stream);
+  }
   const cudaError_t e = launch<D, kAsIs>(p, num_sms, stream);
   return e != cudaSuccess || !p.causal ? e : launch<D, kFarApart>(p, num_sms, stream);
 }

@@ -352,7 +352,7 @@ def test_outlying_and_unseen_values_many_rows(d, q, kvs):
     check_outliers(b, Q, o, lse, True)
     # the blocks listed in any order: those that no row sees among the first
     lists = [[rng.permutation(-(-n // PAGE)).tolist()] for n in kvs]
-    got = b.attend(Q, True, lists=lists, room=max(len(x[0]) for x in lists) + 2)
+    got = b.attend(Q, True, lists=lists, room=300)         # (work for the kernel of many rows)
     check_outliers(b, Q, *got, True)
 
 
@@ -591,18 +591,51 @@ def test_counts_of_a_list_out_of_range_are_clipped_and_recorded(many):
     d, H, q = 64, 2, 30
     b = Batch(rng, [HC.keys_values(rng, 300, 1, d)] * 2, H, [q, q], many, d)
     Q = normal(rng, 2 * q, H, d)
-    b.attend(Q, False, lists=[[[0, 1, 2]], [[3]]], room=3)
+    room = 300 if many else 3                           # work for the kernel of many rows
+    b.attend(Q, False, lists=[[[0, 1, 2]], [[3]]], room=room)
     assert b.c.status.item() == 0
-    for counts, lists in (((99, 1), [[[2, 0, 4]], [[3]]]), ((3, -2), [[[2, 0, 4]], [[]]])):
+    for counts, lists in (((9999, 1), [[[2, 0, 4]], [[3]]]), ((3, -2), [[[2, 0, 4]], [[]]])):
         b.c.status.zero_()
         R = len(b.table)
-        sel = ints(np.array([[[2, 0, 4]], [[3, 1, 0]]] + [[[0, 1, 2]]] * (R - 2)))
-        count = ints(np.array([[counts[0]], [counts[1]]] + [[3]] * (R - 2)))
+        if counts[0] > room:                            # as many as there are: the others have no tokens
+            lists = [[[2, 0, 4] + list(range(5, room + 2))], lists[1]]
+        sel = np.broadcast_to(np.arange(room), (R, 1, room)).copy()
+        sel[0, 0, :] = [2, 0, 4] + list(range(5, room + 2))
+        sel[1, 0, :3] = [3, 1, 0]
+        sel, count = ints(sel), ints(np.array([[counts[0]], [counts[1]]] + [[room]] * (R - 2)))
         Qd = torch.zeros((b.rows, H, d), dtype=torch.bfloat16, device="cuda")
         Qd[:b.T] = HC.up(Q)
         out, lse = torch.zeros(Qd.shape, device="cuda"), torch.zeros(Qd.shape[:2], device="cuda")
         b.c.attend(Qd, out, lse, max_q=b.max_q, sel=sel, sel_count=count)
         torch.cuda.synchronize()
         assert b.c.status.item() == 5
+        lists = [[[j for j in x if j * PAGE < 300] for x in of] for of in lists]
         b.check(Q, out[:b.T].cpu().numpy().astype(np.float64), lse[:b.T].cpu().numpy().astype(np.float64), False,
                 lists=lists)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -30, 2.0 ** -60])
+def test_a_list_that_hides_the_new_tokens_from_some_rows(d, size):
+    """Old values `size` times the new ones; the listed page of new tokens is seen by
+    the later rows only, and comes first or in between."""
+    rng = np.random.default_rng(d)
+    H, q, n = 2, 100, 700
+    K, V = HC.keys_values(rng, n, 1, d)
+    V[:500] = HC.bf16_round(V[:500] * size)
+    b = Batch(rng, [(K, V)] * 2, H, [q] * 2, True, d)
+    Q = normal(rng, 2 * q, H, d)
+    lists = [[[10, 0, 1, 2]], [[3, 1, 10, 0]]]
+    o, lse = b.attend(Q, True, lists=lists, room=300)      # work for the kernel of many rows
+    assert b.c.status.item() == 0
+    at = 0
+    for r in range(2):
+        k, v, y, x, pos = b.rows_of(r, 0, lists)
+        for t in range(q):
+            seen = pos < n - (q - 1 - t)
+            qr = Q[at + t].astype(np.float64)
+            oo, e, P = OH.attend_rows(qr, k[seen], v[seen], d ** -0.5)
+            dS = HC.logit_bound(qr, y[seen], d ** -0.5, d)
+            HC.check(o[at + t], lse[at + t], oo, e, P, (np.abs(v) * (1 + 2.0 ** -4 + 2.0 ** -7))[seen], v[seen], dS,
+                     False, (r, t))
+        at += q
