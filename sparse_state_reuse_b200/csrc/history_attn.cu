@@ -48,8 +48,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxBlocks = 768;      // most blocks of a launch (the workspace has room for them)
 constexpr int kSetup = 8;            // pages that beginning and finishing an item counts for
 // p s' in fp16: p is at most 2^8 (the lazy rescaling), s' at most the reference;
-// 2^6 more uses the range that is left.
-constexpr float kWeightScale = 64.f;
+// 2^6 more uses the range that is left but for one power of two, in which the next
+// pages' scales may be larger.
+constexpr float kWeightScale = 64.f, kMostScale = 128.f;
 constexpr float kFirstScale = 0x1p69f;   // before the first weight: 2^6 over 2^-63
 
 // Key of row n of an 8-key tile.  The order within a tile is free (scores and
@@ -76,6 +77,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // The least power of two above x >= 0, from 2^-63 to 2^127.
 __device__ __forceinline__ float power_above(float x) {
   return __uint_as_float(min(max((__float_as_uint(x) >> 23) + 1u, 64u), 254u) << 23);
+}
+// Of powers of two a and b: a / b, as long as that is one of 2^-126 ... 2^127 (0 below),
+// without a division's code.
+__device__ __forceinline__ float power_ratio(float a, float b) {
+  const int bits = (int)(__float_as_uint(a) - __float_as_uint(b)) + (127 << 23);
+  return __uint_as_float((uint32_t)max(bits, 0));
 }
 
 template <int D>
@@ -208,7 +215,7 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float fit = top_s * w.vs[2 * x + e];
-      misfit = misfit || fit > kWeightScale || (fit < 1.f && top != 0u);
+      misfit = misfit || fit > kMostScale || (fit < 1.f && top != 0u);
     }
   if (__any_sync(0xffffffffu, need || misfit)) {
     float vmul[2 * NR];
@@ -217,7 +224,7 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
     if (__any_sync(0xffffffffu, misfit)) {
       // scales within 2^6 of one another, and of those before, that every row sees:
       // the largest holds for all rows
-      const float vnew = kWeightScale / power_above(top_s);
+      const float vnew = power_ratio(kWeightScale, power_above(top_s));
       const uint32_t low = __reduce_min_sync(0xffffffffu, min(sa16 ? sa16 : 0xffffu, sb16 ? sb16 : 0xffffu));
       bool alike = top <= low + (6u << 7) && (!MASKED || vis_all >= kv);
 #pragma unroll
@@ -235,7 +242,7 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
           for (int e = 0; e < E; ++e) {
             const int y = 2 * x + e;
             if (top_s * w.vs[y] > kWeightScale) {
-              vmul[y] = vnew / w.vs[y];
+              vmul[y] = power_ratio(vnew, w.vs[y]);
               w.vs[y] = vnew;
             }
           }
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, NR == 2 ? 2 : (D == 128 ? 3 : 4)) kv
         w.z[y] += __shfl_xor_sync(0xffffffffu, w.z[y], o);
       }
       float *row = mg + (E == 2 ? 8 * x + 2 * t + e : 4 * x + t) * S::kMergeStride;
-      const float z = w.z[y], vout = 1.f / w.vs[y];
+      const float z = w.z[y], vout = power_ratio(1.f, w.vs[y]);
       auto val = [&](int j, int up) { return fmaf(w.o[x][j][2 * up + e], vout, z); };
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
