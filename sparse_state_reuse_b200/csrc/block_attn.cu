@@ -19,8 +19,8 @@
 // columns of S and feeds the second product from there.
 // Bound: 4 * 128 * 128 * d flops a tile against the exponentials of 128 * 128
 // scores, and 2 * 128 * d * 2 bytes of L2 reads a tile.  600 query blocks of 40
-// heads of 128 over 150 key blocks each: 12.8 ms at the boost clock, 13.4 to 14.3
-// under the power limit, 1180 and 1060 to 1120 TFLOP/s (65 to 73% of the measured
+// heads of 128 over 150 key blocks each: 12.7 ms at the boost clock, 13.4 to 14.9
+// under the power limit, 1190 and 1020 to 1130 TFLOP/s (62 to 73% of the measured
 // bf16 rate; the dense kernel of this library reaches 67%).  Register splits of
 // 192/64 and 208/48 were slower or the same.
 

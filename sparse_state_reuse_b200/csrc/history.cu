@@ -11,9 +11,9 @@ namespace hist {
 // running sum of need - have, the tokens' offsets from that of new.  Every
 // block sums all requests again (a few KB of L2 reads) and then writes its own
 // share of the table and the slot map, so that one launch does everything; it
-// is latency-bound: 6.0 us for the 64 single tokens of a step, 7.1 us for 512
-// requests with up to 400 new tokens each (cold, one launch alone), most of it
-// launch and two dependent reads; the bytes are below 1 MB.
+// is latency-bound: 6.2 us for the 64 single tokens of a step and 6.4 us for 512
+// requests with up to 400 new tokens each, replayed in a graph, most of it launch
+// and two dependent reads; the bytes are below 1 MB.
 constexpr int kTabThreads = 256;
 
 struct TablesParams {
@@ -220,7 +220,7 @@ __device__ __forceinline__ uint32_t scale_bits(float lo, float hi) {
 // values each (16-byte loads), so that all lanes are busy for every d and the
 // address arithmetic is spread over 16 to 32 values; least and largest value
 // are found with packed bf16 minima of (x, -x) and two shuffles.
-// 28800 tokens of 24 heads of 96: 87.5 us for 336 MB, 3.8 TB/s.  Bound by issue
+// 28800 tokens of 24 heads of 96: 89 us for 336 MB, 3.8 TB/s.  Bound by issue
 // (65% of the slots, the exact quotients most of it) and by the loads' latency
 // with 28 warps an SM; the next row fetched ahead (90 us), five and six blocks an
 // SM (spills) and one branch for the inexact groups of a row (93 us) were slower.
@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const RowsParams p) {
 
 // ---------------------------------------------------------------- page summaries
 // 8-bit codes of the mean key of every page that holds tokens [ctx, kv) of a
-// request.  The sum over the page's tokens (all of them, not only the new
+// request.  28800 tokens of 24 heads of 96: 84 us (36 MB, 6 us at the copy rate), the
+// last pages of 64 requests, 8 heads of 128: 12 us; bound by its byte loads and fp64,
+// one page after the other.  The sum over the page's tokens (all of them, not only the new
 // ones) is formed from the codes in fp64, where it is exact, so that a page
 // has one summary whatever order and number of calls filled it.
 struct SummaryParams {

@@ -6,10 +6,10 @@
 // nothing to do for them:
 //   K  s (c - 8) over a power of two of the tile: a significand of 8 bits times
 //      a number of -8 ... 7 has 11 bits, so it is exact in fp16 (but for what lies
-//      2^-25 below the tile's largest key).  What is left,
-//      h sum(q), is one more step of the product: h and sum(q) are split into
-//      three fp16 parts each, and six of the 16 columns of that step hold the
-//      pairs that matter (the rest is below 2^-32 of it).
+//      2^-25 below the tile's largest key).  What is left, h sum(q), is one more
+//      step of the product: h and sum(q) are split into three fp16 parts each, and
+//      six of the 16 columns of that step hold the pairs that matter (the rest is
+//      below 2^-32 of it).
 //   V  s' (c' - 8) + h' in fp16 (2^-12, eight times finer than the bf16 it was
 //      made from) over a power of two that no value of the item so far exceeds.
 //      Where a causal item's last tiles hold values that some rows do not see and
@@ -41,9 +41,11 @@
 // overwrites the first 64 columns of its S.  Each block takes an equal share of
 // the line of work.
 //
-// 3600 queries over 25200 tokens, 24 heads of 96: 1.20 ms, 697 TFLOP/s (43% of the
-// measured bf16 rate); the tensor pipe is busy 37% of the time, the exponentials'
-// unit 46%, the issue slots 47%.  The step of a row tile is a chain, Q K^T (1/5 of
+// 3600 queries over 25200 tokens, 24 heads of 96: 1.21 ms, 690 TFLOP/s (42% of the
+// measured bf16 rate); the tensor pipe is busy 36% of the time, the exponentials'
+// unit 45%, the issue slots 46%.  4000 causal queries over their own tokens, 40 query
+// and 8 key heads of 128: 0.70 ms (tiles that no row of an item sees are computed like
+// the others, half of all here).  The step of a row tile is a chain, Q K^T (1/5 of
 // it), softmax (3/5) and P V (1/5), of which the two row tiles hide only each
 // other's products.  Scores in halves of 64 keys, so that one half's product runs
 // under the other's softmax, took away most of the wait for S but make Q K^T twice
@@ -64,8 +66,8 @@ constexpr int TR = 2 * BM;           // rows of an item
 constexpr int BN = 2 * kPage;        // keys of a tile
 constexpr int kThreads = 512;
 constexpr int kLaunchRegs = 128;     // 65536 / 512
-// 1.19 ms for 3600 queries of 24 heads of 96 channels after 25200 tokens (of the splits that
-// were tried: 176/80 1.30 ms, where the producers spill, 160/96 1.37)
+// of the splits that were tried at 3600 queries of 24 heads of 96 channels after 25200
+// tokens, 1.19 ms with this one then: 176/80 1.30 ms, where the producers spill, 160/96 1.37
 constexpr int kSoftmaxRegs = 168, kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 2 * 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
 constexpr int kProducers = 96;       // threads that unpack K, and as many for V
@@ -95,16 +97,18 @@ __device__ __forceinline__ bool outgrown(float mx, float m) {
 // 2^-25 of the largest value.)  A call that is causal is launched twice: kAsIs looks,
 // before it begins, whether any of these keys are 2^7, or their values 2^10, from
 // one another, and kFarApart, which does nothing else, does the work once more where
-// they are; with lists it does the work alone.  A test for it in the loops below costs them 3 to 25% (the registers are
-// full), the look 1% and the empty launch 3 us.
+// they are; with lists, where a row may see none of its neighbours, it does the work
+// alone.  Tests for it in the loops of one kernel cost them 3% (K) to 25% (K and V):
+// their registers are full.  The look costs 1%, the empty launch 3 us.
 enum Sizes { kAsIs, kFarApart };
 
 // What is known of a tile before its codes are unpacked.
 //
-// kFarApart: where the sizes of such a tile's keys differ by
+// kFarApart: where the sizes of the keys of a tile that not all rows see differ by
 // more than 2^4, K is held key by key: each over a power of two of its own, which
-// the softmax puts back into the scores.  Where the values differ by more than 2^10, from one another or from those before,
-// this tile and those after it hold V in bf16, and the softmax P.
+// the softmax puts back into the scores.  Where the values differ by more than 2^10,
+// from one another or from those before, this tile and those after it hold V in
+// bf16, and the softmax P.
 constexpr int kRing = 4;
 constexpr uint32_t kEven = 4, kEvenV = 10;
 constexpr uint32_t kOwnK = 1, kWideV = 2;
