@@ -95,7 +95,7 @@ __device__ __forceinline__ bool outgrown(float mx, float m) {
 // be of any size beside the others.  (Keys that a row sees need no such care: what
 // the largest takes from the others is below the rounding of its own score, and
 // 2^-25 of the largest value.)  A call that is causal is launched twice: kAsIs looks,
-// before it begins, whether any of these keys are 2^7, or their values 2^10, from
+// before it begins, whether any of these keys are 2^6, or their values 2^10, from
 // one another, and kFarApart, which does nothing else, does the work once more where
 // they are; with lists, where a row may see none of its neighbours, it does the work
 // alone.  Tests for it in the loops of one kernel cost them 3% (K) to 25% (K and V):
@@ -203,7 +203,7 @@ constexpr uint32_t kBothBf16 = (1u << 7) | (1u << 10);
 // The sizes of a causal item's keys and values that not all of its rows see, and of
 // its first row's own, are near enough to one another for kAsIs.  All threads.
 // near[4]: largest and least K, V.
-constexpr uint32_t kNearK = 7, kNearV = 10;
+constexpr uint32_t kNearK = 6, kNearV = 10;
 __device__ __forceinline__ float bound_of(uint32_t meta) {     // of |x| of a row: |least| or |least + 15 s|, or not finite
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(bf_hi(meta))), "f"(fabsf(fmaf(15.f, bf_lo(meta), bf_hi(meta)))));

@@ -639,3 +639,23 @@ def test_a_list_that_hides_the_new_tokens_from_some_rows(d, size):
             HC.check(o[at + t], lse[at + t], oo, e, P, (np.abs(v) * (1 + 2.0 ** -4 + 2.0 ** -7))[seen], v[seen], dS,
                      False, (r, t))
         at += q
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("key,value", [(2.0 ** 4, 1.0), (2.0 ** 5.9, 1.0), (2.0 ** 6.5, 1.0), (1.0, 2.0 ** 9),
+                                       (1.0, 2.0 ** 9.9), (1.0, 2.0 ** 10.5), (2.0 ** -5, 2.0 ** -9)])
+def test_sizes_on_either_side_of_far_apart(d, key, value):
+    """The last tokens' keys and values `key` and `value` times the others': around
+    the sizes at which a causal call is done in the other way."""
+    rng = np.random.default_rng(d)
+    H, q, n = 2, 60, 400
+    K, V = HC.keys_values(rng, n, 1, d)
+    K, V = (np.clip(x, -3, 3) for x in (K, V))
+    K[:, :, 0] = V[:, :, 0] = 3.0                         # every row's bound is 3 or a little more
+    K[n - 20:] = HC.bf16_round(K[n - 20:] * key)
+    V[n - 20:] = HC.bf16_round(V[n - 20:] * value)
+    b = Batch(rng, [(HC.bf16_round(K), HC.bf16_round(V))], H, [q], True, d)
+    Q = HC.bf16_round(normal(rng, q, H, d) / max(key, 1.0))
+    o, lse = b.attend(Q, True)
+    assert b.c.status.item() == 0
+    check_outliers(b, Q, o, lse, True)
