@@ -10,12 +10,12 @@
 //      step of the product: h and sum(q) are split into three fp16 parts each, and
 //      six of the 16 columns of that step hold the pairs that matter (the rest is
 //      below 2^-32 of it).
-//   V  s' (c' - 8) + h' in fp16 (2^-12, eight times finer than the bf16 it was
+//   V  s' (c' - 8) + h' in fp16 (2^-11, eight times finer than the bf16 it was
 //      made from) over a power of two that no value of the item so far exceeds.
 //      Where a causal item's last tiles hold values that some rows do not see and
 //      that are far from the others, V and P are bf16 from there on, over a power of
-//      two that leaves room for every bf16 value: 2^-9 and 2^-9, but no row's values
-//      depend on another's keys.
+//      two that leaves room for every bf16 value: rounded to 2^-8 each, but no row's
+//      values depend on another's keys.
 // P is fp16.
 //
 // One block of threads an SM takes two row tiles (256 rows) against the same

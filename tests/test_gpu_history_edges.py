@@ -257,8 +257,9 @@ def outliers(rng, n, Hkv, d, key, unseen=True):
 
 
 def check_outliers(b, Q, o, lse, wide):
-    """As Batch.check, P s' rounded once; `wide`: P is rounded to fp16 and then with V
-    to bf16, 2^-12 + 2 2^-9 of P |v| and their products."""
+    """As Batch.check, P s' rounded once; `wide`: P is rounded to fp16 (2^-11) and then
+    with V to bf16 (2^-8 each), together at most (1 + 2^-11)(1 + 2^-8)^2 - 1 < 2^-8
+    (2 + 2^-2) of P |v|."""
     scale, G, at = b.d ** -0.5, b.H // b.Hkv, 0
     for r, n in enumerate(b.q_lens):
         for h in range(b.Hkv):
@@ -269,7 +270,7 @@ def check_outliers(b, Q, o, lse, wide):
                 qr = Q[at + t, g].astype(np.float64)
                 oo, e, P = OH.attend_rows(qr, k[seen], v[seen], scale)
                 dS = HC.logit_bound(qr, y[seen], scale, b.d)
-                HC.check(o[at + t, g], lse[at + t, g], oo, e, P, (np.abs(v) * (1 + 2.0 ** -4 + 2.0 ** -7) if wide else x)[seen],
+                HC.check(o[at + t, g], lse[at + t, g], oo, e, P, (np.abs(v) * (2 + 2.0 ** -2) if wide else x)[seen],
                          v[seen], dS, False, (r, h, t))
         at += n
 
@@ -618,7 +619,8 @@ def test_counts_of_a_list_out_of_range_are_clipped_and_recorded(many):
 @pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -30, 2.0 ** -60])
 def test_a_list_that_hides_the_new_tokens_from_some_rows(d, size):
     """Old values `size` times the new ones; the listed page of new tokens is seen by
-    the later rows only, and comes first or in between."""
+    the later rows only, and comes first or in between.  (P and V in bf16: as
+    check_outliers says.)"""
     rng = np.random.default_rng(d)
     H, q, n = 2, 100, 700
     K, V = HC.keys_values(rng, n, 1, d)
@@ -636,7 +638,7 @@ def test_a_list_that_hides_the_new_tokens_from_some_rows(d, size):
             qr = Q[at + t].astype(np.float64)
             oo, e, P = OH.attend_rows(qr, k[seen], v[seen], d ** -0.5)
             dS = HC.logit_bound(qr, y[seen], d ** -0.5, d)
-            HC.check(o[at + t], lse[at + t], oo, e, P, (np.abs(v) * (1 + 2.0 ** -4 + 2.0 ** -7))[seen], v[seen], dS,
+            HC.check(o[at + t], lse[at + t], oo, e, P, (np.abs(v) * (2 + 2.0 ** -2))[seen], v[seen], dS,
                      False, (r, t))
         at += q
 
