@@ -11,10 +11,10 @@
 // 2^-11.  Q is scaled by a power of two a row to lie below 2 (an exact step for
 // all but values 2^-24 of the row's largest), p s' by one of the row's own: 2^6
 // over the largest V scale met so far, as long as the scales that the warp meets
-// are of one size.  Where they are not (a page's largest is above what the row
-// is held to, or 2^6 below it), the row is held to the weights that it has
-// itself, so that neither a key that it does not see nor one whose probability is
-// nothing pushes the others out of fp16.
+// are of one size.  Where they are not (those of a page are 2^8 and more apart, or
+// its largest is above what the row is held to, or 2^6 below it), the row is held to
+// the weights that it has itself, so that neither a key that it does not see nor one
+// whose probability is nothing pushes the others out of fp16.
 //
 // Keys and channels are the rows of the products (m16n8k16, S^T = K Q^T and
 // O^T = V^T P^T) and query rows their 8 columns: 8 rows at a time, of which a
@@ -208,8 +208,10 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
   if (sa16 >= 0x7f80u) sa16 = 0u;
   if (sb16 >= 0x7f80u) sb16 = 0u;
   const uint32_t top = __reduce_max_sync(0xffffffffu, max(sa16, sb16));
+  const uint32_t low = __reduce_min_sync(0xffffffffu, min(sa16 ? sa16 : 0xffffu, sb16 ? sb16 : 0xffffu));
   const float top_s = __uint_as_float(top << 16);
-  bool misfit = false, refit = false;
+  const bool spread = top > low + (8u << 7);        // by more than 2^8 (0 is no scale)
+  bool misfit = spread, refit = false;
 #pragma unroll
   for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -222,11 +224,10 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
 #pragma unroll
     for (int y = 0; y < 2 * NR; ++y) vmul[y] = 1.f;
     if (__any_sync(0xffffffffu, misfit)) {
-      // scales within 2^6 of one another, and of those before, that every row sees:
-      // the largest holds for all rows
+      // scales of one size that every row sees, and within 2^6 of those before: the
+      // largest holds for all rows
       const float vnew = power_ratio(kWeightScale, power_above(top_s));
-      const uint32_t low = __reduce_min_sync(0xffffffffu, min(sa16 ? sa16 : 0xffffu, sb16 ? sb16 : 0xffffu));
-      bool alike = top <= low + (6u << 7) && (!MASKED || vis_all >= kv);
+      bool alike = !spread && (!MASKED || vis_all >= kv);
 #pragma unroll
       for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -316,22 +317,24 @@ __device__ __forceinline__ void page_values(WarpTile<D, NR> &w, const Unpack &un
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         }
+        const float old = w.vs[y];
+        float vs = old, ao = 1.f;
         if (most > 0.f) {
           // that weight becomes 1/2 to 2^13, where the page's largest scale asks for
-          // neither more nor less; what there is of O stays finite
-          const float unit = 0x1p-8f / power_above(most), old = w.vs[y];
-          float vs = top_s > 0.f ? kWeightScale / power_above(top_s) : unit, ao = 1.f;
-          vs = fminf(fminf(fmaxf(vs, unit), unit * 0x1p13f), kFirstScale);
-          if (big > 0.f) {
-            vs = fminf(vs, old * fminf(0x1p100f / power_above(big), 0x1p90f));
-            ao = vs / old;
-          }
-          w.vs[y] = vs;
+          // neither more nor less
+          const float unit = 0x1p-8f / power_above(most), want = top_s > 0.f ? kWeightScale / power_above(top_s) : unit;
+          vs = fminf(fminf(fmaxf(want, unit), unit * 0x1p13f), kFirstScale);
+        }
+        vs = fminf(vs, 0x1p126f / power_above(top_s));       // s' vs is finite where p is 0
+        if (big > 0.f) {                                     // and what there is of O
+          vs = fminf(vs, old * fminf(0x1p100f / power_above(big), 0x1p90f));
+          ao = vs / old;
+        }
+        w.vs[y] = vs;
 #pragma unroll
-          for (int j = 0; j < T::MT; ++j) {
-            w.o[x][j][e] *= ao;
-            w.o[x][j][2 + e] *= ao;
-          }
+        for (int j = 0; j < T::MT; ++j) {
+          w.o[x][j][e] *= ao;
+          w.o[x][j][2 + e] *= ao;
         }
       }
   }

@@ -661,3 +661,39 @@ def test_sizes_on_either_side_of_far_apart(d, key, value):
     o, lse = b.attend(Q, True)
     assert b.c.status.item() == 0
     check_outliers(b, Q, o, lse, True)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("G", [1, 3, 8, 16])
+@pytest.mark.parametrize("big,small", [(2.0 ** 85, 1.0), (2.0 ** 40, 2.0 ** -58), (2.0 ** 100, 2.0 ** -20), (2.0 ** 9, 1.0)])
+def test_a_later_key_that_takes_all_has_a_small_value(d, G, big, small):
+    """Values of `big` with ordinary logits in the first page and in a later one, where
+    a key 150 above them has a value of `small`: the outputs are that value (in both
+    orders of the pages).  Many requests alike, so that one warp takes both pages."""
+    rng = np.random.default_rng(d + G)
+    n, R = 9 * PAGE, 1500
+    K, V = HC.bf16_round(0.1 * rng.standard_normal((n, 1, d))), normal(rng, n, 1, d)
+    V[::7] = HC.bf16_round(V[::7] * big)
+    V[5 * PAGE] = HC.bf16_round(normal(rng, 1, d) * small)
+    K[5 * PAGE] = 0
+    K[5 * PAGE, 0, 0] = 16.0
+    K[:, 0, 1] = 0
+    b = Batch(rng, [(K, V)], G, [1], False, d)
+    table = b.c.block_table.repeat(R, 1)
+    table[R // 2:] = table[R // 2:].flip(1)
+    c = dt.KV4Cache(b.c.n_pages, 1, d, R, 9, R, H=G, data=b.c.data, block_table=table)
+    c.kv_len.fill_(n)
+    c.q_off.copy_(torch.arange(R + 1, dtype=torch.int32))
+    Q = np.zeros((1, G, d), np.float32)
+    Q[..., 0] = HC.bf16_round(150 / 16.0 * d ** 0.5)
+    Q[..., 1:] = HC.bf16_round(0.1 * rng.standard_normal((1, G, d - 1)))
+    out, lse = torch.zeros((R, G, d), device="cuda"), torch.zeros((R, G), device="cuda")
+    c.attend(HC.up(Q).repeat(R, 1, 1), out, lse, max_q=1)
+    torch.cuda.synchronize()
+    k, v, y, x, pos = b.rows_of(0, 0)
+    o, e, P = OH.attend_rows(Q[0].astype(np.float64), k, v, d ** -0.5)
+    dS = HC.logit_bound(Q[0].astype(np.float64), y, d ** -0.5, d)
+    got, got_l = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all() and c.status.item() == 0
+    for r in range(0, R, 37):
+        HC.check(got[r], got_l[r], o, e, P, x, v, dS, False, r)
