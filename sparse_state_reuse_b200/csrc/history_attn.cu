@@ -33,7 +33,7 @@
 //
 // One token over 86400 of 24 heads of 96: 58 us, 3.7 TB/s (57% of the copy rate);
 // the copies alone, without arithmetic, 44 us.  48 requests of 1 to 16000 tokens, 8
-// key heads of 128: 107 us (the copies alone 76 us).  The first page lands 7.7 us
+// key heads of 128: 108 us (the copies alone 76 us).  The first page lands 7.7 us
 // after the start (lengths, page numbers and the copy follow one another), and the
 // join of the parts takes the last 4 us.  Reading Q before the pages, which shortens
 // its own wait, delays the copies as much (59 us).
